@@ -63,7 +63,9 @@ typedef enum spmv_status {
     SPMV_ERR_TOO_LARGE = 5,    /* format exceeds int32 slots or opts.max_bytes  */
     SPMV_ERR_OOM = 6,          /* device allocation failed                      */
     SPMV_ERR_HIP = 7,          /* HIP runtime or kernel launch error            */
-    SPMV_ERR_DEVICE = 8        /* handle used on another device than its own    */
+    SPMV_ERR_DEVICE = 8,       /* handle used on another device than its own    */
+    SPMV_ERR_BAD_VALUE = 9     /* a weight or scale that is not finite, a zero
+                                  point above 15, a scale out of its type's range */
 } spmv_status;
 
 /* Blocked COO layout constant (SPMV_COO_BLOCKED): rows per row block, whose
@@ -461,6 +463,147 @@ spmv_status spmv_export(const spmv_handle *h, spmv_array which, void *host_dst, 
 /* Free the handle and its device memory (synchronises its device first).
  * NULL is accepted. */
 spmv_status spmv_destroy(spmv_handle *h);
+
+/* ---------------------------------------------------------------------------
+ * Weight tables: 4-bit matrices with group scales, row lookups by token, and
+ * the gradient of a lookup.
+ *
+ * A model's token table is read at both ends: its rows by token (lookup: the
+ * product of a selection matrix, one entry per row, with the table), and all
+ * of it at once (logits: a matrix-vector product).  Its gradient is the
+ * product of the transposed selection matrix with the rows' gradients.
+ *
+ * Types.  Matrices, vectors and rows are fp32, fp16 or bf16 (spmv_dtype);
+ * token ids int32 or int64.  Row strides (`ld`) count elements and are at
+ * least the row's length; the elements of a row are consecutive.  Offsets are
+ * 64-bit.  Pointers need the alignment of their element only.
+ * Sums are kept in fp32 and rounded once to the output's type.
+ * Every result is bit-reproducible: no sum depends on the order in which
+ * workgroups run.
+ * spmv_quant_run, spmv_quant_lookup, spmv_lookup and spmv_lookup_grad are
+ * asynchronous on `stream`, allocate nothing, never synchronise, and can be
+ * captured in a HIP graph.  Inputs and outputs must not overlap.
+ * ------------------------------------------------------------------------- */
+typedef enum spmv_dtype {
+    SPMV_FP32 = 0,
+    SPMV_FP16 = 1,
+    SPMV_BF16 = 2,
+    SPMV_INT32 = 3,
+    SPMV_INT64 = 4
+} spmv_dtype;
+
+/* A dense matrix W [R, C] in 4 bits per weight:
+ *   W[r, c] = scale[r, g] * (code[r, c] - zero[r, g]),  g = c / group,
+ * codes and zero points in 0..15, one scale (fp32, fp16 or bf16) per row and
+ * group of `group` consecutive columns; the last group of a row may be short.
+ * Without zero points zero[r, g] = 8.  `group` is 32, 64 or a multiple of 128. */
+typedef struct spmv_quant spmv_quant;
+
+typedef struct spmv_quant_info {
+    int32_t num_rows;
+    int32_t num_cols;
+    int32_t group_size;
+    int32_t num_groups;   /* groups per row: ceil(C / group)              */
+    int32_t scale_dtype;  /* spmv_dtype of the scales                     */
+    int32_t zero_points;  /* 1 if the matrix has zero points              */
+    int64_t device_bytes; /* device memory owned by the handle            */
+} spmv_quant_info;
+
+/* Arrays spmv_quant_export copies, in the caller's order. */
+typedef enum spmv_quant_array {
+    SPMV_Q_CODES = 0,  /* uint8 [R, ceil(C/2)]: column 2i in the low half of byte i, column
+                          2i+1 in the high half (0 past the last column)               */
+    SPMV_Q_SCALES = 1, /* [R, num_groups] of scale_dtype                                */
+    SPMV_Q_ZEROS = 2   /* uint8 [R, num_groups]; no bytes without zero points           */
+} spmv_quant_array;
+
+/*
+ * spmv_quant_build -- quantise a dense matrix on the device.
+ *   weights_dev: [R, C] of weight_dtype with row stride ld.
+ *   Per row and group, with rne = round to nearest even of the exact quotient:
+ *     zero_points = 0: scale = (max |w|) / 7, zero = 8;
+ *     zero_points = 1: lo = min(0, min w), hi = max(0, max w),
+ *                      scale = (hi - lo) / 15, zero = clamp(rne(-lo / scale), 0, 15);
+ *     (fp32 arithmetic, the quotient rounded to scale_dtype)
+ *     code = clamp(rne(w / scale) + zero, 0, 15); a scale of 0 makes every code `zero`.
+ *   A weight that is not finite, or a scale beyond scale_dtype's range, is
+ *   refused with SPMV_ERR_BAD_VALUE.  Host-synchronous; the handle owns its arrays.
+ */
+spmv_status spmv_quant_build(spmv_quant **out, int32_t num_rows, int32_t num_cols,
+                             int32_t group_size, int32_t zero_points, spmv_dtype scale_dtype,
+                             const void *weights_dev, int64_t ld, spmv_dtype weight_dtype,
+                             void *stream);
+
+/*
+ * spmv_quant_build_packed -- the handle of a matrix that is quantised already.
+ *   codes_dev, scales_dev, zeros_dev: as SPMV_Q_CODES, SPMV_Q_SCALES and
+ *   SPMV_Q_ZEROS above, contiguous; zeros_dev NULL: zero points of 8.
+ *   `validate` nonzero: scales must be finite and zero points at most 15
+ *   (SPMV_ERR_BAD_VALUE); zero points are kept modulo 16 without it.
+ *   Host-synchronous; the inputs may be freed when it returns.
+ */
+spmv_status spmv_quant_build_packed(spmv_quant **out, int32_t num_rows, int32_t num_cols,
+                                    int32_t group_size, const uint8_t *codes_dev,
+                                    const void *scales_dev, spmv_dtype scale_dtype,
+                                    const uint8_t *zeros_dev, int32_t validate, void *stream);
+
+/*
+ * spmv_quant_run -- y <- W x + y (accumulate nonzero) or y <- W x, for `n`
+ * vectors: row v of x_dev [n, C] gives row v of y_dev [n, R].
+ *   y_dtype is x_dtype or SPMV_FP32.  Products of fp32 vectors keep all 24 bits
+ *   of x.  Infinities and NaN in x reach exactly the vectors that hold them.
+ *   Must be called on the handle's device (SPMV_ERR_DEVICE).
+ */
+spmv_status spmv_quant_run(const spmv_quant *q, int32_t n, const void *x_dev, int64_t x_ld,
+                           spmv_dtype x_dtype, void *y_dev, int64_t y_ld, spmv_dtype y_dtype,
+                           int32_t accumulate, void *stream);
+
+/* spmv_quant_lookup -- as spmv_lookup, the table being the 4-bit matrix
+ * (num_rows = R rows of C columns).  Must be called on the handle's device. */
+spmv_status spmv_quant_lookup(const spmv_quant *q, int64_t n, const void *ids_dev,
+                              spmv_dtype id_dtype, float scale, void *out_dev, int64_t out_ld,
+                              spmv_dtype out_dtype, void *stream);
+
+spmv_status spmv_quant_get_info(const spmv_quant *q, spmv_quant_info *info_host);
+spmv_status spmv_quant_array_bytes(const spmv_quant *q, spmv_quant_array which, size_t *bytes);
+/* Copies an array to host memory (synchronous); `bytes` must equal its size. */
+spmv_status spmv_quant_export(const spmv_quant *q, spmv_quant_array which, void *host_dst,
+                              size_t bytes);
+/* Frees the handle (synchronises its device first).  NULL is accepted. */
+spmv_status spmv_quant_destroy(spmv_quant *q);
+
+/*
+ * spmv_lookup -- out[t, :] = scale * table[ids[t], :] for t < n.
+ *   table_dev: [num_rows, num_cols] of table_dtype; out_dev: [n, num_cols] of
+ *   out_dtype.  A token outside [0, num_rows) (a padded position) gives a row
+ *   of zeros.
+ */
+spmv_status spmv_lookup(int32_t num_rows, int32_t num_cols, const void *table_dev,
+                        int64_t table_ld, spmv_dtype table_dtype, int64_t n,
+                        const void *ids_dev, spmv_dtype id_dtype, float scale, void *out_dev,
+                        int64_t out_ld, spmv_dtype out_dtype, void *stream);
+
+/*
+ * spmv_lookup_grad -- the gradient of spmv_lookup with respect to its table:
+ *     dtable[v, :] = scale * sum of grad[t, :] over t with ids[t] = v
+ *                    (+ dtable[v, :] if accumulate is nonzero).
+ *   grad_dev: [n, num_cols] of grad_dtype; dtable_dev: [num_rows, num_cols] of
+ *   table_dtype.  Without `accumulate` every row is written, zeros where no
+ *   token names it; with it, rows that no token names are left untouched.
+ *   Tokens outside [0, num_rows) contribute nothing.  The tokens are sorted
+ *   (stable radix sort) and each row's gradients summed in token order.
+ *   n is below 2^31 (SPMV_ERR_TOO_LARGE); n * num_cols may pass it.
+ *   workspace_dev: at least spmv_lookup_grad_workspace() bytes, 16-byte
+ *   aligned, used until the work on `stream` is done; calls that may overlap
+ *   in time need workspaces of their own.
+ */
+spmv_status spmv_lookup_grad_workspace(int32_t num_rows, int32_t num_cols, int64_t n,
+                                       size_t *bytes);
+spmv_status spmv_lookup_grad(int32_t num_rows, int32_t num_cols, int64_t n, const void *ids_dev,
+                             spmv_dtype id_dtype, const void *grad_dev, int64_t grad_ld,
+                             spmv_dtype grad_dtype, float scale, int32_t accumulate,
+                             void *dtable_dev, int64_t dtable_ld, spmv_dtype table_dtype,
+                             void *workspace_dev, size_t workspace_bytes, void *stream);
 
 const char *spmv_status_string(spmv_status status);
 const char *spmv_format_name(spmv_format format);

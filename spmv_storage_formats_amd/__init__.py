@@ -9,6 +9,14 @@ call raises.
     import torch, spmv_storage_formats_amd as spmv
     h = spmv.build("auto", row_ptrs, col_idx, values, num_cols)   # cuda tensors
     h.run(x, y)                  # y += A x on torch's current stream
+
+Weight tables (fp32, fp16 and bf16; token ids int32 or int64):
+
+    q = spmv.build_quant(weights, group_size=128)    # 4 bits per weight, scales per group
+    q.run(x, y)                                      # y += W x, one vector or several
+    rows = q.lookup(ids)                             # rows of W by token
+    rows = spmv.lookup(table, ids, scale=1.0)        # rows of a dense table by token
+    dtable = spmv.lookup_grad(drows, ids, num_rows)  # its gradient, by sorted tokens
 """
 from __future__ import annotations
 
@@ -22,7 +30,8 @@ import numpy as np
 
 __all__ = ["SpmvError", "Handle", "FORMATS", "ARRAYS", "load_library", "analyze", "select",
            "build", "build_coo", "build_tuned", "coo_to_csr", "library_path",
-           "declared_functions"]
+           "declared_functions", "QuantHandle", "build_quant", "build_quant_packed", "lookup",
+           "lookup_grad", "lookup_grad_workspace"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_PKG)
@@ -52,7 +61,8 @@ BC_BLOCK_ROWS = 32768           # SPMV_BC_BLOCK_ROWS: blocked COO rows per row b
 BC_BLOCK_ROWS_TALL = 38912      # SPMV_BC_BLOCK_ROWS_TALL: blocks of balanced layouts
 STATUS = {0: "SPMV_OK", 1: "SPMV_ERR_INVALID_ARG", 2: "SPMV_ERR_BAD_ROWPTRS",
           3: "SPMV_ERR_BAD_COLIDX", 4: "SPMV_ERR_BAD_ROWIDX", 5: "SPMV_ERR_TOO_LARGE",
-          6: "SPMV_ERR_OOM", 7: "SPMV_ERR_HIP", 8: "SPMV_ERR_DEVICE"}
+          6: "SPMV_ERR_OOM", 7: "SPMV_ERR_HIP", 8: "SPMV_ERR_DEVICE", 9: "SPMV_ERR_BAD_VALUE"}
+DTYPES = {"float32": 0, "float16": 1, "bfloat16": 2, "int32": 3, "int64": 4}   # spmv_dtype
 
 
 class SpmvError(RuntimeError):
@@ -93,6 +103,13 @@ class _TuneEntry(ctypes.Structure):
                 ("status", ctypes.c_int32), ("us", ctypes.c_float)]
 
 
+class _QuantInfo(ctypes.Structure):
+    _fields_ = [("num_rows", ctypes.c_int32), ("num_cols", ctypes.c_int32),
+                ("group_size", ctypes.c_int32), ("num_groups", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int32), ("zero_points", ctypes.c_int32),
+                ("device_bytes", ctypes.c_int64)]
+
+
 TUNE_MAX = 32
 
 
@@ -105,6 +122,7 @@ _lock = threading.Lock()
 _lib = None
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 
 
 def library_path() -> str:
@@ -153,6 +171,26 @@ def load_library():
             "spmv_array_bytes": (ctypes.c_int, [_vp, ctypes.c_int, P(ctypes.c_size_t)]),
             "spmv_export": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_size_t]),
             "spmv_destroy": (ctypes.c_int, [_vp]),
+            "spmv_quant_build": (ctypes.c_int, [P(_vp), _i32, _i32, _i32, _i32, ctypes.c_int,
+                                                _vp, _i64, ctypes.c_int, _vp]),
+            "spmv_quant_build_packed": (ctypes.c_int, [P(_vp), _i32, _i32, _i32, _vp, _vp,
+                                                       ctypes.c_int, _vp, _i32, _vp]),
+            "spmv_quant_run": (ctypes.c_int, [_vp, _i32, _vp, _i64, ctypes.c_int, _vp, _i64,
+                                              ctypes.c_int, _i32, _vp]),
+            "spmv_quant_lookup": (ctypes.c_int, [_vp, _i64, _vp, ctypes.c_int, ctypes.c_float,
+                                                 _vp, _i64, ctypes.c_int, _vp]),
+            "spmv_quant_get_info": (ctypes.c_int, [_vp, P(_QuantInfo)]),
+            "spmv_quant_array_bytes": (ctypes.c_int, [_vp, ctypes.c_int, P(ctypes.c_size_t)]),
+            "spmv_quant_export": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_size_t]),
+            "spmv_quant_destroy": (ctypes.c_int, [_vp]),
+            "spmv_lookup": (ctypes.c_int, [_i32, _i32, _vp, _i64, ctypes.c_int, _i64, _vp,
+                                           ctypes.c_int, ctypes.c_float, _vp, _i64, ctypes.c_int,
+                                           _vp]),
+            "spmv_lookup_grad_workspace": (ctypes.c_int, [_i32, _i32, _i64,
+                                                          P(ctypes.c_size_t)]),
+            "spmv_lookup_grad": (ctypes.c_int, [_i32, _i32, _i64, _vp, ctypes.c_int, _vp, _i64,
+                                                ctypes.c_int, ctypes.c_float, _i32, _vp, _i64,
+                                                ctypes.c_int, _vp, ctypes.c_size_t, _vp]),
             "spmv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "spmv_format_name": (ctypes.c_char_p, [ctypes.c_int]),
         }
@@ -449,3 +487,349 @@ def build_tuned(row_ptrs, col_idx, values, num_cols: int, *, formats=None, runs:
                        "status": STATUS.get(e.status, e.status), "us": float(e.us),
                        "chosen": i == rep.chosen})
     return Handle(out.value, row_ptrs.device), report
+
+
+# ------------------------------------------------------------- weight tables
+
+_FLOATS = ("float32", "float16", "bfloat16")
+_IDS = ("int32", "int64")
+_codes = {}     # torch dtype -> spmv_dtype, filled by _kind
+
+
+def _kind(dtype, allowed, name):
+    """spmv_dtype of a torch dtype, which must be one of `allowed`."""
+    hit = _codes.get((dtype, allowed))
+    if hit is None:
+        s = str(dtype).replace("torch.", "")
+        if s not in allowed:
+            raise TypeError(f"{name} must be one of {', '.join(allowed)}, got {dtype}")
+        hit = _codes[(dtype, allowed)] = DTYPES[s]
+    return hit
+
+
+def _rows(t, name, device, rows, cols):
+    """(pointer, row stride, spmv_dtype) of a cuda matrix [rows, cols] whose rows are
+    contiguous (rows None: any number)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a cuda tensor")
+    kind = _kind(t.dtype, _FLOATS, name)
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"({'any' if rows is None else rows}, {cols})")
+    ld, step = t.stride()
+    if (step != 1 and cols > 1) or (ld < cols and t.shape[0] > 1):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr() if t.numel() else None, ld, kind
+
+
+def _token_ids(ids, device=None):
+    """(pointer, count, spmv_dtype) of contiguous token ids of any shape."""
+    import torch
+    if not isinstance(ids, torch.Tensor) or not ids.is_cuda:
+        raise TypeError("ids must be a cuda tensor")
+    kind = _kind(ids.dtype, _IDS, "ids")
+    if device is not None and ids.device != device:
+        raise ValueError(f"ids are on {ids.device}, expected {device}")
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    n = ids.numel()
+    return ids.data_ptr() if n else None, n, kind
+
+
+def _apart(a, b, what):
+    """Refuse tensors whose memory overlaps.  Column ranges of one buffer that lie side
+    by side (equal row strides) do not."""
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    a1, b1 = a0 + _span(a), b0 + _span(b)
+    if a0 >= b1 or b0 >= a1 or a0 == a1 or b0 == b1:
+        return
+    if a.dim() == 2 and b.dim() == 2:
+        step = a.stride(0) * a.element_size()
+        if step == b.stride(0) * b.element_size() and step > 0:
+            at = (b0 - a0) % step
+            if at >= a.shape[1] * a.element_size() and at + b.shape[1] * b.element_size() <= step:
+                return
+    raise ValueError(f"{what} must not overlap")
+
+
+def _span(t):
+    """Bytes from a tensor's first element to behind its last."""
+    if t.is_contiguous():
+        return t.numel() * t.element_size()
+    return t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+
+
+def _on(device, stream, call, *made):
+    """call(stream handle) with `device` current.  Tensors in `made` were allocated
+    for the call on torch's current stream: where the work runs on another one,
+    their memory must not be reused before it is done."""
+    import torch
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _on(device, stream, call, *made)
+    current = torch.cuda.current_stream(device)
+    if stream is None:
+        return call(current.cuda_stream)
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if made and handle != current.cuda_stream:
+        other = (stream if isinstance(stream, torch.cuda.Stream)
+                 else torch.cuda.ExternalStream(handle, device=device))
+        other.wait_stream(current)      # an allocation may still be in use there
+        for t in made:
+            t.record_stream(other)
+    return call(handle)
+
+
+class QuantHandle:
+    """A matrix in 4 bits per weight: W[r, c] = scale[r, g] * (code[r, c] - zero[r, g])
+    with g = c // group_size.  Owns its device arrays."""
+
+    ARRAYS = {"codes": 0, "scales": 1, "zero_points": 2}
+
+    def __init__(self, ptr: int, device, scale_dtype):
+        self._ptr = ctypes.c_void_p(ptr)
+        self.device = device
+        self.scale_dtype = scale_dtype
+        info = _QuantInfo()
+        _check(load_library().spmv_quant_get_info(self._ptr, ctypes.byref(info)),
+               "spmv_quant_get_info")
+        self.info = {k: int(getattr(info, k)) for k, _ in _QuantInfo._fields_
+                     if k != "scale_dtype"}
+        self.num_rows = info.num_rows
+        self.num_cols = info.num_cols
+        self.group_size = info.group_size
+
+    def _live(self):
+        if self._ptr is None:
+            raise RuntimeError("handle destroyed")
+        return self._ptr
+
+    def run(self, x, y, *, accumulate: bool = True, stream=None):
+        """y <- W x + y (accumulate) or y <- W x, enqueued on `stream` (default: torch's
+        current stream).  x [C] and y [R], or x [n, C] and y [n, R] for n vectors; y of
+        x's type or fp32."""
+        ptr = self._live()
+        if x.dim() == 1 and y.dim() == 1:
+            self.run(x[None], y[None], accumulate=accumulate, stream=stream)
+            return y
+        n = y.shape[0] if y.dim() else 0
+        xp, x_ld, xk = _rows(x, "x", self.device, n, self.num_cols)
+        yp, y_ld, yk = _rows(y, "y", self.device, n, self.num_rows)
+        if yk != xk and yk != 0:
+            raise TypeError(f"y must be {x.dtype} or torch.float32, got {y.dtype}")
+        _apart(x, y, "x and y")
+        lib = load_library()
+        _check(_on(self.device, stream, lambda s: lib.spmv_quant_run(
+            ptr, n, xp, x_ld, xk, yp, y_ld, yk, 1 if accumulate else 0, s)), "spmv_quant_run")
+        return y
+
+    def lookup(self, ids, out=None, *, scale: float = 1.0, dtype=None, stream=None):
+        """Rows of the matrix by token: out[t, :] = scale * W[ids[t], :], zeros for ids
+        outside [0, R).  Returns `out` (default: a new tensor ids.shape + [C] of `dtype`,
+        fp32 unless given)."""
+        import torch
+        ptr = self._live()
+        ip, n, ik = _token_ids(ids, self.device)
+        made = ()
+        if out is None:
+            out = torch.empty((*ids.shape, self.num_cols), dtype=dtype or torch.float32,
+                              device=self.device)
+            made = (out,)
+        flat = _by_token(out, ids, self.num_cols, "out", dtype)
+        op, ld, ok = _rows(flat, "out", self.device, n, self.num_cols)
+        _apart(ids, out, "ids and out")
+        lib = load_library()
+        _check(_on(self.device, stream, lambda s: lib.spmv_quant_lookup(
+            ptr, n, ip, ik, scale, op, ld, ok, s), *made), "spmv_quant_lookup")
+        return out
+
+    def array(self, name: str) -> np.ndarray:
+        """Copy one of the matrix's arrays to a numpy array: "codes" (uint8 [R, ceil(C/2)],
+        the even column in the low half), "scales" (float32 values [R, groups]) or
+        "zero_points" (uint8 [R, groups]; empty without zero points)."""
+        import torch
+        ptr = self._live()
+        lib = load_library()
+        which = self.ARRAYS[name]
+        n = ctypes.c_size_t()
+        _check(lib.spmv_quant_array_bytes(ptr, which, ctypes.byref(n)), "spmv_quant_array_bytes")
+        raw = np.empty(n.value, np.uint8)
+        with torch.cuda.device(self.device):
+            _check(lib.spmv_quant_export(ptr, which, raw.ctypes.data if raw.size else None,
+                                         n.value), "spmv_quant_export")
+        if name == "scales":
+            if raw.size == 0:
+                return np.empty((self.num_rows, self.info["num_groups"]), np.float32)
+            raw = torch.from_numpy(raw).view(self.scale_dtype).float().numpy()
+        if name == "codes":
+            return raw.reshape(self.num_rows, (self.num_cols + 1) // 2)
+        return raw.reshape(self.num_rows, -1) if raw.size else raw
+
+    def close(self):
+        if sys.is_finalizing():
+            return  # the HIP runtime may already be gone; the process frees it
+        if getattr(self, "_ptr", None) is not None and _lib is not None:
+            _lib.spmv_quant_destroy(self._ptr)
+        self._ptr = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _by_token(t, ids, cols, name, dtype=None):
+    """A tensor of shape ids.shape + [cols] as a matrix over the tokens."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.shape != (*ids.shape, cols):
+        raise ValueError(f"{name} must be a tensor of shape {(*ids.shape, cols)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, dtype says {dtype}")
+    if t.dim() == 2:
+        return t
+    try:
+        return t.view(ids.numel(), cols)
+    except RuntimeError:
+        raise ValueError(f"{name}'s rows must lie at one stride") from None
+
+
+def build_quant(weights, *, group_size: int = 128, zero_points: bool = False, scale_dtype=None,
+                stream=None) -> QuantHandle:
+    """Quantise a dense cuda matrix [R, C] (fp32, fp16 or bf16) to 4 bits per weight with a
+    scale, and with `zero_points` a zero point, per row and group of `group_size` columns
+    (32, 64 or a multiple of 128).  Scales are kept in `scale_dtype` (default: weights')."""
+    import torch
+    if not isinstance(weights, torch.Tensor) or weights.dim() != 2:
+        raise ValueError("weights must be a matrix")
+    R, C = weights.shape
+    wp, ld, wk = _rows(weights, "weights", None, R, C)
+    scale_dtype = scale_dtype or weights.dtype
+    sk = _kind(scale_dtype, _FLOATS, "scale_dtype")
+    lib = load_library()
+    out = ctypes.c_void_p()
+    _check(_on(weights.device, stream, lambda s: lib.spmv_quant_build(
+        ctypes.byref(out), R, C, int(group_size), 1 if zero_points else 0, sk, wp, ld, wk, s)),
+        "spmv_quant_build")
+    return QuantHandle(out.value, weights.device, scale_dtype)
+
+
+def build_quant_packed(codes, scales, num_cols: int, *, group_size: int = 128, zero_points=None,
+                       validate: bool = True, stream=None) -> QuantHandle:
+    """The handle of a matrix that is quantised already: codes uint8 [R, ceil(num_cols/2)]
+    (the even column in the low half of a byte), scales [R, ceil(num_cols/group_size)]
+    (fp32, fp16 or bf16) and zero_points uint8 like scales (None: 8 everywhere)."""
+    import torch
+    num_cols, group_size = int(num_cols), int(group_size)
+    cp = _dev(codes, torch.uint8, "codes")
+    if codes.dim() != 2 or num_cols < 0 or codes.shape[1] != (num_cols + 1) // 2:
+        raise ValueError(f"codes must be [R, {(num_cols + 1) // 2}], got {tuple(codes.shape)}")
+    R = codes.shape[0]
+    if group_size <= 0:
+        raise ValueError("group_size must be positive")
+    shape = (R, -(-num_cols // group_size))
+    sk = _kind(getattr(scales, "dtype", None), _FLOATS, "scales")
+    sp = _dev(scales, scales.dtype, "scales")
+    zp = None if zero_points is None else _dev(zero_points, torch.uint8, "zero_points")
+    for t, name in ((scales, "scales"), (zero_points, "zero_points")):
+        if t is not None and (tuple(t.shape) != shape or t.device != codes.device):
+            raise ValueError(f"{name} must be {shape} on {codes.device}, got "
+                             f"{tuple(t.shape)} on {t.device}")
+    lib = load_library()
+    out = ctypes.c_void_p()
+    _check(_on(codes.device, stream, lambda s: lib.spmv_quant_build_packed(
+        ctypes.byref(out), R, num_cols, group_size, cp, sp, sk, zp, 1 if validate else 0, s)),
+        "spmv_quant_build_packed")
+    return QuantHandle(out.value, codes.device, scales.dtype)
+
+
+def lookup(table, ids, out=None, *, scale: float = 1.0, dtype=None, stream=None):
+    """Rows of a dense table [V, D] by token: out[t, :] = scale * table[ids[t], :], zeros for
+    ids outside [0, V) (padded positions).  Returns `out` (default: a new tensor
+    ids.shape + [D] of `dtype`, the table's unless given)."""
+    import torch
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be a matrix")
+    V, D = table.shape
+    tp, t_ld, tk = _rows(table, "table", None, V, D)
+    device = table.device
+    ip, n, ik = _token_ids(ids, device)
+    made = ()
+    if out is None:
+        out = torch.empty((*ids.shape, D), dtype=dtype or table.dtype, device=device)
+        made = (out,)
+    flat = _by_token(out, ids, D, "out", dtype)
+    op, o_ld, ok = _rows(flat, "out", device, n, D)
+    if not made:
+        _apart(table, out, "table and out")
+        _apart(ids, out, "ids and out")
+    lib = load_library()
+    _check(_on(device, stream, lambda s: lib.spmv_lookup(
+        V, D, tp, t_ld, tk, n, ip, ik, scale, op, o_ld, ok, s), *made), "spmv_lookup")
+    return out
+
+
+def lookup_grad_workspace(num_tokens: int, num_rows: int, num_cols: int) -> int:
+    """Bytes of workspace that lookup_grad needs for these sizes."""
+    n = ctypes.c_size_t()
+    _check(load_library().spmv_lookup_grad_workspace(num_rows, num_cols, num_tokens,
+                                                     ctypes.byref(n)),
+           "spmv_lookup_grad_workspace")
+    return n.value
+
+
+def lookup_grad(grad, ids, num_rows: int, out=None, *, scale: float = 1.0,
+                accumulate: bool = False, dtype=None, workspace=None, stream=None):
+    """Gradient of lookup with respect to its table: out[v, :] = scale * the sum of grad[t, :]
+    over the tokens t with ids[t] = v, added to `out` with `accumulate`.  grad is ids.shape +
+    [D]; ids outside [0, num_rows) contribute nothing.  Returns `out` (default: a new tensor
+    [num_rows, D] of `dtype`, grad's unless given).  `workspace`: a contiguous uint8 cuda
+    tensor of at least lookup_grad_workspace() bytes, for this call alone until its work is
+    done (default: allocated for the call)."""
+    import torch
+    num_rows = int(num_rows)
+    if not isinstance(grad, torch.Tensor) or not grad.is_cuda or grad.dim() < 1:
+        raise TypeError("grad must be a cuda tensor")
+    device, D = grad.device, grad.shape[-1]
+    ip, n, ik = _token_ids(ids, device)
+    flat = _by_token(grad, ids, D, "grad")
+    gp, g_ld, gk = _rows(flat, "grad", device, n, D)
+    if num_rows < 0:
+        raise ValueError("num_rows must not be negative")
+    made = []
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty(num_rows, D, dtype=dtype or grad.dtype, device=device)
+        made.append(out)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out is {out.dtype}, dtype says {dtype}")
+    op, o_ld, ok = _rows(out, "out", device, num_rows, D)
+    if not made:
+        _apart(grad, out, "grad and out")
+        _apart(ids, out, "ids and out")
+    need = lookup_grad_workspace(n, num_rows, D)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        made.append(workspace)
+    else:
+        _apart(workspace, out, "workspace and out")
+        _apart(workspace, grad, "workspace and grad")
+        _apart(workspace, ids, "workspace and ids")
+    wp = _dev(workspace, torch.uint8, "workspace")
+    if workspace.numel() < need or workspace.device != device:
+        raise ValueError(f"workspace must hold {need} bytes on {device}")
+    lib = load_library()
+    _check(_on(device, stream, lambda s: lib.spmv_lookup_grad(
+        num_rows, D, n, ip, ik, gp, g_ld, gk, scale, 1 if accumulate else 0, op, o_ld, ok, wp,
+        workspace.numel(), s), *made), "spmv_lookup_grad")
+    return out

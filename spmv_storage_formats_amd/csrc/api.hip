@@ -1081,6 +1081,7 @@ const char *spmv_status_string(spmv_status st) {
     case SPMV_ERR_OOM: return "device out of memory";
     case SPMV_ERR_HIP: return "HIP runtime error";
     case SPMV_ERR_DEVICE: return "handle used on a different device";
+    case SPMV_ERR_BAD_VALUE: return "value not finite or out of range";
     default: return "unknown status";
     }
 }
