@@ -12,9 +12,8 @@ constexpr int kThreads = 256;
          i += static_cast<int64_t>(gridDim.x) * kThreads)
 
 __device__ inline int64_t word_index(int32_t r, int32_t octet, int32_t blocks) {
-    const int64_t block = static_cast<int64_t>(r / kQuantRows) * blocks + octet / kQuantRowWords;
-    return block * kQuantBlockWords + (r % kQuantRows) * kQuantRowWords +
-           quant_word(octet % kQuantRowWords);
+    const int64_t block = static_cast<int64_t>(r / kQuantRows) * blocks + octet / kQuantOctets;
+    return block * kQuantBlockWords + quant_word(r % kQuantRows, octet % kQuantOctets);
 }
 
 __device__ inline int64_t scale_index(int32_t r, int32_t g, int32_t groups_pad) {

@@ -8,16 +8,18 @@
 #include "internal.h"
 
 // The 4-bit matrix.  Rows are cut into tiles of kQuantRows, columns into
-// blocks of kQuantCols; both are padded with code 0 and scale 0.  The codes
-// of one (tile, block) are 2 KiB: 16 rows of 128 consecutive bytes, so that a
-// row's part is one cache line for the lookup and the whole block one stream
-// for the product.  A word holds eight consecutive columns k0 .. k0+7 (an
-// octet): bits rotated left by 3 of  sum_i code[k0 + 2i] << 4i  |  code[k0 + 2i + 1] << (16 + 4i),
+// blocks of kQuantCols; both are padded with code 0 and scale 0.  The codes of
+// one (tile, block) are 1 KiB.  A word holds eight consecutive columns
+// k0 .. k0+7 (an octet): bits rotated left by 3 of
+//     sum_i code[k0 + 2i] << 4i  |  code[k0 + 2i + 1] << (16 + 4i),
 // so that a shift and a mask bring two neighbouring codes to the mantissa
-// bits of two 16-bit floats.  Octet o of the block (o = 0..31) is word
-// (o / 16) * 16 + (o % 4) * 4 + (o % 16) / 4 of its row: the 16 bytes that a
-// lane loads are the four octets it feeds to four matrix instructions, each of
-// which covers 32 consecutive columns.
+// bits of two 16-bit floats.  The 16 bytes that a lane of the product loads
+// are octets q, q + 4, q + 8, q + 12 of a row's 16 (q = the lane's quad): four
+// matrix instructions, each over 32 consecutive columns.  Four rows' 16 bytes
+// lie side by side (neighbouring lanes load neighbouring bytes: 16 accesses
+// of the vector cache per load instruction instead of 64), then the quads,
+// then the next four rows: a row's 64 bytes are spread over 256, which is
+// what a lookup of it reads.
 // Scales and zero points: [tile][group][16 rows], `groups_pad` groups.
 struct spmv_quant {
     int device = 0;
@@ -36,9 +38,9 @@ struct spmv_quant {
 namespace spmv {
 
 constexpr int kQuantRows = 16;
-constexpr int kQuantCols = 256;
-constexpr int kQuantRowWords = kQuantCols / 8;                 // 32
-constexpr int kQuantBlockWords = kQuantRows * kQuantRowWords;  // 512
+constexpr int kQuantCols = 128;
+constexpr int kQuantOctets = kQuantCols / 8;                 // 16
+constexpr int kQuantBlockWords = kQuantRows * kQuantOctets;  // 256
 
 using bf16 = __bf16;
 using f16 = _Float16;
@@ -115,10 +117,10 @@ __device__ inline void store_octet_tail(T *p, int count, const float *in) {
         if (i < count) p[i] = static_cast<T>(in[i]);
 }
 
-// Word of octet o (0..31) in its row's 32 words, and the code of column
-// k0 + e in a word (the layout above).
-__host__ __device__ inline int quant_word(int o) {
-    return (o / 16) * 16 + (o % 4) * 4 + (o % 16) / 4;
+// Word of (row r of a tile, octet o of a block) in its block, and the code of
+// column k0 + e in a word (the layout above).
+__host__ __device__ inline int quant_word(int r, int o) {
+    return (r / 4) * 64 + (o % 4) * 16 + (r % 4) * 4 + o / 4;
 }
 __device__ inline uint32_t quant_code(uint32_t word, int e) {
     const int bit = ((e & 1) * 16 + (e >> 1) * 4 + 3) & 31;

@@ -14,7 +14,8 @@ import pytest
 
 from spmv_storage_formats_amd import _build
 
-SOURCES = ["quant.hip", "quant_run.hip", "lookup.hip"]
+SOURCES = ["quant.hip", "quant_run_fp32.hip", "quant_run_fp16.hip", "quant_run_bf16.hip",
+           "lookup.hip"]
 SCC_COMPARES = ("s_cmp", "s_bitcmp", "s_and", "s_or", "s_xor", "s_andn", "s_nor", "s_not")
 SCC_WRITERS = re.compile(r"s_(add|addc|sub|subb|cmp\w*|bitcmp\w*|and|or|xor|not|nand|nor|xnor|"
                          r"andn\w*|orn\w*|lshl|lshr|ashr|bfe|abs|min|max|bcnt\w*|absdiff|addk|"
@@ -67,6 +68,6 @@ def test_conditions_are_read_where_they_were_set(listings, name):
     assert misread_conditions(listings[name]) == []
 
 
-@pytest.mark.parametrize("name", ["quant_run.hip", "lookup.hip"])
+@pytest.mark.parametrize("name", SOURCES[1:])
 def test_no_global_atomics(listings, name):
     assert not re.search(r"\b(global|flat|buffer)_atomic_", listings[name])
