@@ -175,38 +175,110 @@ __device__ inline void sort_tile(SortShared &s, const uint32_t *key, const uint3
     __syncthreads();
 }
 
-// All passes of at most kSortTile tokens in one workgroup.
+// Up to kMergeMost tokens are sorted in two launches: tiles of kRankTile by
+// counting, then all tiles merged by searching.  (Radix passes over many
+// tiles take two launches each.)
+constexpr int kRankTile = kSortWaves * kWave;
+constexpr int kMergeMost = 1 << 16;
+
+// A token's place in its tile is the number of the tile's tokens that sort
+// before it.  A workgroup ranks 64 tokens, one per lane, in all its waves;
+// each wave holds 64 of the tile's keys and broadcasts them in turn.
 template <typename I>
-__global__ __launch_bounds__(kSortThreads) void k_sort_one(const I *__restrict__ ids, int32_t V,
-                                                           int count, int passes, int bits,
-                                                           uint32_t *__restrict__ keys_out,
-                                                           uint32_t *__restrict__ pos_out) {
-    __shared__ SortShared s;
-    const int lane = __lane_id(), w = threadIdx.x / kWave;
-    uint32_t key[kSortSteps], pos[kSortSteps];
+__global__ __launch_bounds__(kSortThreads) void k_sort_tiles(const I *__restrict__ ids, int32_t V,
+                                                             int n,
+                                                             uint32_t *__restrict__ keys_out,
+                                                             uint32_t *__restrict__ pos_out) {
+    __shared__ int part[kSortWaves][kWave];
+    const int lane = __lane_id();
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int tile = static_cast<int>(blockIdx.x) / kSortWaves * kRankTile;
+    const int own = static_cast<int>(blockIdx.x) % kSortWaves;
+    const int t = tile + own * kWave + lane, j = tile + w * kWave + lane;
+    const uint32_t key = t < n ? token_key(ids, t, V) : 0u;
+    const uint32_t k = j < n ? token_key(ids, j, V) : 0xffffffffu;  // behind every key
+    int before = 0;
+    if (w != own) {
+        // equal keys of an earlier wave come first: k < key + 1
+        const uint32_t limit = key + (w < own ? 1u : 0u);
 #pragma unroll
-    for (int j = 0; j < kSortSteps; ++j) {
-        const int i = (w * kSortSteps + j) * kWave + lane;
-        pos[j] = i;
-        key[j] = i < count ? token_key(ids, i, V) : 0u;
+        for (int l = 0; l < kWave; ++l)
+            before += static_cast<uint32_t>(__builtin_amdgcn_readlane(k, l)) < limit;
+    } else {
+#pragma unroll
+        for (int l = 0; l < kWave; ++l)
+            before += static_cast<uint32_t>(__builtin_amdgcn_readlane(k, l)) <
+                      key + (l < lane ? 1u : 0u);
     }
-    for (int p = 0; p < passes; ++p) {
-        sort_tile(s, key, pos, count, p * bits, bits);
+    part[w][lane] = before;
+    __syncthreads();
+    if (w == 0 && t < n) {
+        int at = tile;
 #pragma unroll
-        for (int j = 0; j < kSortSteps; ++j) {
-            const int i = (w * kSortSteps + j) * kWave + lane;
-            key[j] = i < count ? s.key[i] : 0u;
-            pos[j] = i < count ? s.pos[i] : 0u;
+        for (int i = 0; i < kSortWaves; ++i) at += part[i][lane];
+        keys_out[at] = key;
+        pos_out[at] = t;
+    }
+}
+
+// A token's place in the whole list: its place in its tile, and in every other
+// tile the number of tokens before it, by binary search.  kAbreast tiles at a
+// time are brought to LDS and searched side by side (searching them where they
+// lie costs one access of the vector cache per lane and step: 53 us against
+// the 9 of this for 32768 tokens).
+__global__ __launch_bounds__(kThreads) void k_sort_merge(int n, const uint32_t *__restrict__ keys,
+                                                         const uint32_t *__restrict__ pos,
+                                                         uint32_t *__restrict__ keys_out,
+                                                         uint32_t *__restrict__ pos_out) {
+    constexpr int kAbreast = 4;
+    constexpr int kPieces = kAbreast * kRankTile / (4 * kThreads);
+    using Four = uint32_t __attribute__((ext_vector_type(4)));
+    __shared__ __attribute__((aligned(16))) uint32_t s_key[kAbreast * kRankTile];
+    const int e = static_cast<int>(blockIdx.x) * kThreads + threadIdx.x;
+    const uint32_t key = e < n ? keys[e] : 0u;
+    const int own = e / kRankTile;
+    int at = e % kRankTile;
+    Four in[kPieces];
+    auto load = [&](int first) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int j = first + (i * kThreads + static_cast<int>(threadIdx.x)) * 4;
+            in[i] = Four{~0u, ~0u, ~0u, ~0u};  // past the end: behind every key
+            if (j + 4 <= n) {
+                in[i] = *reinterpret_cast<const Four *>(keys + j);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (j + q < n) in[i][q] = keys[j + q];
+            }
         }
+    };
+    load(0);
+    for (int first = 0; first < n; first += kAbreast * kRankTile) {
         __syncthreads();
-    }
 #pragma unroll
-    for (int j = 0; j < kSortSteps; ++j) {
-        const int i = (w * kSortSteps + j) * kWave + lane;
-        if (i < count) {
-            keys_out[i] = key[j];
-            pos_out[i] = pos[j];
+        for (int i = 0; i < kPieces; ++i)
+            *reinterpret_cast<Four *>(&s_key[(i * kThreads + threadIdx.x) * 4]) = in[i];
+        __syncthreads();
+        load(first + kAbreast * kRankTile);
+        int lo[kAbreast];
+#pragma unroll
+        for (int i = 0; i < kAbreast; ++i) lo[i] = 0;
+#pragma unroll
+        for (int s = kRankTile / 2; s >= 0; s = s > 1 ? s / 2 : s - 1) {
+            const int hop = s > 0 ? s : 1;  // the last compare is of one more key
+#pragma unroll
+            for (int i = 0; i < kAbreast; ++i) {
+                const uint32_t limit = key + (first / kRankTile + i < own ? 1u : 0u);
+                lo[i] += s_key[i * kRankTile + lo[i] + hop - 1] < limit ? hop : 0;
+            }
         }
+#pragma unroll
+        for (int i = 0; i < kAbreast; ++i) at += first / kRankTile + i != own ? lo[i] : 0;
+    }
+    if (e < n) {
+        keys_out[at] = key;
+        pos_out[at] = pos[e];
     }
 }
 
@@ -257,18 +329,29 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(
 
 // ----------------------------------------------------------------- gradient
 
-// Sorted tokens per chunk, and table rows that one workgroup clears.
-constexpr int kChunk = 32;
-constexpr int kClearRows = 16;
+constexpr int kMaxChunk = 32;   // sorted tokens per chunk, at most
+constexpr int kMinLanes = 8;    // lanes per chunk, at least
+constexpr int kClearRows = 16;  // table rows that one wave clears
 constexpr int kAhead = 8;       // gradient rows in flight per lane
-constexpr int kJoinParts = 16;  // waves that share a cut row's parts
+constexpr int kJoinParts = 4;   // waves that share a cut row's parts
 constexpr int kJoinThreads = kJoinParts * kWave;
+constexpr int kJoinCols = 4 * kWave;
 
-__device__ inline uint32_t first_not_below(const uint32_t *keys, uint32_t n, uint32_t v) {
-    uint32_t lo = 0, hi = n;
-    while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (keys[mid] < v) lo = mid + 1; else hi = mid;
+// First index in [lo, n) whose key is at least v, by all lanes of a wave:
+// 64 probes at a time.
+__device__ inline uint32_t first_not_below(const uint32_t *keys, uint32_t lo, uint32_t n,
+                                           uint32_t v) {
+    const uint32_t lane = __lane_id();
+    uint32_t len = n - lo;
+    while (len > 0) {
+        const uint32_t step = (len + kWave - 1) / kWave;
+        const uint32_t i = lane * step;
+        const bool below = i < len && keys[lo + i] < v;
+        const uint32_t c = static_cast<uint32_t>(__popcll(__ballot(below)));
+        if (c == 0) return lo;
+        const uint32_t skip = (c - 1) * step + 1;  // those are below
+        lo += skip;
+        len = len - skip < step - 1 ? len - skip : step - 1;
     }
     return lo;
 }
@@ -292,45 +375,52 @@ __device__ inline void put_row(T *p, int left, float scale, int accumulate, cons
         store_octet_tail(p, left, v);
 }
 
-// Items [0, chunks): the sums of one chunk of sorted tokens over one range of
-// columns, an octet per lane.  A row whose tokens all lie in the chunk is
-// written; the part of one that goes on from the chunk before goes to
-// head[chunk], the part of one that goes on into the next to tail[chunk]
-// (one that does both: head).
+// The sums of chunks of sorted tokens over a range of columns: a group of L
+// lanes per chunk, an octet of columns per lane.  A row whose tokens all lie
+// in the chunk is written; the part of one that goes on from the chunk before
+// goes to head[chunk], the part of one that goes on into the next to
+// tail[chunk] (one that does both: head).
 template <typename G, typename T>
 __device__ inline void grad_chunk(int32_t V, int32_t D, int64_t n,
                                   const uint32_t *__restrict__ keys,
                                   const uint32_t *__restrict__ pos, const G *__restrict__ grad,
                                   int64_t grad_ld, float scale, int accumulate,
                                   T *__restrict__ out, int64_t ld, float *__restrict__ head,
-                                  float *__restrict__ tail, int64_t chunk, int64_t col) {
-    __shared__ uint32_t s_key[kChunk];
-    __shared__ uint32_t s_pos[kChunk];
-    const int64_t base = chunk * kChunk;
-    const int count = static_cast<int>(n - base < kChunk ? n - base : kChunk);
+                                  float *__restrict__ tail, int per_chunk, int L, int64_t first,
+                                  int64_t part) {
+    __shared__ uint32_t lds_key[kThreads / kMinLanes][kMaxChunk];
+    __shared__ uint32_t lds_pos[kThreads / kMinLanes][kMaxChunk];
+    const int group = threadIdx.x / L, lane = threadIdx.x % L;
+    uint32_t *const s_key = lds_key[group], *const s_pos = lds_pos[group];
+    const int64_t chunk = first + group, base = chunk * per_chunk;
+    const int count =
+        static_cast<int>(n <= base ? 0 : n - base < per_chunk ? n - base : per_chunk);
     __syncthreads();  // the item before may still read s_key
-    if (static_cast<int>(threadIdx.x) < count) {
-        s_key[threadIdx.x] = keys[base + threadIdx.x];
-        s_pos[threadIdx.x] = pos[base + threadIdx.x];
+    for (int i = lane; i < count; i += L) {
+        s_key[i] = keys[base + i];
+        s_pos[i] = pos[base + i];
     }
     const uint32_t none = 0xffffffffu;
-    const uint32_t prev = base > 0 ? keys[base - 1] : none;
+    const uint32_t prev = count > 0 && base > 0 ? keys[base - 1] : none;
     const uint32_t next = base + count < n ? keys[base + count] : none;
     __syncthreads();
-    if (col >= D) return;
+    const int64_t col = (part * L + lane) * 8;
+    if (col >= D || count == 0) return;
     const int left = static_cast<int>(D - col < 8 ? D - col : 8);
     float sum[8] = {};
     bool from_before = s_key[0] == prev;
     for (int k0 = 0; k0 < count; k0 += kAhead) {
-        float g[kAhead][8];
+        Octet<G> g[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int k = k0 + j < count ? k0 + j : count - 1;
             const G *p = grad + static_cast<int64_t>(s_pos[k]) * grad_ld + col;
-            if (left == 8)
-                load_octet(p, g[j]);
-            else
-                load_octet_tail(p, left, g[j]);
+            if (left == 8) {
+                __builtin_memcpy(&g[j], p, sizeof(g[j]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[j].v[i] = i < left ? p[i] : static_cast<G>(0.f);
+            }
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
@@ -339,7 +429,7 @@ __device__ inline void grad_chunk(int32_t V, int32_t D, int64_t n,
             const uint32_t key = s_key[k];
             if (key >= static_cast<uint32_t>(V)) return;  // tokens that name no row come last
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += g[j][i];
+            for (int i = 0; i < 8; ++i) sum[i] += static_cast<float>(g[j].v[i]);
             const bool last = k + 1 == count;
             const uint32_t after = last ? next : s_key[k + 1];
             if (!last && after == key) continue;
@@ -359,36 +449,37 @@ __device__ inline void grad_chunk(int32_t V, int32_t D, int64_t n,
     }
 }
 
-// Items behind the chunks: zeros into those of kClearRows table rows that no
-// token names.
+// Behind the chunks: a wave writes zeros into those of kClearRows table rows
+// that no token names.
 template <typename T>
-__device__ inline void grad_clear(int32_t V, int32_t D, int64_t n,
+__device__ inline void grad_clear(int32_t V, int32_t D, uint32_t n,
                                   const uint32_t *__restrict__ keys, T *__restrict__ out,
-                                  int64_t ld, int64_t r0, int64_t col) {
-    __shared__ unsigned long long missing;
-    __syncthreads();
-    if (threadIdx.x < kWave) {
-        const int64_t v = r0 + threadIdx.x;
-        bool none = false;
-        if (threadIdx.x < kClearRows && v < V) {
-            const uint32_t at =
-                first_not_below(keys, static_cast<uint32_t>(n), static_cast<uint32_t>(v));
-            none = at == static_cast<uint32_t>(n) || keys[at] != static_cast<uint32_t>(v);
-        }
-        const unsigned long long m = __ballot(none);
-        if (threadIdx.x == 0) missing = m;
+                                  int64_t ld, int64_t r0) {
+    const int lane = __lane_id();
+    if (r0 >= V) return;
+    const uint32_t rows = static_cast<uint32_t>(V - r0 < kClearRows ? V - r0 : kClearRows);
+    const uint32_t first = static_cast<uint32_t>(r0);
+    uint32_t named = 0, at = first_not_below(keys, 0, n, first);
+    while (at < n) {
+        const uint32_t k = at + lane < n ? keys[at + lane] - first : rows;
+#pragma unroll
+        for (uint32_t i = 0; i < kClearRows; ++i) named |= __ballot(k == i) ? 1u << i : 0u;
+        const uint32_t last = __builtin_amdgcn_readlane(k, kWave - 1);
+        if (last >= rows) break;
+        at = first_not_below(keys, at + kWave, n, first + last + 1);
     }
-    __syncthreads();
-    if (col >= D) return;
-    const int left = static_cast<int>(D - col < 8 ? D - col : 8);
-    const float zero[8] = {};
-    for (int i = 0; i < kClearRows; ++i) {
-        if (!((missing >> i) & 1)) continue;
-        T *p = out + (r0 + i) * ld + col;
-        if (left == 8)
-            store_octet(p, zero);
-        else
-            store_octet_tail(p, left, zero);
+    constexpr int kPer = 16 / sizeof(T);
+    using Piece = uint32_t __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+    for (uint32_t i = 0; i < rows; ++i) {
+        if ((named >> i) & 1) continue;
+        T *p = out + (r0 + i) * ld;
+        for (int64_t c = static_cast<int64_t>(lane) * kPer; c < D; c += kWave * kPer) {
+            if (c + kPer <= D) {
+                *reinterpret_cast<Piece *>(p + c) = Piece{0, 0, 0, 0};
+            } else {
+                for (int64_t e = c; e < D; ++e) p[e] = static_cast<T>(0.f);
+            }
+        }
     }
 }
 
@@ -397,15 +488,17 @@ __global__ __launch_bounds__(kThreads) void k_grad_chunks(
     int32_t V, int32_t D, int64_t n, const uint32_t *__restrict__ keys,
     const uint32_t *__restrict__ pos, const G *__restrict__ grad, int64_t grad_ld, float scale,
     int accumulate, T *__restrict__ out, int64_t ld, float *__restrict__ head,
-    float *__restrict__ tail, int64_t chunks, int64_t clears, int64_t parts) {
-    for (int64_t i = blockIdx.x; i < (chunks + clears) * parts; i += gridDim.x) {
-        const int64_t item = i / parts;
-        const int64_t col = ((i % parts) * blockDim.x + threadIdx.x) * 8;
-        if (item < chunks)
+    float *__restrict__ tail, int per_chunk, int L, int64_t sums, int64_t clears, int64_t parts) {
+    constexpr int kWaves = kThreads / kWave;
+    for (int64_t i = blockIdx.x; i < sums + clears; i += gridDim.x) {
+        if (i < sums) {
             grad_chunk(V, D, n, keys, pos, grad, grad_ld, scale, accumulate, out, ld, head, tail,
-                       item, col);
-        else
-            grad_clear(V, D, n, keys, out, ld, (item - chunks) * kClearRows, col);
+                       per_chunk, L, i / parts * (kThreads / L), i % parts);
+        } else {
+            const int64_t w =
+                (i - sums) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+            grad_clear(V, D, static_cast<uint32_t>(n), keys, out, ld, w * kClearRows);
+        }
     }
 }
 
@@ -417,48 +510,69 @@ template <typename T>
 __global__ __launch_bounds__(kJoinThreads) void k_grad_join(
     int32_t V, int32_t D, int64_t n, const uint32_t *__restrict__ keys, float scale,
     int accumulate, T *__restrict__ out, int64_t ld, const float *__restrict__ head,
-    const float *__restrict__ tail, int64_t cuts, int64_t cols) {
-    __shared__ float s[kJoinParts][kWave];
+    const float *__restrict__ tail, int per_chunk, int64_t cuts, int64_t cols) {
+    __shared__ float s[kJoinParts][kJoinCols];
     for (int64_t item = blockIdx.x; item < cuts * cols; item += gridDim.x) {
         const int64_t c = item / cols;
-        const int64_t end = (c + 1) * kChunk;  // < n: the last chunk has no workgroup
+        const int64_t end = (c + 1) * per_chunk;  // < n: the last chunk has no workgroup
         const uint32_t key = keys[end - 1];
         if (key >= static_cast<uint32_t>(V) || keys[end] != key) continue;
-        if (c > 0 && keys[c * kChunk - 1] == key) continue;  // began before: not this chunk's
-        // The row's last token, by doubling and halving over [end, n).  Token
-        // indices are 32-bit: with 64-bit ones clang 22 selects `hi` by the scalar
-        // condition code where its compare has set the vector one.
-        uint32_t lo = static_cast<uint32_t>(end), hi = lo + 1, step = kChunk;
-        const uint32_t count = static_cast<uint32_t>(n);
-        while (hi < count && keys[hi] == key) {
-            lo = hi;
-            hi = hi + step < count ? hi + step : count;
-            step *= 2;
-        }
-        while (hi - lo > 1) {  // keys[lo] == key, keys[hi] != key or hi == n
-            const uint32_t mid = lo + (hi - lo) / 2;
-            if (keys[mid] == key) lo = mid; else hi = mid;
-        }
-        const int64_t parts = lo / kChunk - c + 1;
+        if (c > 0 && keys[c * per_chunk - 1] == key) continue;  // began before: not this chunk's
+        // the row's first token behind `end` that is another's
+        const uint32_t stop = first_not_below(keys, static_cast<uint32_t>(end) + 1,
+                                              static_cast<uint32_t>(n), key + 1);
+        const int64_t parts = (stop - 1) / per_chunk - c + 1;
         const int w = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-        const int64_t col = (item % cols) * kWave + lane;
+        const int64_t col = (item % cols) * kJoinCols + lane * 4;
+        const int left = static_cast<int>(D - col < 4 ? D - col : 4);
         const int64_t from = parts * w / kJoinParts, to = parts * (w + 1) / kJoinParts;
-        float sum = 0.f;
-        if (col < D) {
-            for (int64_t p = from; p < to; ++p)
-                sum += p == 0 ? tail[c * D + col] : head[(c + p) * D + col];
+        float sum[4] = {};
+        auto add = [&](const float *p, int count) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] += e < count ? p[e] : 0.f;
+        };
+        if (left >= 4) {
+            if (from == 0 && to > 0) add(tail + c * D + col, 4);
+            const float *p = head + c * D + col;
+#pragma unroll 8
+            for (int64_t i = from > 1 ? from : 1; i < to; ++i) {
+                float v[4];
+                __builtin_memcpy(v, p + i * D, 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] += v[e];
+            }
+        } else if (left > 0) {
+            for (int64_t i = from; i < to; ++i)
+                add((i == 0 ? tail : head + i * D) + c * D + col, left);
         }
         __syncthreads();  // the item before may still read s
-        s[w][lane] = sum;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[w][lane * 4 + e] = sum[e];
         __syncthreads();
-        if (w == 0 && col < D) {
+        const int64_t one = (item % cols) * kJoinCols + threadIdx.x;
+        if (one < D) {
             float t = 0.f;
 #pragma unroll
-            for (int i = 0; i < kJoinParts; ++i) t += s[i][lane];
-            T *p = out + static_cast<int64_t>(key) * ld + col;
+            for (int i = 0; i < kJoinParts; ++i) t += s[i][threadIdx.x];
+            T *p = out + static_cast<int64_t>(key) * ld + one;
             *p = static_cast<T>(fmaf(scale, t, accumulate ? static_cast<float>(*p) : 0.f));
         }
     }
+}
+
+// Lanes per chunk, a power of two.
+int chunk_lanes(int32_t D) {
+    return std::max(kMinLanes, lanes_for((static_cast<int64_t>(D) + 7) / 8, kThreads));
+}
+
+// Sorted tokens per chunk: short chunks while there are few, so that the sums
+// have 2048 waves (8 per CU); long ones leave fewer cut rows to join.
+int chunk_length(int32_t D, int64_t n) {
+    const int64_t octets = (static_cast<int64_t>(D) + 7) / 8, L = chunk_lanes(D);
+    const int64_t lanes = (octets + L - 1) / L * L;
+    int k = 8;
+    while (k < kMaxChunk && n * lanes > int64_t{2048} * kWave * k) k *= 2;
+    return k;
 }
 
 // Parts of the gradient's workspace, each 256-byte aligned.
@@ -478,12 +592,13 @@ GradWorkspace grad_workspace(int32_t D, int64_t n, void *base) {
         return p;
     };
     const size_t tiles = static_cast<size_t>((n + kSortTile - 1) / kSortTile);
-    const size_t chunks = static_cast<size_t>((n + kChunk - 1) / kChunk);
+    const int per_chunk = chunk_length(D, n);
+    const size_t chunks = static_cast<size_t>((n + per_chunk - 1) / per_chunk);
     for (int i = 0; i < 2; ++i) {
         w.keys[i] = reinterpret_cast<uint32_t *>(take(static_cast<size_t>(n) * 4));
         w.pos[i] = reinterpret_cast<uint32_t *>(take(static_cast<size_t>(n) * 4));
     }
-    w.counts = reinterpret_cast<int32_t *>(take(tiles > 1 ? tiles * kSortDigits * 4 : 0));
+    w.counts = reinterpret_cast<int32_t *>(take(n > kMergeMost ? tiles * kSortDigits * 4 : 0));
     const size_t part = chunks > 1 ? chunks * static_cast<size_t>(D) * 4 : 0;
     w.head = reinterpret_cast<float *>(take(part));
     w.tail = reinterpret_cast<float *>(take(part));
@@ -498,12 +613,20 @@ spmv_status sort_tokens(int32_t V, int64_t n, const I *ids, const GradWorkspace 
     const int passes = (need + kSortBits - 1) / kSortBits;
     const int bits = (need + passes - 1) / passes;
     const int32_t tiles = static_cast<int32_t>((n + kSortTile - 1) / kSortTile);
-    if (tiles == 1) {
-        k_sort_one<I><<<1, kSortThreads, 0, s>>>(ids, V, static_cast<int>(n), passes, bits,
-                                                 w.keys[0], w.pos[0]);
+    if (n <= kMergeMost) {
+        const int count = static_cast<int>(n);
+        const int rank_tiles = (count + kRankTile - 1) / kRankTile;
+        const int last = rank_tiles > 1 ? 1 : 0;
+        k_sort_tiles<I><<<(count + kWave - 1) / kWave, kSortThreads, 0, s>>>(
+            ids, V, count, w.keys[0], w.pos[0]);
         SPMV_HIP(hipGetLastError());
-        *keys = w.keys[0];
-        *pos = w.pos[0];
+        if (rank_tiles > 1) {
+            k_sort_merge<<<(count + kThreads - 1) / kThreads, kThreads, 0, s>>>(
+                count, w.keys[0], w.pos[0], w.keys[1], w.pos[1]);
+            SPMV_HIP(hipGetLastError());
+        }
+        *keys = w.keys[last];
+        *pos = w.pos[last];
         return SPMV_OK;
     }
     const uint32_t *k = nullptr, *p = nullptr;
@@ -563,29 +686,33 @@ spmv_status lookup_grad(int32_t V, int32_t D, int64_t n, const void *ids, int32_
             SPMV_TRY(sort_tokens(V, n, static_cast<const int32_t *>(ids), w, &keys, &pos, s));
     }
     const int64_t octets = (static_cast<int64_t>(D) + 7) / 8;
-    const int threads = std::max(kWave, lanes_for(octets, kThreads));
-    const int64_t parts = (octets + threads - 1) / threads;
-    const int64_t chunks = (n + kChunk - 1) / kChunk;
-    const int64_t clears = accumulate ? 0 : (static_cast<int64_t>(V) + kClearRows - 1) / kClearRows;
+    const int L = chunk_lanes(D);
+    const int64_t parts = (octets + L - 1) / L;
+    const int per_chunk = chunk_length(D, n);
+    const int64_t chunks = (n + per_chunk - 1) / per_chunk;
+    const int64_t sums = (chunks + kThreads / L - 1) / (kThreads / L) * parts;
+    constexpr int64_t per_group = kThreads / kWave * kClearRows;
+    const int64_t clears = accumulate ? 0 : (V + per_group - 1) / per_group;
     if (chunks + clears > 0) {
         with_float(grad_dtype, [&](auto a) {
             with_float(dtype, [&](auto b) {
                 using G = decltype(a);
                 using T = decltype(b);
-                k_grad_chunks<G, T><<<groups_for((chunks + clears) * parts, 1), threads, 0, s>>>(
+                k_grad_chunks<G, T><<<groups_for(sums + clears, 1), kThreads, 0, s>>>(
                     V, D, n, keys, pos, static_cast<const G *>(grad), grad_ld, scale, accumulate,
-                    static_cast<T *>(dtable), ld, w.head, w.tail, chunks, clears, parts);
+                    static_cast<T *>(dtable), ld, w.head, w.tail, per_chunk, L, sums, clears,
+                    parts);
             });
         });
         SPMV_HIP(hipGetLastError());
     }
     if (chunks > 1) {
-        const int64_t cols = (static_cast<int64_t>(D) + kWave - 1) / kWave;
+        const int64_t cols = (static_cast<int64_t>(D) + kJoinCols - 1) / kJoinCols;
         with_float(dtype, [&](auto b) {
             using T = decltype(b);
             k_grad_join<T><<<groups_for((chunks - 1) * cols, 1), kJoinThreads, 0, s>>>(
                 V, D, n, keys, scale, accumulate, static_cast<T *>(dtable), ld, w.head, w.tail,
-                chunks - 1, cols);
+                per_chunk, chunks - 1, cols);
         });
         SPMV_HIP(hipGetLastError());
     }
