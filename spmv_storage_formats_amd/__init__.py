@@ -21,6 +21,7 @@ Weight tables (fp32, fp16 and bf16; token ids int32 or int64):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import sys
@@ -493,7 +494,7 @@ def build_tuned(row_ptrs, col_idx, values, num_cols: int, *, formats=None, runs:
 
 _FLOATS = ("float32", "float16", "bfloat16")
 _IDS = ("int32", "int64")
-_codes = {}     # torch dtype -> spmv_dtype, filled by _kind
+_codes = {}     # (torch dtype, names allowed) -> spmv_dtype, filled by _kind
 
 
 def _kind(dtype, allowed, name):
@@ -507,36 +508,44 @@ def _kind(dtype, allowed, name):
     return hit
 
 
-def _rows(t, name, device, rows, cols):
-    """(pointer, row stride, spmv_dtype) of a cuda matrix [rows, cols] whose rows are
-    contiguous (rows None: any number)."""
+def _rows(t, name, index, rows, cols):
+    """A cuda matrix [rows, cols] whose rows are contiguous (rows None: any number), on
+    device `index` (None: any): (pointer, row stride, spmv_dtype, end of its memory)."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a cuda tensor")
     kind = _kind(t.dtype, _FLOATS, name)
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected "
                          f"({'any' if rows is None else rows}, {cols})")
+    n = shape[0]
     ld, step = t.stride()
-    if (step != 1 and cols > 1) or (ld < cols and t.shape[0] > 1):
+    if (step != 1 and cols > 1) or (ld < cols and n > 1):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return t.data_ptr() if t.numel() else None, ld, kind
+    if n == 0 or cols == 0:
+        return None, ld, kind, 0
+    p = t.data_ptr()
+    return p, ld, kind, p + ((n - 1) * ld + cols) * (2 if kind else 4)
 
 
-def _token_ids(ids, device=None):
-    """(pointer, count, spmv_dtype) of contiguous token ids of any shape."""
+def _token_ids(ids, index=None):
+    """(pointer, count, spmv_dtype, end) of contiguous token ids of any shape."""
     import torch
     if not isinstance(ids, torch.Tensor) or not ids.is_cuda:
         raise TypeError("ids must be a cuda tensor")
     kind = _kind(ids.dtype, _IDS, "ids")
-    if device is not None and ids.device != device:
-        raise ValueError(f"ids are on {ids.device}, expected {device}")
+    if index is not None and ids.get_device() != index:
+        raise ValueError(f"ids are on {ids.device}, expected cuda:{index}")
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
     n = ids.numel()
-    return ids.data_ptr() if n else None, n, kind
+    if n == 0:
+        return None, 0, kind, 0
+    p = ids.data_ptr()
+    return p, n, kind, p + n * (8 if kind == 4 else 4)
 
 
 def _apart(a, b, what):
@@ -557,30 +566,33 @@ def _apart(a, b, what):
 
 def _span(t):
     """Bytes from a tensor's first element to behind its last."""
-    if t.is_contiguous():
-        return t.numel() * t.element_size()
+    if t.numel() == 0:
+        return 0
     return t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
 
 
-def _on(device, stream, call, *made):
-    """call(stream handle) with `device` current.  Tensors in `made` were allocated
-    for the call on torch's current stream: where the work runs on another one,
-    their memory must not be reused before it is done."""
+def _stream_of(index, stream, *made):
+    """Stream handle for work on device `index` (the current device).  Tensors in `made`
+    were allocated for the call on torch's current stream: where the work runs on another
+    one, it waits for that stream, and their memory is not reused before it is done."""
     import torch
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            return _on(device, stream, call, *made)
-    current = torch.cuda.current_stream(device)
     if stream is None:
-        return call(current.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(index)
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    current = torch.cuda.current_stream(index)
     if made and handle != current.cuda_stream:
         other = (stream if isinstance(stream, torch.cuda.Stream)
-                 else torch.cuda.ExternalStream(handle, device=device))
+                 else torch.cuda.ExternalStream(handle, device=index))
         other.wait_stream(current)      # an allocation may still be in use there
         for t in made:
             t.record_stream(other)
-    return call(handle)
+    return handle
+
+
+def _elsewhere(index):
+    """Whether another device than `index` is current."""
+    import torch
+    return torch.cuda.current_device() != index
 
 
 class QuantHandle:
@@ -615,15 +627,21 @@ class QuantHandle:
         if x.dim() == 1 and y.dim() == 1:
             self.run(x[None], y[None], accumulate=accumulate, stream=stream)
             return y
-        n = y.shape[0] if y.dim() else 0
-        xp, x_ld, xk = _rows(x, "x", self.device, n, self.num_cols)
-        yp, y_ld, yk = _rows(y, "y", self.device, n, self.num_rows)
+        index = self.device.index
+        if _elsewhere(index):
+            import torch
+            with torch.cuda.device(index):
+                return self.run(x, y, accumulate=accumulate, stream=stream)
+        xp, x_ld, xk, xe = _rows(x, "x", index, None, self.num_cols)
+        n = x.shape[0]
+        yp, y_ld, yk, ye = _rows(y, "y", index, n, self.num_rows)
         if yk != xk and yk != 0:
             raise TypeError(f"y must be {x.dtype} or torch.float32, got {y.dtype}")
-        _apart(x, y, "x and y")
-        lib = load_library()
-        _check(_on(self.device, stream, lambda s: lib.spmv_quant_run(
-            ptr, n, xp, x_ld, xk, yp, y_ld, yk, 1 if accumulate else 0, s)), "spmv_quant_run")
+        if xe and ye and xp < ye and yp < xe:
+            _apart(x, y, "x and y")
+        _check(load_library().spmv_quant_run(ptr, n, xp, x_ld, xk, yp, y_ld, yk,
+                                             1 if accumulate else 0, _stream_of(index, stream)),
+               "spmv_quant_run")
         return y
 
     def lookup(self, ids, out=None, *, scale: float = 1.0, dtype=None, stream=None):
@@ -632,18 +650,23 @@ class QuantHandle:
         fp32 unless given)."""
         import torch
         ptr = self._live()
-        ip, n, ik = _token_ids(ids, self.device)
+        index = self.device.index
+        if _elsewhere(index):
+            with torch.cuda.device(index):
+                return self.lookup(ids, out, scale=scale, dtype=dtype, stream=stream)
+        ip, n, ik, ie = _token_ids(ids, index)
         made = ()
         if out is None:
             out = torch.empty((*ids.shape, self.num_cols), dtype=dtype or torch.float32,
                               device=self.device)
             made = (out,)
         flat = _by_token(out, ids, self.num_cols, "out", dtype)
-        op, ld, ok = _rows(flat, "out", self.device, n, self.num_cols)
-        _apart(ids, out, "ids and out")
-        lib = load_library()
-        _check(_on(self.device, stream, lambda s: lib.spmv_quant_lookup(
-            ptr, n, ip, ik, scale, op, ld, ok, s), *made), "spmv_quant_lookup")
+        op, ld, ok, oe = _rows(flat, "out", index, n, self.num_cols)
+        if ie and oe and ip < oe and op < ie:
+            _apart(ids, flat, "ids and out")
+        _check(load_library().spmv_quant_lookup(ptr, n, ip, ik, scale, op, ld, ok,
+                                                _stream_of(index, stream, *made)),
+               "spmv_quant_lookup")
         return out
 
     def array(self, name: str) -> np.ndarray:
@@ -712,14 +735,14 @@ def build_quant(weights, *, group_size: int = 128, zero_points: bool = False, sc
     if not isinstance(weights, torch.Tensor) or weights.dim() != 2:
         raise ValueError("weights must be a matrix")
     R, C = weights.shape
-    wp, ld, wk = _rows(weights, "weights", None, R, C)
+    wp, ld, wk, _ = _rows(weights, "weights", None, R, C)
     scale_dtype = scale_dtype or weights.dtype
     sk = _kind(scale_dtype, _FLOATS, "scale_dtype")
-    lib = load_library()
     out = ctypes.c_void_p()
-    _check(_on(weights.device, stream, lambda s: lib.spmv_quant_build(
-        ctypes.byref(out), R, C, int(group_size), 1 if zero_points else 0, sk, wp, ld, wk, s)),
-        "spmv_quant_build")
+    with torch.cuda.device(weights.device):
+        _check(load_library().spmv_quant_build(
+            ctypes.byref(out), R, C, int(group_size), 1 if zero_points else 0, sk, wp, ld, wk,
+            _stream_of(weights.get_device(), stream)), "spmv_quant_build")
     return QuantHandle(out.value, weights.device, scale_dtype)
 
 
@@ -744,11 +767,11 @@ def build_quant_packed(codes, scales, num_cols: int, *, group_size: int = 128, z
         if t is not None and (tuple(t.shape) != shape or t.device != codes.device):
             raise ValueError(f"{name} must be {shape} on {codes.device}, got "
                              f"{tuple(t.shape)} on {t.device}")
-    lib = load_library()
     out = ctypes.c_void_p()
-    _check(_on(codes.device, stream, lambda s: lib.spmv_quant_build_packed(
-        ctypes.byref(out), R, num_cols, group_size, cp, sp, sk, zp, 1 if validate else 0, s)),
-        "spmv_quant_build_packed")
+    with torch.cuda.device(codes.device):
+        _check(load_library().spmv_quant_build_packed(
+            ctypes.byref(out), R, num_cols, group_size, cp, sp, sk, zp, 1 if validate else 0,
+            _stream_of(codes.get_device(), stream)), "spmv_quant_build_packed")
     return QuantHandle(out.value, codes.device, scales.dtype)
 
 
@@ -760,31 +783,39 @@ def lookup(table, ids, out=None, *, scale: float = 1.0, dtype=None, stream=None)
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be a matrix")
     V, D = table.shape
-    tp, t_ld, tk = _rows(table, "table", None, V, D)
-    device = table.device
-    ip, n, ik = _token_ids(ids, device)
+    tp, t_ld, tk, te = _rows(table, "table", None, V, D)
+    index = table.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return lookup(table, ids, out, scale=scale, dtype=dtype, stream=stream)
+    ip, n, ik, ie = _token_ids(ids, index)
     made = ()
     if out is None:
-        out = torch.empty((*ids.shape, D), dtype=dtype or table.dtype, device=device)
+        out = torch.empty((*ids.shape, D), dtype=dtype or table.dtype, device=table.device)
         made = (out,)
     flat = _by_token(out, ids, D, "out", dtype)
-    op, o_ld, ok = _rows(flat, "out", device, n, D)
+    op, o_ld, ok, oe = _rows(flat, "out", index, n, D)
     if not made:
-        _apart(table, out, "table and out")
-        _apart(ids, out, "ids and out")
-    lib = load_library()
-    _check(_on(device, stream, lambda s: lib.spmv_lookup(
-        V, D, tp, t_ld, tk, n, ip, ik, scale, op, o_ld, ok, s), *made), "spmv_lookup")
+        if te and oe and tp < oe and op < te:
+            _apart(table, flat, "table and out")
+        if ie and oe and ip < oe and op < ie:
+            _apart(ids, flat, "ids and out")
+    _check(load_library().spmv_lookup(V, D, tp, t_ld, tk, n, ip, ik, scale, op, o_ld, ok,
+                                      _stream_of(index, stream, *made)), "spmv_lookup")
     return out
 
 
 def lookup_grad_workspace(num_tokens: int, num_rows: int, num_cols: int) -> int:
     """Bytes of workspace that lookup_grad needs for these sizes."""
-    n = ctypes.c_size_t()
-    _check(load_library().spmv_lookup_grad_workspace(num_rows, num_cols, num_tokens,
-                                                     ctypes.byref(n)),
+    return _workspace_bytes(int(num_tokens), int(num_rows), int(num_cols))
+
+
+@functools.lru_cache(maxsize=64)
+def _workspace_bytes(n, rows, cols):
+    size = ctypes.c_size_t()
+    _check(load_library().spmv_lookup_grad_workspace(rows, cols, n, ctypes.byref(size)),
            "spmv_lookup_grad_workspace")
-    return n.value
+    return size.value
 
 
 def lookup_grad(grad, ids, num_rows: int, out=None, *, scale: float = 1.0,
@@ -799,37 +830,39 @@ def lookup_grad(grad, ids, num_rows: int, out=None, *, scale: float = 1.0,
     num_rows = int(num_rows)
     if not isinstance(grad, torch.Tensor) or not grad.is_cuda or grad.dim() < 1:
         raise TypeError("grad must be a cuda tensor")
-    device, D = grad.device, grad.shape[-1]
-    ip, n, ik = _token_ids(ids, device)
-    flat = _by_token(grad, ids, D, "grad")
-    gp, g_ld, gk = _rows(flat, "grad", device, n, D)
+    index, D = grad.get_device(), grad.shape[-1]
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return lookup_grad(grad, ids, num_rows, out, scale=scale, accumulate=accumulate,
+                               dtype=dtype, workspace=workspace, stream=stream)
+    ip, n, ik, ie = _token_ids(ids, index)
+    gp, g_ld, gk, ge = _rows(_by_token(grad, ids, D, "grad"), "grad", index, n, D)
     if num_rows < 0:
         raise ValueError("num_rows must not be negative")
     made = []
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty(num_rows, D, dtype=dtype or grad.dtype, device=device)
+        out = torch.empty(num_rows, D, dtype=dtype or grad.dtype, device=grad.device)
         made.append(out)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out is {out.dtype}, dtype says {dtype}")
-    op, o_ld, ok = _rows(out, "out", device, num_rows, D)
+    op, o_ld, ok, oe = _rows(out, "out", index, num_rows, D)
     if not made:
         _apart(grad, out, "grad and out")
         _apart(ids, out, "ids and out")
-    need = lookup_grad_workspace(n, num_rows, D)
+    need = _workspace_bytes(n, num_rows, D)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=grad.device)
         made.append(workspace)
     else:
-        _apart(workspace, out, "workspace and out")
-        _apart(workspace, grad, "workspace and grad")
-        _apart(workspace, ids, "workspace and ids")
+        for t, name in ((out, "out"), (grad, "grad"), (ids, "ids")):
+            _apart(workspace, t, f"workspace and {name}")
     wp = _dev(workspace, torch.uint8, "workspace")
-    if workspace.numel() < need or workspace.device != device:
-        raise ValueError(f"workspace must hold {need} bytes on {device}")
-    lib = load_library()
-    _check(_on(device, stream, lambda s: lib.spmv_lookup_grad(
+    size = workspace.numel()
+    if size < need or workspace.get_device() != index:
+        raise ValueError(f"workspace must hold {need} bytes on cuda:{index}")
+    _check(load_library().spmv_lookup_grad(
         num_rows, D, n, ip, ik, gp, g_ld, gk, scale, 1 if accumulate else 0, op, o_ld, ok, wp,
-        workspace.numel(), s), *made), "spmv_lookup_grad")
+        size, _stream_of(index, stream, *made)), "spmv_lookup_grad")
     return out
