@@ -552,11 +552,17 @@ spmv_status spmv_quant_build_packed(spmv_quant **out, int32_t num_rows, int32_t 
  * vectors: row v of x_dev [n, C] gives row v of y_dev [n, R].
  *   y_dtype is x_dtype or SPMV_FP32.  Products of fp32 vectors keep all 24 bits
  *   of x.  Infinities and NaN in x reach exactly the vectors that hold them.
+ *   workspace_dev: at least spmv_quant_run_workspace() bytes, 16-byte aligned
+ *   (none for few vectors), used until the work on `stream` is done; calls that
+ *   may overlap in time need workspaces of their own.
  *   Must be called on the handle's device (SPMV_ERR_DEVICE).
  */
+spmv_status spmv_quant_run_workspace(const spmv_quant *q, int32_t n, spmv_dtype x_dtype,
+                                     size_t *bytes);
 spmv_status spmv_quant_run(const spmv_quant *q, int32_t n, const void *x_dev, int64_t x_ld,
                            spmv_dtype x_dtype, void *y_dev, int64_t y_ld, spmv_dtype y_dtype,
-                           int32_t accumulate, void *stream);
+                           int32_t accumulate, void *workspace_dev, size_t workspace_bytes,
+                           void *stream);
 
 /* spmv_quant_lookup -- as spmv_lookup, the table being the 4-bit matrix
  * (num_rows = R rows of C columns).  Must be called on the handle's device. */

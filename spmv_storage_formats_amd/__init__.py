@@ -176,8 +176,10 @@ def load_library():
                                                 _vp, _i64, ctypes.c_int, _vp]),
             "spmv_quant_build_packed": (ctypes.c_int, [P(_vp), _i32, _i32, _i32, _vp, _vp,
                                                        ctypes.c_int, _vp, _i32, _vp]),
+            "spmv_quant_run_workspace": (ctypes.c_int, [_vp, _i32, ctypes.c_int,
+                                                        P(ctypes.c_size_t)]),
             "spmv_quant_run": (ctypes.c_int, [_vp, _i32, _vp, _i64, ctypes.c_int, _vp, _i64,
-                                              ctypes.c_int, _i32, _vp]),
+                                              ctypes.c_int, _i32, _vp, ctypes.c_size_t, _vp]),
             "spmv_quant_lookup": (ctypes.c_int, [_vp, _i64, _vp, ctypes.c_int, ctypes.c_float,
                                                  _vp, _i64, ctypes.c_int, _vp]),
             "spmv_quant_get_info": (ctypes.c_int, [_vp, P(_QuantInfo)]),
@@ -589,6 +591,16 @@ def _stream_of(index, stream, *made):
     return handle
 
 
+def _workspace(t, need, index):
+    """(pointer, bytes) of a contiguous uint8 cuda tensor of at least `need` bytes."""
+    import torch
+    p = _dev(t, torch.uint8, "workspace")
+    size = t.numel()
+    if size < need or t.get_device() != index or (p or 0) % 16:
+        raise ValueError(f"workspace must hold {need} bytes on cuda:{index}, 16-byte aligned")
+    return p, size
+
+
 def _elsewhere(index):
     """Whether another device than `index` is current."""
     import torch
@@ -613,25 +625,42 @@ class QuantHandle:
         self.num_rows = info.num_rows
         self.num_cols = info.num_cols
         self.group_size = info.group_size
+        self._need = {}     # (vectors, spmv_dtype) -> bytes of workspace
 
     def _live(self):
         if self._ptr is None:
             raise RuntimeError("handle destroyed")
         return self._ptr
 
-    def run(self, x, y, *, accumulate: bool = True, stream=None):
+    def run_workspace(self, n: int, dtype) -> int:
+        """Bytes of workspace that run needs for n vectors of `dtype` (0 for few)."""
+        kind = _kind(dtype, _FLOATS, "dtype")
+        hit = self._need.get((n, kind))
+        if hit is None:
+            size = ctypes.c_size_t()
+            _check(load_library().spmv_quant_run_workspace(self._live(), n, kind,
+                                                           ctypes.byref(size)),
+                   "spmv_quant_run_workspace")
+            hit = self._need[(n, kind)] = size.value
+        return hit
+
+    def run(self, x, y, *, accumulate: bool = True, workspace=None, stream=None):
         """y <- W x + y (accumulate) or y <- W x, enqueued on `stream` (default: torch's
         current stream).  x [C] and y [R], or x [n, C] and y [n, R] for n vectors; y of
-        x's type or fp32."""
+        x's type or fp32.  `workspace`: a contiguous uint8 cuda tensor of at least
+        run_workspace() bytes, for this call alone until its work is done (default:
+        allocated for the call where it needs one)."""
         ptr = self._live()
         if x.dim() == 1 and y.dim() == 1:
-            self.run(x[None], y[None], accumulate=accumulate, stream=stream)
+            self.run(x[None], y[None], accumulate=accumulate, workspace=workspace,
+                     stream=stream)
             return y
         index = self.device.index
         if _elsewhere(index):
             import torch
             with torch.cuda.device(index):
-                return self.run(x, y, accumulate=accumulate, stream=stream)
+                return self.run(x, y, accumulate=accumulate, workspace=workspace,
+                                stream=stream)
         xp, x_ld, xk, xe = _rows(x, "x", index, None, self.num_cols)
         n = x.shape[0]
         yp, y_ld, yk, ye = _rows(y, "y", index, n, self.num_rows)
@@ -639,8 +668,20 @@ class QuantHandle:
             raise TypeError(f"y must be {x.dtype} or torch.float32, got {y.dtype}")
         if xe and ye and xp < ye and yp < xe:
             _apart(x, y, "x and y")
+        need = self.run_workspace(n, x.dtype)
+        wp, size, made = None, 0, ()
+        if need:
+            if workspace is None:
+                import torch
+                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+                made = (workspace,)
+            else:
+                _apart(workspace, x, "workspace and x")
+                _apart(workspace, y, "workspace and y")
+            wp, size = _workspace(workspace, need, index)
         _check(load_library().spmv_quant_run(ptr, n, xp, x_ld, xk, yp, y_ld, yk,
-                                             1 if accumulate else 0, _stream_of(index, stream)),
+                                             1 if accumulate else 0, wp, size,
+                                             _stream_of(index, stream, *made)),
                "spmv_quant_run")
         return y
 
@@ -858,10 +899,7 @@ def lookup_grad(grad, ids, num_rows: int, out=None, *, scale: float = 1.0,
     else:
         for t, name in ((out, "out"), (grad, "grad"), (ids, "ids")):
             _apart(workspace, t, f"workspace and {name}")
-    wp = _dev(workspace, torch.uint8, "workspace")
-    size = workspace.numel()
-    if size < need or workspace.get_device() != index:
-        raise ValueError(f"workspace must hold {need} bytes on cuda:{index}")
+    wp, size = _workspace(workspace, need, index)
     _check(load_library().spmv_lookup_grad(
         num_rows, D, n, ip, ik, gp, g_ld, gk, scale, 1 if accumulate else 0, op, o_ld, ok, wp,
         size, _stream_of(index, stream, *made)), "spmv_lookup_grad")

@@ -16,10 +16,6 @@ __device__ inline int64_t word_index(int32_t r, int32_t octet, int32_t blocks) {
     return block * kQuantBlockWords + quant_word(r % kQuantRows, octet % kQuantOctets);
 }
 
-__device__ inline int64_t scale_index(int32_t r, int32_t g, int32_t groups_pad) {
-    return (static_cast<int64_t>(r / kQuantRows) * groups_pad + g) * kQuantRows + r % kQuantRows;
-}
-
 // rne(w / s) with the quotient taken exactly, s > 0.  k = rint of the rounded
 // quotient is off by at most one; w - k s is exact in one fused operation
 // (a multiple of both operands' last places, below s in size), so comparing
@@ -37,7 +33,7 @@ __device__ inline float rne_quotient(float w, float s) {
 // read of the weights comes from the cache).
 template <typename T, typename S>
 __global__ __launch_bounds__(kThreads) void k_quant_build(
-    int32_t R, int32_t C, int32_t group, int32_t groups, int32_t groups_pad, int32_t blocks,
+    int32_t R, int32_t C, int32_t group, int32_t groups, int32_t set, int32_t sets, int32_t blocks,
     int L, const T *__restrict__ w, int64_t ld, uint32_t *__restrict__ codes,
     S *__restrict__ scales, uint8_t *__restrict__ zeros, int *__restrict__ flag) {
     const int per_block = kThreads / L;
@@ -80,8 +76,8 @@ __global__ __launch_bounds__(kThreads) void k_quant_build(
         float z = 8.f;
         if (zeros) z = s > 0.f ? fminf(rne_quotient(-lo, s), 15.f) : 0.f;
         if (live && sub == 0) {
-            scales[scale_index(r, g, groups_pad)] = static_cast<S>(s);
-            if (zeros) zeros[scale_index(r, g, groups_pad)] = static_cast<uint8_t>(z);
+            scales[quant_scale_at(r, g, set, sets)] = static_cast<S>(s);
+            if (zeros) zeros[quant_zero_at(r, g, set, sets)] = static_cast<uint8_t>(z);
         }
         for (int o = sub; o < octets; o += L) {
             float v[8];
@@ -123,18 +119,18 @@ __global__ __launch_bounds__(kThreads) void k_quant_pack(int32_t R, int32_t C, i
 
 template <typename S>
 __global__ __launch_bounds__(kThreads) void k_quant_scales(
-    int32_t R, int32_t groups, int32_t groups_pad, int check, const S *__restrict__ scales_in,
-    const uint8_t *__restrict__ zeros_in, S *__restrict__ scales, uint8_t *__restrict__ zeros,
-    int *__restrict__ flag) {
+    int32_t R, int32_t groups, int32_t set, int32_t sets, int check,
+    const S *__restrict__ scales_in, const uint8_t *__restrict__ zeros_in,
+    S *__restrict__ scales, uint8_t *__restrict__ zeros, int *__restrict__ flag) {
     EACH_ITEM(i, static_cast<int64_t>(R) * groups) {
         const int32_t r = static_cast<int32_t>(i / groups), g = static_cast<int32_t>(i % groups);
         const S s = scales_in[i];
         bool bad = !(fabsf(static_cast<float>(s)) <= 3.402823466e38f);
-        scales[scale_index(r, g, groups_pad)] = s;
+        scales[quant_scale_at(r, g, set, sets)] = s;
         if (zeros_in) {
             const uint8_t z = zeros_in[i];
             bad |= z > 15;
-            zeros[scale_index(r, g, groups_pad)] = z & 15;
+            zeros[quant_zero_at(r, g, set, sets)] = z & 15;
         }
         if (check && bad) atomicOr(flag, 1);
     }
@@ -154,12 +150,15 @@ __global__ __launch_bounds__(kThreads) void k_quant_unpack(int32_t R, int32_t C,
     }
 }
 
-template <typename S>
-__global__ __launch_bounds__(kThreads) void k_quant_unpack_groups(
-    int32_t R, int32_t groups, int32_t groups_pad, const S *__restrict__ in, S *__restrict__ out) {
+template <typename S, bool Zeros>
+__global__ __launch_bounds__(kThreads) void k_quant_unpack_groups(int32_t R, int32_t groups,
+                                                                  int32_t set, int32_t sets,
+                                                                  const S *__restrict__ in,
+                                                                  S *__restrict__ out) {
     EACH_ITEM(i, static_cast<int64_t>(R) * groups) {
-        out[i] = in[scale_index(static_cast<int32_t>(i / groups), static_cast<int32_t>(i % groups),
-                                groups_pad)];
+        const int64_t r = i / groups;
+        const int32_t g = static_cast<int32_t>(i % groups);
+        out[i] = in[Zeros ? quant_zero_at(r, g, set, sets) : quant_scale_at(r, g, set, sets)];
     }
 }
 
@@ -167,7 +166,7 @@ __global__ __launch_bounds__(kThreads) void k_quant_unpack_groups(
 // (one word, eight values, one 16- or 32-byte store) each per step.
 template <typename S, typename T, typename I>
 __global__ __launch_bounds__(kThreads) void k_quant_lookup(
-    int32_t R, int32_t C, int32_t group, int32_t groups_pad, int32_t blocks, int L,
+    int32_t R, int32_t C, int32_t group, int32_t set, int32_t sets, int32_t blocks, int L,
     const uint32_t *__restrict__ codes, const S *__restrict__ scales,
     const uint8_t *__restrict__ zeros, int64_t n, const I *__restrict__ ids, float scale,
     T *__restrict__ out, int64_t ld) {
@@ -183,9 +182,10 @@ __global__ __launch_bounds__(kThreads) void k_quant_lookup(
             float v[8];
             if (there) {
                 const uint32_t w = codes[word_index(r, o, blocks)];
-                const int64_t si = scale_index(r, o * 8 / group, groups_pad);
-                const float s = static_cast<float>(scales[si]);
-                const float z = zeros ? static_cast<float>(zeros[si]) : 8.f;
+                const int32_t g = o * 8 / group;
+                const float s = static_cast<float>(scales[quant_scale_at(r, g, set, sets)]);
+                const float z =
+                    zeros ? static_cast<float>(zeros[quant_zero_at(r, g, set, sets)]) : 8.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     v[e] = (static_cast<float>(quant_code(w, e)) - z) * s * scale;
@@ -214,7 +214,7 @@ spmv_status quant_fill_dense(spmv_quant *q, const void *w, int64_t ld, int32_t d
             using T = decltype(t);
             using S = decltype(sc);
             k_quant_build<T, S><<<grid, kThreads, 0, s>>>(
-                q->R, q->C, q->group, q->groups, q->groups_pad, q->blocks, L,
+                q->R, q->C, q->group, q->groups, q->set, q->sets, q->blocks, L,
                 static_cast<const T *>(w), ld, q->codes, static_cast<S *>(q->scales), q->zeros,
                 flag);
         });
@@ -235,7 +235,7 @@ spmv_status quant_fill_packed(spmv_quant *q, const uint8_t *codes, const void *s
     with_float(q->scale_dtype, [&](auto sc) {
         using S = decltype(sc);
         k_quant_scales<S><<<groups_for(items, kThreads), kThreads, 0, s>>>(
-            q->R, q->groups, q->groups_pad, validate, static_cast<const S *>(scales), zeros,
+            q->R, q->groups, q->set, q->sets, validate, static_cast<const S *>(scales), zeros,
             static_cast<S *>(q->scales), q->zeros, flag);
     });
     SPMV_HIP(hipGetLastError());
@@ -249,13 +249,13 @@ spmv_status quant_unpack(const spmv_quant *q, spmv_quant_array which, void *dst,
         k_quant_unpack<<<groups_for(bytes, kThreads), kThreads, 0, s>>>(
             q->R, q->C, q->blocks, q->codes, static_cast<uint8_t *>(dst));
     } else if (which == SPMV_Q_ZEROS) {
-        k_quant_unpack_groups<uint8_t><<<groups_for(items, kThreads), kThreads, 0, s>>>(
-            q->R, q->groups, q->groups_pad, q->zeros, static_cast<uint8_t *>(dst));
+        k_quant_unpack_groups<uint8_t, true><<<groups_for(items, kThreads), kThreads, 0, s>>>(
+            q->R, q->groups, q->set, q->sets, q->zeros, static_cast<uint8_t *>(dst));
     } else {
         with_float(q->scale_dtype, [&](auto sc) {
             using S = decltype(sc);
-            k_quant_unpack_groups<S><<<groups_for(items, kThreads), kThreads, 0, s>>>(
-                q->R, q->groups, q->groups_pad, static_cast<const S *>(q->scales),
+            k_quant_unpack_groups<S, false><<<groups_for(items, kThreads), kThreads, 0, s>>>(
+                q->R, q->groups, q->set, q->sets, static_cast<const S *>(q->scales),
                 static_cast<S *>(dst));
         });
     }
@@ -273,12 +273,12 @@ spmv_status quant_lookup(const spmv_quant *q, int64_t n, const void *ids, int32_
             using T = decltype(t);
             if (id_dtype == SPMV_INT64)
                 k_quant_lookup<S, T, int64_t><<<grid, kThreads, 0, s>>>(
-                    q->R, q->C, q->group, q->groups_pad, q->blocks, L, q->codes,
+                    q->R, q->C, q->group, q->set, q->sets, q->blocks, L, q->codes,
                     static_cast<const S *>(q->scales), q->zeros, n,
                     static_cast<const int64_t *>(ids), scale, static_cast<T *>(out), ld);
             else
                 k_quant_lookup<S, T, int32_t><<<grid, kThreads, 0, s>>>(
-                    q->R, q->C, q->group, q->groups_pad, q->blocks, L, q->codes,
+                    q->R, q->C, q->group, q->set, q->sets, q->blocks, L, q->codes,
                     static_cast<const S *>(q->scales), q->zeros, n,
                     static_cast<const int32_t *>(ids), scale, static_cast<T *>(out), ld);
         });

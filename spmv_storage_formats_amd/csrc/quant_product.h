@@ -7,7 +7,7 @@
 namespace spmv {
 
 struct QuantArgs {
-    int32_t R, C, n, blocks, group, groups_pad;
+    int32_t R, C, n, blocks, group, set, sets;
     const uint32_t *codes;
     const void *scales;
     const uint8_t *zeros;
@@ -18,8 +18,18 @@ struct QuantArgs {
     int32_t accumulate;
     int32_t y_fp32;
     int32_t passes;       // groups of vectors
+    int32_t splits;       // parts of the columns, each a workgroup's (wide products)
+    float *partial;       // their sums [splits][n][R], where there are several
     int32_t group_shift;  // log2 of the group, or -1
 };
+
+// Matrix-unit columns of one pass over n vectors of `parts` columns each: at
+// most 48, the passes even.
+inline int64_t wide_columns(int32_t n, int parts) {
+    const int64_t vecs = 48 / parts;
+    const int64_t passes = (n + vecs - 1) / vecs;
+    return (n + passes - 1) / passes * parts;
+}
 
 void quant_run_fp32(const QuantArgs &a, int32_t scale_dtype, hipStream_t s);
 void quant_run_fp16(const QuantArgs &a, int32_t scale_dtype, hipStream_t s);
@@ -120,21 +130,23 @@ __device__ float plain_dot(const QuantArgs &a, int32_t r, int32_t v) {
         const uint32_t w =
             a.codes[(tile * a.blocks + o / kQuantOctets) * kQuantBlockWords +
                     quant_word(r % kQuantRows, o % kQuantOctets)];
-        const int64_t si = (tile * a.groups_pad + c / a.group) * kQuantRows + r % kQuantRows;
-        const float s = static_cast<float>(static_cast<const S *>(a.scales)[si]);
-        const float z = a.zeros ? static_cast<float>(a.zeros[si]) : 8.f;
+        const int32_t g = c / a.group;
+        const float s = static_cast<float>(
+            static_cast<const S *>(a.scales)[quant_scale_at(r, g, a.set, a.sets)]);
+        const float z =
+            a.zeros ? static_cast<float>(a.zeros[quant_zero_at(r, g, a.set, a.sets)]) : 8.f;
         sum = fmaf((static_cast<float>(quant_code(w, c & 7)) - z) * s, static_cast<float>(x[c]),
                    sum);
     }
     return sum;
 }
 
-// Four scales as they are loaded (8 or 16 bytes).
-template <typename S>
-struct alignas(8) ScaleQuad {
-    uint32_t raw[2];
-    __device__ inline float get(int i) const {
-        const uint32_t w = raw[i / 2];
+// The scales of four rows and N groups as they are loaded.
+template <typename S, int N>
+struct alignas(N == 1 ? 8 : 16) Scales {
+    uint32_t raw[2 * N];
+    __device__ inline float get(int g, int i) const {
+        const uint32_t w = raw[2 * g + i / 2];
         if constexpr (std::is_same_v<S, bf16>)
             return __builtin_bit_cast(float, i % 2 ? w & 0xffff0000u : w << 16);
         else
@@ -142,25 +154,136 @@ struct alignas(8) ScaleQuad {
                 __builtin_bit_cast(f16, static_cast<uint16_t>(i % 2 ? w >> 16 : w)));
     }
 };
-template <>
-struct alignas(16) ScaleQuad<float> {
-    float raw[4];
-    __device__ inline float get(int i) const { return raw[i]; }
+template <int N>
+struct alignas(16) Scales<float, N> {
+    float raw[4 * N];
+    __device__ inline float get(int g, int i) const { return raw[4 * g + i]; }
 };
+
+// The zero points of one row and N groups: bytes, loaded whole.
+template <int N>
+__device__ inline uint32_t load_zeros(const char *p) {
+    if constexpr (N == 4) return *reinterpret_cast<const uint32_t *>(p);
+    if constexpr (N == 2) return *reinterpret_cast<const uint16_t *>(p);
+    return *reinterpret_cast<const uint8_t *>(p);
+}
 
 // What a wave loads for one block of 128 columns: RT tiles' codes, scales and
 // zero points, and its share of the vectors.
 template <typename X, typename S, int GS, int RT, int NX>
 struct Block {
     u32x4 code[RT];
-    ScaleQuad<S> scale[RT][128 / GS];
-    uint32_t zero[RT][128 / GS];
+    Scales<S, 128 / GS> scale[RT];
+    uint32_t zero[RT];
     XOctet<X> x[NX];
 };
 
 // Bytes between the columns of a block's vectors in LDS: 128 elements and a
 // gap that spreads eight lanes' 16-byte reads over all banks.
 constexpr int kColBytes = 256 + 16;
+
+// What both kernels below do with a block, a lane at a time.
+template <typename X, typename S, bool Z, int GS>
+struct Lane {
+    using U = Unit<X>;
+    static constexpr int kScales = 128 / GS;  // scales per block and row
+    int r16, quad;
+    uint32_t code_at, scale_at, zero_at;  // this lane's bytes in a block's data
+    uint32_t sixteen = U::kSixteen, mask = U::kMask;
+
+    __device__ inline explicit Lane(int lane) : r16(lane % 16), quad(lane / 16) {
+        code_at = quant_word(r16, quad) * 4;
+        scale_at = quad * 4 * kScales * sizeof(S);
+        zero_at = r16 * kScales;
+        asm("" : "+v"(sixteen));  // one operand of v_and_or_b32 in a VGPR, the other in an SGPR
+        asm("" : "+s"(mask));
+    }
+
+    // Codes, scales and zero points of RT tiles: a uniform address, then the lane's bytes.
+    template <int RT, int NX>
+    __device__ inline void load(const QuantArgs &a, const int64_t *tile, int block,
+                                Block<X, S, GS, RT, NX> &b) const {
+        const int set = GS < 128 ? block
+                        : a.group_shift >= 0 ? block >> (a.group_shift - 7)
+                                             : block / (a.group >> 7);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            const char *codes = reinterpret_cast<const char *>(
+                a.codes + (tile[t] * a.blocks + block) * kQuantBlockWords);
+            b.code[t] = *reinterpret_cast<const u32x4 *>(codes + code_at);
+            const int64_t s = (tile[t] * a.sets + set) * (kQuantRows * kScales);
+            const char *scales = static_cast<const char *>(a.scales) + s * sizeof(S);
+            b.scale[t] = *reinterpret_cast<const Scales<S, kScales> *>(scales + scale_at);
+            b.zero[t] = 0x08080808u;
+            if constexpr (Z)
+                b.zero[t] =
+                    load_zeros<kScales>(reinterpret_cast<const char *>(a.zeros + s) + zero_at);
+        }
+    }
+
+    // y += the block's matrix times the vectors that lie in LDS at x.
+    template <int RT, int NX, int NT>
+    __device__ inline void multiply(const Block<X, S, GS, RT, NX> &s, const char *x,
+                                    f32x4 (&y)[RT][NT]) const {
+#pragma unroll
+        for (int g = 0; g < kScales; ++g) {
+            f32x4 acc[RT][NT];
+            u32x4 off[RT];
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                // -(16 + zero) in both halves
+                const uint32_t z = (s.zero[t] >> (8 * g)) & 15u;
+                const uint32_t o = (z * U::kStep) | (U::kSixteen | 0x80008000u);
+                off[t] = u32x4{o, o, o, o};
+            }
+#pragma unroll
+            for (int jj = 0; jj < GS / 32; ++jj) {
+                const int j = g * (GS / 32) + jj;
+                u32x4 b[NT];
+#pragma unroll
+                for (int u = 0; u < NT; ++u)
+                    b[u] = *reinterpret_cast<const u32x4 *>(x + (u * 16 + r16) * kColBytes +
+                                                            j * 64 + quad * 16);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    u32x4 q;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        q[i] = (U::pair(s.code[t][j], i) & mask) | sixteen;
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) {
+                        acc[t][u] =
+                            U::mfma(off[t], b[u], jj == 0 ? f32x4{0, 0, 0, 0} : acc[t][u]);
+                        acc[t][u] = U::mfma(q, b[u], acc[t][u]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int u = 0; u < NT; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        y[t][u][i] = fmaf(s.scale[t].get(g, i), acc[t][u][i], y[t][u][i]);
+        }
+    }
+};
+
+// The product's element (r, v) to memory.  Infinities among the moved codes'
+// products cancel to NaN, and moved codes may pass the range where the codes
+// do not: such an element is computed plainly.
+template <typename X, typename S>
+__device__ inline void put_element(const QuantArgs &a, int64_t r, int32_t v, float sum) {
+    if (!(fabsf(sum) <= 3.402823466e38f)) sum = plain_dot<X, S>(a, static_cast<int32_t>(r), v);
+    const int64_t to = v * a.y_ld + r;
+    if (a.y_fp32) {
+        float *p = static_cast<float *>(a.y) + to;
+        *p = a.accumulate ? sum + *p : sum;
+    } else {
+        X *p = static_cast<X *>(a.y) + to;
+        *p = static_cast<X>(a.accumulate ? sum + static_cast<float>(*p) : sum);
+    }
+}
 
 // A workgroup takes RT tiles of 16 rows and NC columns (vectors, or parts of
 // fp32 vectors); its W waves take every W-th block of 128 matrix columns and
@@ -173,21 +296,16 @@ __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
     constexpr int NT = (NC + 15) / 16;
     constexpr int kVecs = NC / U::kParts;       // vectors per pass
     constexpr int NX = (kVecs + 3) / 4;         // octets of them per lane and block
-    constexpr int kScales = 128 / GS;           // scales per block and row
     constexpr int kWaveBytes = NT * 16 * kColBytes;
     static_assert(kWaveBytes >= NT * 4 * kWave * 4, "the sums reuse the vectors' part");
     __shared__ __attribute__((aligned(16))) char lds[W * kWaveBytes];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int r16 = lane % 16, quad = lane / 16;
-    const uint32_t code_lane = quant_word(r16, quad) * 4;
-    const uint32_t scale_lane = quad * 4 * sizeof(S);
+    const Lane<X, S, Z, GS> me(lane);
+    const int r16 = me.r16, quad = me.quad;
     char *const mine = lds + wave * kWaveBytes;
     const int64_t row_groups = (static_cast<int64_t>(a.R) + RT * 16 - 1) / (RT * 16);
     const int64_t last_tile = (static_cast<int64_t>(a.R) - 1) / 16;
-    uint32_t sixteen = U::kSixteen, mask = U::kMask;
-    asm("" : "+v"(sixteen));  // one operand of v_and_or_b32 in a VGPR, the other in an SGPR
-    asm("" : "+s"(mask));
     for (int64_t item = blockIdx.x; item < row_groups * a.passes; item += gridDim.x) {
         const int64_t tile0 = (item % row_groups) * RT;
         const int32_t v0 = static_cast<int32_t>(item / row_groups) * kVecs;
@@ -211,30 +329,6 @@ __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
             for (int u = 0; u < NT; ++u) y[t][u] = f32x4{0, 0, 0, 0};
 
         using B = Block<X, S, GS, RT, NX>;
-        // uniform address, then this lane's bytes
-        auto at = [](const void *p, int64_t bytes, uint32_t lane_bytes) {
-            return static_cast<const char *>(p) + bytes + lane_bytes;
-        };
-        auto load = [&](B &b, int block) {
-            const int g0 = GS < 128 ? block * kScales
-                           : a.group_shift >= 0 ? block >> (a.group_shift - 7)
-                                                : block / (a.group >> 7);
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                const int64_t word = (tile[t] * a.blocks + block) * kQuantBlockWords;
-                b.code[t] = *reinterpret_cast<const u32x4 *>(at(a.codes, word * 4, code_lane));
-                const int64_t g = (tile[t] * a.groups_pad + g0) * kQuantRows;
-#pragma unroll
-                for (int i = 0; i < kScales; ++i) {
-                    b.scale[t][i] = *reinterpret_cast<const ScaleQuad<S> *>(
-                        at(a.scales, (g + i * kQuantRows) * sizeof(S), scale_lane));
-                    b.zero[t][i] = 8;
-                    if constexpr (Z)
-                        b.zero[t][i] = *reinterpret_cast<const uint8_t *>(
-                            at(a.zeros, g + i * kQuantRows, r16));
-                }
-            }
-        };
         // The vectors' octets to LDS: octet r16 of vector i * 4 + quad.
         auto stage = [&](const B &b) {
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -252,66 +346,24 @@ __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         };
-        auto compute = [&](const B &s) {
-#pragma unroll
-            for (int g = 0; g < kScales; ++g) {
-                f32x4 acc[RT][NT];
-                u32x4 off[RT];
-#pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    // -(16 + zero) in both halves
-                    const uint32_t o = (s.zero[t][g] * U::kStep) | (U::kSixteen | 0x80008000u);
-                    off[t] = u32x4{o, o, o, o};
-                }
-#pragma unroll
-                for (int jj = 0; jj < GS / 32; ++jj) {
-                    const int j = g * (GS / 32) + jj;
-                    u32x4 b[NT];
-#pragma unroll
-                    for (int u = 0; u < NT; ++u)
-                        b[u] = *reinterpret_cast<const u32x4 *>(
-                            mine + (u * 16 + r16) * kColBytes + j * 64 + quad * 16);
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) {
-                        u32x4 q;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            q[i] = (U::pair(s.code[t][j], i) & mask) | sixteen;
-#pragma unroll
-                        for (int u = 0; u < NT; ++u) {
-                            acc[t][u] = U::mfma(off[t], b[u],
-                                                jj == 0 ? f32x4{0, 0, 0, 0} : acc[t][u]);
-                            acc[t][u] = U::mfma(q, b[u], acc[t][u]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int u = 0; u < NT; ++u)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            y[t][u][i] = fmaf(s.scale[t][g].get(i), acc[t][u][i], y[t][u][i]);
-            }
-        };
         const int full = a.C / kQuantCols;  // blocks with all their columns
         const int count = wave < full ? (full - wave + W - 1) / W : 0;
         if (count > 0) {
             // No branch around a load: the last block is loaded again instead.
             B cur, nxt;
             int block = wave;
-            load(cur, block);
+            me.load(a, tile, block, cur);
 #pragma unroll
             for (int i = 0; i < NX; ++i) cur.x[i].load(xp[i] + block * kQuantCols);
 #pragma unroll 1
             for (int i = 1; i <= count; ++i) {
                 stage(cur);
                 block += i < count ? W : 0;
-                load(nxt, block);
+                me.load(a, tile, block, nxt);
 #pragma unroll
                 for (int u = 0; u < NX; ++u) nxt.x[u].load(xp[u] + block * kQuantCols);
                 __builtin_amdgcn_sched_barrier(0);
-                compute(cur);
+                me.multiply(cur, mine, y);
                 cur = nxt;
             }
         }
@@ -319,11 +371,11 @@ __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
             int left = a.C - full * kQuantCols - r16 * 8;
             asm volatile("" : "+v"(left));  // keeps the tail's comparisons out of the item loop
             B b;
-            load(b, full);
+            me.load(a, tile, full, b);
 #pragma unroll
             for (int i = 0; i < NX; ++i) b.x[i].load_tail(xp[i] + full * kQuantCols, left);
             stage(b);
-            compute(b);
+            me.multiply(b, mine, y);
         }
 
         // a row tile at a time: the waves' parts, then each element's sum
@@ -352,22 +404,162 @@ __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
                         s += part(w, c / 16, row % 4, (row / 4) * 16 + c % 16);
                     sum += s;
                 }
-                // Infinities among the moved codes' products cancel to NaN, and moved codes may
-                // pass the range where the codes do not: such an element is computed plainly.
-                if (!(fabsf(sum) <= 3.402823466e38f))
-                    sum = plain_dot<X, S>(a, static_cast<int32_t>(r), v0 + v);
-                const int64_t to = (v0 + v) * a.y_ld + r;
-                if (a.y_fp32) {
-                    float *p = static_cast<float *>(a.y) + to;
-                    *p = a.accumulate ? sum + *p : sum;
-                } else {
-                    X *p = static_cast<X *>(a.y) + to;
-                    *p = static_cast<X>(a.accumulate ? sum + static_cast<float>(*p) : sum);
-                }
+                put_element<X, S>(a, r, v0 + v, sum);
             }
         }
         __syncthreads();  // the next item's vectors overwrite the parts
     }
+}
+
+// Many columns: a workgroup's waves take RT tiles of rows each and share the
+// block's vectors, which all threads bring to LDS (two buffers, one barrier per
+// block): a vector is read once per kWideRows rows instead of once per 16 RT.
+// Where that leaves too few workgroups, the matrix's columns are split among
+// `splits` of them, whose sums meet in the workspace.
+constexpr int kWideWaves = 4;
+constexpr int kWideTiles = 2;
+constexpr int kWideRows = kWideWaves * kWideTiles * 16;
+
+template <typename X, typename S, bool Z, int GS, int NT>
+__global__ __launch_bounds__(kWideWaves *kWave) void k_quant_wide(QuantArgs a) {
+    using U = Unit<X>;
+    constexpr int RT = kWideTiles;
+    constexpr int kVecs = NT * 16 / U::kParts;
+    constexpr int NX = (kVecs + 15) / 16;  // octets of the vectors per thread and block
+    constexpr int kBufBytes = NT * 16 * kColBytes;
+    static_assert(2 * kBufBytes >= kWideWaves * NT * 4 * kWave * 4, "the sums reuse the buffers");
+    __shared__ __attribute__((aligned(16))) char lds[2 * kBufBytes];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const Lane<X, S, Z, GS> me(lane);
+    const int octet = threadIdx.x % 16, slot = threadIdx.x / 16;
+    const int64_t row_blocks = (static_cast<int64_t>(a.R) + kWideRows - 1) / kWideRows;
+    const int64_t last_tile = (static_cast<int64_t>(a.R) - 1) / 16;
+    const int full = a.C / kQuantCols;  // blocks with all their columns
+    for (int64_t item = blockIdx.x; item < row_blocks * a.splits * a.passes; item += gridDim.x) {
+        const int64_t tile0 = (item % row_blocks) * (kWideRows / 16) + wave * RT;
+        const int32_t split = static_cast<int32_t>(item / row_blocks) % a.splits;
+        const int32_t v0 = static_cast<int32_t>(item / row_blocks) / a.splits * kVecs;
+        const int begin = static_cast<int>(static_cast<int64_t>(a.blocks) * split / a.splits);
+        const int end = static_cast<int>(static_cast<int64_t>(a.blocks) * (split + 1) / a.splits);
+        const X *xp[NX];
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            int32_t v = i * 16 + slot;
+            v = v < kVecs ? v0 + v : v0;
+            v = v < a.n ? v : a.n - 1;
+            xp[i] = static_cast<const X *>(a.x) + v * a.x_ld + octet * 8;
+        }
+        int64_t tile[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) tile[t] = tile0 + t < last_tile ? tile0 + t : last_tile;
+        f32x4 y[RT][NT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int u = 0; u < NT; ++u) y[t][u] = f32x4{0, 0, 0, 0};
+
+        using B = Block<X, S, GS, RT, NX>;
+        auto stage = [&](const B &b, char *to) {
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                if (i * 16 + slot >= kVecs) continue;
+                u32x4 part[U::kParts];
+                b.x[i].split(part);
+#pragma unroll
+                for (int p = 0; p < U::kParts; ++p)
+                    *reinterpret_cast<u32x4 *>(
+                        to + ((i * 16 + slot) * U::kParts + p) * kColBytes + octet * 16) = part[p];
+            }
+        };
+        // Two buffers and one barrier per block: whoever writes a buffer again
+        // has passed the barrier behind which nobody reads it any more.
+        int turn = 0;
+        const int whole = end < full ? end : full;
+        if (begin < whole) {
+            B cur, nxt;
+            me.load(a, tile, begin, cur);
+#pragma unroll
+            for (int i = 0; i < NX; ++i) cur.x[i].load(xp[i] + begin * kQuantCols);
+#pragma unroll 1
+            for (int block = begin; block < whole; ++block) {
+                char *buf = lds + turn * kBufBytes;
+                stage(cur, buf);
+                // no branch around a load: the last block is loaded again instead
+                const int next = block + 1 < whole ? block + 1 : block;
+                me.load(a, tile, next, nxt);
+#pragma unroll
+                for (int i = 0; i < NX; ++i) nxt.x[i].load(xp[i] + next * kQuantCols);
+                __syncthreads();
+                me.multiply(cur, buf, y);
+                cur = nxt;
+                turn ^= 1;
+            }
+        }
+        if (whole < end) {  // the block with the last columns
+            int left = a.C - full * kQuantCols - octet * 8;
+            asm volatile("" : "+v"(left));  // keeps the tail's comparisons out of the item loop
+            B b;
+            me.load(a, tile, full, b);
+#pragma unroll
+            for (int i = 0; i < NX; ++i) b.x[i].load_tail(xp[i] + full * kQuantCols, left);
+            char *buf = lds + turn * kBufBytes;
+            stage(b, buf);
+            __syncthreads();
+            me.multiply(b, buf, y);
+        }
+
+        // a wave's tiles through its own part of LDS, to neighbouring rows
+        float *part = reinterpret_cast<float *>(lds) + wave * NT * 4 * kWave;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < NT; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[(u * 4 + i) * kWave + lane] = y[t][u][i];
+            __syncthreads();
+            for (int e = lane; e < kVecs * 16; e += kWave) {
+                const int row = e % 16, v = e / 16;
+                const int64_t r = (tile0 + t) * 16 + row;
+                if (r >= a.R || v0 + v >= a.n) continue;
+                float sum = 0.f;
+#pragma unroll
+                for (int p = U::kParts - 1; p >= 0; --p) {
+                    const int c = v * U::kParts + p;
+                    sum += part[(c / 16 * 4 + row % 4) * kWave + (row / 4) * 16 + c % 16];
+                }
+                if (a.splits > 1)
+                    a.partial[(static_cast<int64_t>(split) * a.n + v0 + v) * a.R + r] = sum;
+                else
+                    put_element<X, S>(a, r, v0 + v, sum);
+            }
+        }
+        __syncthreads();  // the next item's vectors overwrite the parts
+    }
+}
+
+// The splits' sums in order.
+template <typename X, typename S>
+__global__ __launch_bounds__(256) void k_quant_join(QuantArgs a) {
+    const int64_t all = static_cast<int64_t>(a.n) * a.R;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        float sum = 0.f;
+        for (int s = 0; s < a.splits; ++s) sum += a.partial[s * all + i];
+        put_element<X, S>(a, i % a.R, static_cast<int32_t>(i / a.R), sum);
+    }
+}
+
+template <typename X, typename S, bool Z, int GS, int NT>
+void launch_wide(QuantArgs a, hipStream_t s) {
+    constexpr int kVecs = NT * 16 / Unit<X>::kParts;
+    a.passes = a.n / kVecs + (a.n % kVecs != 0);
+    const int64_t row_blocks = (static_cast<int64_t>(a.R) + kWideRows - 1) / kWideRows;
+    k_quant_wide<X, S, Z, GS, NT><<<groups_for(row_blocks * a.splits * a.passes, 1),
+                                    kWideWaves * kWave, 0, s>>>(a);
+    if (a.splits > 1)
+        k_quant_join<X, S><<<groups_for(static_cast<int64_t>(a.n) * a.R, 256), 256, 0, s>>>(a);
 }
 
 template <typename X, typename S, bool Z, int GS, int RT, int NC, int W>
@@ -379,27 +571,33 @@ void launch(QuantArgs a, hipStream_t s) {
         <<<groups_for(row_groups * a.passes, 1), W * kWave, 0, s>>>(a);
 }
 
-// The kernel's shape by the number of vectors and of row tiles.
+// The kernel and its shape by the number of columns and of row tiles.
 template <typename X, typename S, bool Z, int GS>
 void launch_shape(const QuantArgs &a, hipStream_t s) {
     constexpr int P = Unit<X>::kParts;
-    const int64_t passes = (static_cast<int64_t>(a.n) * P + 47) / 48;
-    const int64_t cols = ((a.n + passes - 1) / passes) * P;
-    const bool tall = a.R > 16 * 1024;
+    const int64_t cols = wide_columns(a.n, P);
+    if (cols > 16) {
+        if (cols <= 32)
+            launch_wide<X, S, Z, GS, 2>(a, s);
+        else
+            launch_wide<X, S, Z, GS, 3>(a, s);
+        return;
+    }
+    const bool tall = a.R > 16 * 1024, middle = a.R > 16 * 512;
     if (cols <= 4) {
         if (tall)
             launch<X, S, Z, GS, 2, 4, 4>(a, s);
+        else if (middle)
+            launch<X, S, Z, GS, 1, 4, 4>(a, s);
         else
             launch<X, S, Z, GS, 1, 4, 8>(a, s);
-    } else if (cols <= 15 || (cols == 16 && P == 1)) {
+    } else {
         if (tall)
             launch<X, S, Z, GS, 2, 16, 4>(a, s);
+        else if (middle)
+            launch<X, S, Z, GS, 1, 16, 4>(a, s);
         else
             launch<X, S, Z, GS, 1, 16, 8>(a, s);
-    } else if (cols <= 32 && P == 1) {
-        launch<X, S, Z, GS, 2, 32, 8>(a, s);
-    } else {
-        launch<X, S, Z, GS, 2, 48, 8>(a, s);
     }
 }
 

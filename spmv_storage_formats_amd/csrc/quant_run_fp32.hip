@@ -7,16 +7,41 @@ void quant_run_fp32(const QuantArgs &a, int32_t scale_dtype, hipStream_t s) {
     launch_product<float>(a, scale_dtype, s);
 }
 
+namespace {
+
+// Parts of the columns of a wide product: enough for two workgroups per CU, of
+// eight blocks at least.
+int32_t column_splits(const spmv_quant *q, int32_t n, int32_t x_dtype) {
+    const int parts = x_dtype == SPMV_FP32 ? Unit<float>::kParts : 1;
+    const int64_t cols = wide_columns(n, parts);
+    if (cols <= 16) return 1;
+    const int64_t passes = (static_cast<int64_t>(n) * parts + cols - 1) / cols;
+    const int64_t groups = (static_cast<int64_t>(q->R) + kWideRows - 1) / kWideRows * passes;
+    const int64_t want = (512 + groups - 1) / groups;
+    return static_cast<int32_t>(std::max<int64_t>(
+        1, std::min<int64_t>({want, int64_t{8}, static_cast<int64_t>(q->blocks / 8)})));
+}
+
+}  // namespace
+
+size_t quant_run_bytes(const spmv_quant *q, int32_t n, int32_t x_dtype) {
+    const int32_t splits = column_splits(q, n, x_dtype);
+    return splits > 1 ? static_cast<size_t>(splits) * static_cast<size_t>(n) *
+                            static_cast<size_t>(q->R) * sizeof(float)
+                      : 0;
+}
+
 spmv_status quant_run(const spmv_quant *q, int32_t n, const void *x, int64_t x_ld,
                       int32_t x_dtype, void *y, int64_t y_ld, int32_t y_dtype, int accumulate,
-                      hipStream_t s) {
+                      void *workspace, hipStream_t s) {
     QuantArgs a{};
     a.R = q->R;
     a.C = q->C;
     a.n = n;
     a.blocks = q->blocks;
     a.group = q->group;
-    a.groups_pad = q->groups_pad;
+    a.set = q->set;
+    a.sets = q->sets;
     a.group_shift = (q->group & (q->group - 1)) ? -1 : bits_for(q->group) - 1;
     a.codes = q->codes;
     a.scales = q->scales;
@@ -27,6 +52,8 @@ spmv_status quant_run(const spmv_quant *q, int32_t n, const void *x, int64_t x_l
     a.y_ld = y_ld;
     a.accumulate = accumulate;
     a.y_fp32 = y_dtype == SPMV_FP32;
+    a.splits = column_splits(q, n, x_dtype);
+    a.partial = static_cast<float *>(workspace);
     if (x_dtype == SPMV_FP32)
         quant_run_fp32(a, q->scale_dtype, s);
     else if (x_dtype == SPMV_FP16)

@@ -1,5 +1,5 @@
 // Internal declarations of the weight-table operators: 4-bit matrices with
-// group scales (quant.hip, quant_run.hip), row lookups and their gradient
+// group scales (quant.hip, quant_run_*.hip), row lookups and their gradient
 // (lookup.hip).  Nothing here is part of the public C ABI.
 #pragma once
 
@@ -20,12 +20,16 @@
 // of the vector cache per load instruction instead of 64), then the quads,
 // then the next four rows: a row's 64 bytes are spread over 256, which is
 // what a lookup of it reads.
-// Scales and zero points: [tile][group][16 rows], `groups_pad` groups.
+// Scales and zero points, by tile and set of groups (the `set` groups of one
+// block of columns, or one group of 128 columns and more): scales [4 quads]
+// [set][4 rows], zero points [16 rows][set], so that a lane of the product has
+// its rows' scales, and its row's zero points, of a whole block in one load.
 struct spmv_quant {
     int device = 0;
     int32_t R = 0, C = 0, group = 0;
     int32_t groups = 0;       // ceil(C / group)
-    int32_t groups_pad = 0;   // groups the column blocks reach
+    int32_t set = 1;          // groups per block: 128 / group, at least 1
+    int32_t sets = 0;         // sets that the column blocks reach
     int32_t tiles = 0;        // ceil(R / kQuantRows)
     int32_t blocks = 0;       // ceil(C / kQuantCols)
     int32_t scale_dtype = 0;
@@ -134,6 +138,16 @@ inline int lanes_for(int64_t octets, int most) {
     return L;
 }
 
+// Place of the scale, and of the zero point, of (row r, group g).
+__device__ inline int64_t quant_scale_at(int64_t r, int32_t g, int32_t set, int32_t sets) {
+    const int64_t first = (r / kQuantRows * sets + g / set) * (kQuantRows * set);
+    return first + ((r % kQuantRows / 4) * set + g % set) * 4 + r % 4;
+}
+__device__ inline int64_t quant_zero_at(int64_t r, int32_t g, int32_t set, int32_t sets) {
+    const int64_t first = (r / kQuantRows * sets + g / set) * (kQuantRows * set);
+    return first + r % kQuantRows * set + g % set;
+}
+
 // quant.hip: builders, export, lookup
 spmv_status quant_fill_dense(spmv_quant *q, const void *w, int64_t ld, int32_t dtype, int *flag,
                              hipStream_t s);
@@ -144,10 +158,11 @@ spmv_status quant_unpack(const spmv_quant *q, spmv_quant_array which, void *dev_
 spmv_status quant_lookup(const spmv_quant *q, int64_t n, const void *ids, int32_t id_dtype,
                          float scale, void *out, int64_t ld, int32_t dtype, hipStream_t s);
 
-// quant_run.hip: y <- W x (+ y)
+// quant_run_*.hip: y <- W x (+ y)
+size_t quant_run_bytes(const spmv_quant *q, int32_t n, int32_t x_dtype);  // of workspace
 spmv_status quant_run(const spmv_quant *q, int32_t n, const void *x, int64_t x_ld,
                       int32_t x_dtype, void *y, int64_t y_ld, int32_t y_dtype, int accumulate,
-                      hipStream_t s);
+                      void *workspace, hipStream_t s);
 
 // lookup.hip
 spmv_status lookup_rows(int32_t V, int32_t D, const void *table, int64_t table_ld, int32_t dtype,

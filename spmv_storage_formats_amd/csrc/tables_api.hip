@@ -51,10 +51,12 @@ spmv_status new_quant(QuantPtr &q, int32_t R, int32_t C, int32_t group, bool zer
     q->groups = static_cast<int32_t>((static_cast<int64_t>(C) + group - 1) / group);
     q->tiles = static_cast<int32_t>((static_cast<int64_t>(R) + kQuantRows - 1) / kQuantRows);
     q->blocks = static_cast<int32_t>((static_cast<int64_t>(C) + kQuantCols - 1) / kQuantCols);
+    q->set = std::max(1, kQuantCols / group);
     const int64_t reach = static_cast<int64_t>(q->blocks) * kQuantCols;
-    q->groups_pad = static_cast<int32_t>((reach + group - 1) / group);
+    q->sets = static_cast<int32_t>((reach + group * static_cast<int64_t>(q->set) - 1) /
+                                   (group * static_cast<int64_t>(q->set)));
     q->scale_dtype = scale_dtype;
-    const int64_t groups = static_cast<int64_t>(q->tiles) * q->groups_pad * kQuantRows;
+    const int64_t groups = static_cast<int64_t>(q->tiles) * q->sets * q->set * kQuantRows;
     SPMV_TRY(zeroed(q.get(), &q->codes,
                     static_cast<int64_t>(q->tiles) * q->blocks * kQuantBlockWords * 4, s));
     SPMV_TRY(zeroed(q.get(), &q->scales,
@@ -143,16 +145,28 @@ spmv_status spmv_quant_build_packed(spmv_quant **out, int32_t R, int32_t C, int3
                  });
 }
 
+spmv_status spmv_quant_run_workspace(const spmv_quant *q, int32_t n, spmv_dtype x_dtype,
+                                     size_t *bytes) {
+    if (!q || !bytes || n < 0 || !float_dtype(x_dtype)) return SPMV_ERR_INVALID_ARG;
+    *bytes = n == 0 || q->R == 0 ? 0 : quant_run_bytes(q, n, x_dtype);
+    return SPMV_OK;
+}
+
 spmv_status spmv_quant_run(const spmv_quant *q, int32_t n, const void *x, int64_t x_ld,
                            spmv_dtype x_dtype, void *y, int64_t y_ld, spmv_dtype y_dtype,
-                           int32_t accumulate, void *stream) {
+                           int32_t accumulate, void *workspace, size_t workspace_bytes,
+                           void *stream) {
     if (!q || n < 0 || !float_dtype(x_dtype) || (y_dtype != x_dtype && y_dtype != SPMV_FP32))
         return SPMV_ERR_INVALID_ARG;
     if (n == 0 || q->R == 0 || (q->C == 0 && accumulate)) return SPMV_OK;
     if ((q->C > 0 && !x) || !y || (n > 1 && (x_ld < q->C || y_ld < q->R)))
         return SPMV_ERR_INVALID_ARG;
+    const size_t need = quant_run_bytes(q, n, x_dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need ||
+                     reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
+        return SPMV_ERR_INVALID_ARG;
     SPMV_TRY(check_device(q));
-    return quant_run(q, n, x, x_ld, x_dtype, y, y_ld, y_dtype, accumulate != 0,
+    return quant_run(q, n, x, x_ld, x_dtype, y, y_ld, y_dtype, accumulate != 0, workspace,
                      static_cast<hipStream_t>(stream));
 }
 

@@ -203,6 +203,38 @@ def test_product_strides_and_rows_behind(dev):
     assert np.array_equal(y1.cpu().numpy(), (p.w @ xv[2] + 1).astype(np.float32))
 
 
+def test_product_workspace(dev):
+    """Many vectors over few rows: the columns are split and the parts' sums meet in the
+    workspace, given or allocated; it may hold anything before, and is needed whole."""
+    p = Packed(90, 6000, 64, True, "bf16", 21, exact=True)
+    q = p.build(dev)
+    rng = np.random.default_rng(21)
+    x = rng.integers(-4, 5, (40, 6000)).astype(np.float64)
+    want = torch.from_numpy(x @ p.w.T).float()
+    xt = torch.from_numpy(x).bfloat16().to(dev)
+    assert q.run_workspace(1, torch.bfloat16) == 0
+    need = q.run_workspace(40, torch.bfloat16)
+    assert need >= 2 * 40 * 90 * 4
+    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device=dev)     # NaN as fp32
+    for w in (ws, ws[16:], None):
+        y = torch.full((40, 90), float("nan"), device=dev)
+        q.run(xt, y, accumulate=False, workspace=w)
+        assert torch.equal(y.cpu(), want)
+    assert (ws[need + 16:] == 255).all()          # nothing behind what is needed
+    for bad in (ws[:need - 1], ws[8:], ws.float(), ws[:0]):
+        with pytest.raises((ValueError, TypeError)):
+            q.run(xt, y, workspace=bad)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        y = torch.zeros(40, 90, device=dev)
+        torch.cuda.synchronize()
+        q.run(xt, y, stream=side)
+        junk = torch.full((need // 4,), 9.0, device=dev)      # would reuse a freed workspace
+        torch.cuda.synchronize()
+        assert torch.equal(y.cpu(), want)
+        del junk
+
+
 def test_empty_matrices(dev):
     for R, C in ((0, 64), (5, 0), (0, 0)):
         q = spmv.build_quant(torch.zeros(R, C, device=dev), group_size=32)

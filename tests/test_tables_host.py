@@ -57,7 +57,8 @@ def test_build_packed_refusals(lib, change):
 def test_null_quant_handles(lib):
     n = ctypes.c_size_t()
     info = spmv._QuantInfo()
-    assert lib.spmv_quant_run(None, 1, P, 4, FP32, P, 4, FP32, 1, None) == INVALID
+    assert lib.spmv_quant_run(None, 1, P, 4, FP32, P, 4, FP32, 1, None, 0, None) == INVALID
+    assert lib.spmv_quant_run_workspace(None, 1, FP32, ctypes.byref(n)) == INVALID
     assert lib.spmv_quant_lookup(None, 1, P, INT32, 1.0, P, 4, FP32, None) == INVALID
     assert lib.spmv_quant_get_info(None, ctypes.byref(info)) == INVALID
     assert lib.spmv_quant_array_bytes(None, 0, ctypes.byref(n)) == INVALID
