@@ -496,7 +496,8 @@ typedef enum spmv_dtype {
  *   W[r, c] = scale[r, g] * (code[r, c] - zero[r, g]),  g = c / group,
  * codes and zero points in 0..15, one scale (fp32, fp16 or bf16) per row and
  * group of `group` consecutive columns; the last group of a row may be short.
- * Without zero points zero[r, g] = 8.  `group` is 32, 64 or a multiple of 128. */
+ * Without zero points zero[r, g] = 8.  `group` is 32, 64 or a multiple of 128.
+ * At most 2^28 rows (SPMV_ERR_TOO_LARGE). */
 typedef struct spmv_quant spmv_quant;
 
 typedef struct spmv_quant_info {

@@ -285,6 +285,39 @@ __device__ inline void put_element(const QuantArgs &a, int64_t r, int32_t v, flo
     }
 }
 
+// Elements (r .. r+3, v), as one access where they are finite and inside.
+template <typename X, typename S>
+__device__ inline void put_four(const QuantArgs &a, int64_t r, int32_t v, f32x4 sum) {
+    const f32x4 size = __builtin_elementwise_abs(sum);
+    const float most = fmaxf(fmaxf(size[0], size[1]), fmaxf(size[2], size[3]));
+    // a NaN is no maximum, but makes the sum of all four one
+    const bool plain = !(most <= 3.402823466e38f) || sum[0] + sum[1] + sum[2] + sum[3] !=
+                                                         sum[0] + sum[1] + sum[2] + sum[3];
+    if (plain || r + 4 > a.R) {
+        for (int i = 0; i < 4 && r + i < a.R; ++i) put_element<X, S>(a, r + i, v, sum[i]);
+        return;
+    }
+    auto put = [&](auto *p) {
+        using Y = std::remove_pointer_t<decltype(p)>;
+        struct alignas(sizeof(Y)) Four {
+            Y v[4];
+        } f;
+        if (a.accumulate) {
+            __builtin_memcpy(&f, p, sizeof(f));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] += static_cast<float>(f.v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.v[i] = static_cast<Y>(sum[i]);
+        __builtin_memcpy(p, &f, sizeof(f));
+    };
+    const int64_t to = v * a.y_ld + r;
+    if (a.y_fp32)
+        put(static_cast<float *>(a.y) + to);
+    else
+        put(static_cast<X *>(a.y) + to);
+}
+
 // A workgroup takes RT tiles of 16 rows and NC columns (vectors, or parts of
 // fp32 vectors); its W waves take every W-th block of 128 matrix columns and
 // add up at the end.  A wave keeps its block's vectors in its own part of LDS:
@@ -297,18 +330,17 @@ __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
     constexpr int kVecs = NC / U::kParts;       // vectors per pass
     constexpr int NX = (kVecs + 3) / 4;         // octets of them per lane and block
     constexpr int kWaveBytes = NT * 16 * kColBytes;
-    static_assert(kWaveBytes >= NT * 4 * kWave * 4, "the sums reuse the vectors' part");
+    static_assert(kWaveBytes >= RT * NT * 4 * kWave * 4, "the sums reuse the vectors' part");
     __shared__ __attribute__((aligned(16))) char lds[W * kWaveBytes];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const Lane<X, S, Z, GS> me(lane);
     const int r16 = me.r16, quad = me.quad;
     char *const mine = lds + wave * kWaveBytes;
-    const int64_t row_groups = (static_cast<int64_t>(a.R) + RT * 16 - 1) / (RT * 16);
-    const int64_t last_tile = (static_cast<int64_t>(a.R) - 1) / 16;
-    for (int64_t item = blockIdx.x; item < row_groups * a.passes; item += gridDim.x) {
-        const int64_t tile0 = (item % row_groups) * RT;
-        const int32_t v0 = static_cast<int32_t>(item / row_groups) * kVecs;
+    const int32_t tiles = (a.R - 1) / 16 + 1;
+    for (int32_t pass = blockIdx.y; pass < a.passes; pass += gridDim.y) {
+        const int32_t tile0 = static_cast<int32_t>(blockIdx.x) * RT;
+        const int32_t v0 = pass * kVecs;
         // This lane's share of the vectors.  Slots past the last repeat it: the
         // sums of their columns go nowhere.
         const X *xp[NX];
@@ -321,7 +353,7 @@ __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
         }
         int64_t tile[RT];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) tile[t] = tile0 + t < last_tile ? tile0 + t : last_tile;
+        for (int t = 0; t < RT; ++t) tile[t] = tile0 + t < tiles ? tile0 + t : tiles - 1;
         f32x4 y[RT][NT];
 #pragma unroll
         for (int t = 0; t < RT; ++t)
@@ -378,36 +410,36 @@ __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
             me.multiply(b, mine, y);
         }
 
-        // a row tile at a time: the waves' parts, then each element's sum
-        auto part = [&](int w, int u, int i, int l) -> float & {
-            return reinterpret_cast<float *>(lds + w * kWaveBytes)[(u * 4 + i) * kWave + l];
+        // the waves' parts, then each element's sum
+        auto part = [&](int w, int t, int u, int i, int l) -> float & {
+            return reinterpret_cast<float *>(lds + w * kWaveBytes)[((t * NT + u) * 4 + i) * kWave +
+                                                                   l];
         };
+        __syncthreads();
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            __syncthreads();
+        for (int t = 0; t < RT; ++t)
 #pragma unroll
             for (int u = 0; u < NT; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) part(wave, u, i, lane) = y[t][u][i];
-            __syncthreads();
-            for (int e = threadIdx.x; e < kVecs * 16; e += W * kWave) {
-                const int row = e % 16, v = e / 16;
-                const int64_t r = (tile0 + t) * 16 + row;
-                if (r >= a.R || v0 + v >= a.n) continue;
-                float sum = 0.f;
+                for (int i = 0; i < 4; ++i) part(wave, t, u, i, lane) = y[t][u][i];
+        __syncthreads();
+        for (int e = threadIdx.x; e < kVecs * RT * 16; e += W * kWave) {
+            const int row = e % (RT * 16), v = e / (RT * 16);
+            const int64_t r = static_cast<int64_t>(tile0) * 16 + row;
+            if (r >= a.R || v0 + v >= a.n) continue;
+            float sum = 0.f;
 #pragma unroll
-                for (int p = U::kParts - 1; p >= 0; --p) {
-                    const int c = v * U::kParts + p;
-                    float s = 0.f;
+            for (int p = U::kParts - 1; p >= 0; --p) {
+                const int c = v * U::kParts + p;
+                float s = 0.f;
 #pragma unroll
-                    for (int w = 0; w < W; ++w)
-                        s += part(w, c / 16, row % 4, (row / 4) * 16 + c % 16);
-                    sum += s;
-                }
-                put_element<X, S>(a, r, v0 + v, sum);
+                for (int w = 0; w < W; ++w)
+                    s += part(w, row / 16, c / 16, row % 4, (row % 16 / 4) * 16 + c % 16);
+                sum += s;
             }
+            put_element<X, S>(a, r, v0 + v, sum);
         }
-        __syncthreads();  // the next item's vectors overwrite the parts
+        __syncthreads();  // the next pass's vectors overwrite the parts
     }
 }
 
@@ -425,34 +457,32 @@ __global__ __launch_bounds__(kWideWaves *kWave) void k_quant_wide(QuantArgs a) {
     using U = Unit<X>;
     constexpr int RT = kWideTiles;
     constexpr int kVecs = NT * 16 / U::kParts;
-    constexpr int NX = (kVecs + 15) / 16;  // octets of the vectors per thread and block
+    constexpr int NX = kVecs / 16;  // octets of the vectors per thread and block
     constexpr int kBufBytes = NT * 16 * kColBytes;
-    static_assert(2 * kBufBytes >= kWideWaves * NT * 4 * kWave * 4, "the sums reuse the buffers");
+    static_assert(U::kParts == 1 || U::kParts == NT, "part p of a vector is column p * 16 + v");
     __shared__ __attribute__((aligned(16))) char lds[2 * kBufBytes];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const Lane<X, S, Z, GS> me(lane);
     const int octet = threadIdx.x % 16, slot = threadIdx.x / 16;
-    const int64_t row_blocks = (static_cast<int64_t>(a.R) + kWideRows - 1) / kWideRows;
-    const int64_t last_tile = (static_cast<int64_t>(a.R) - 1) / 16;
+    const int32_t tiles = (a.R - 1) / 16 + 1;
     const int full = a.C / kQuantCols;  // blocks with all their columns
-    for (int64_t item = blockIdx.x; item < row_blocks * a.splits * a.passes; item += gridDim.x) {
-        const int64_t tile0 = (item % row_blocks) * (kWideRows / 16) + wave * RT;
-        const int32_t split = static_cast<int32_t>(item / row_blocks) % a.splits;
-        const int32_t v0 = static_cast<int32_t>(item / row_blocks) / a.splits * kVecs;
+    const int32_t split = blockIdx.y;
+    for (int32_t pass = blockIdx.z; pass < a.passes; pass += gridDim.z) {
+        const int32_t tile0 = static_cast<int32_t>(blockIdx.x) * (kWideRows / 16) + wave * RT;
+        const int32_t v0 = pass * kVecs;
         const int begin = static_cast<int>(static_cast<int64_t>(a.blocks) * split / a.splits);
         const int end = static_cast<int>(static_cast<int64_t>(a.blocks) * (split + 1) / a.splits);
         const X *xp[NX];
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-            int32_t v = i * 16 + slot;
-            v = v < kVecs ? v0 + v : v0;
+            int32_t v = v0 + i * 16 + slot;
             v = v < a.n ? v : a.n - 1;
             xp[i] = static_cast<const X *>(a.x) + v * a.x_ld + octet * 8;
         }
         int64_t tile[RT];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) tile[t] = tile0 + t < last_tile ? tile0 + t : last_tile;
+        for (int t = 0; t < RT; ++t) tile[t] = tile0 + t < tiles ? tile0 + t : tiles - 1;
         f32x4 y[RT][NT];
 #pragma unroll
         for (int t = 0; t < RT; ++t)
@@ -463,13 +493,12 @@ __global__ __launch_bounds__(kWideWaves *kWave) void k_quant_wide(QuantArgs a) {
         auto stage = [&](const B &b, char *to) {
 #pragma unroll
             for (int i = 0; i < NX; ++i) {
-                if (i * 16 + slot >= kVecs) continue;
                 u32x4 part[U::kParts];
                 b.x[i].split(part);
 #pragma unroll
                 for (int p = 0; p < U::kParts; ++p)
-                    *reinterpret_cast<u32x4 *>(
-                        to + ((i * 16 + slot) * U::kParts + p) * kColBytes + octet * 16) = part[p];
+                    *reinterpret_cast<u32x4 *>(to + ((i + p) * 16 + slot) * kColBytes +
+                                               octet * 16) = part[p];
             }
         };
         // Two buffers and one barrier per block: whoever writes a buffer again
@@ -509,33 +538,29 @@ __global__ __launch_bounds__(kWideWaves *kWave) void k_quant_wide(QuantArgs a) {
             me.multiply(b, buf, y);
         }
 
-        // a wave's tiles through its own part of LDS, to neighbouring rows
-        float *part = reinterpret_cast<float *>(lds) + wave * NT * 4 * kWave;
+        // A lane holds four neighbouring rows of one column; fp32: the parts of
+        // one vector in its NT tiles, which add up from the smallest.
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            __syncthreads();
+            const int64_t r = (static_cast<int64_t>(tile0) + t) * 16 + me.quad * 4;
 #pragma unroll
-            for (int u = 0; u < NT; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) part[(u * 4 + i) * kWave + lane] = y[t][u][i];
-            __syncthreads();
-            for (int e = lane; e < kVecs * 16; e += kWave) {
-                const int row = e % 16, v = e / 16;
-                const int64_t r = (tile0 + t) * 16 + row;
-                if (r >= a.R || v0 + v >= a.n) continue;
-                float sum = 0.f;
-#pragma unroll
-                for (int p = U::kParts - 1; p >= 0; --p) {
-                    const int c = v * U::kParts + p;
-                    sum += part[(c / 16 * 4 + row % 4) * kWave + (row / 4) * 16 + c % 16];
+            for (int u = 0; u < NT / U::kParts; ++u) {
+                f32x4 sum = y[t][u];
+                if constexpr (U::kParts == 3) sum = y[t][2] + y[t][1] + y[t][0];
+                const int32_t v = v0 + u * 16 + me.r16;
+                if (v >= a.n) continue;
+                if (a.splits > 1) {
+                    float *p = a.partial + (static_cast<int64_t>(split) * a.n + v) * a.R + r;
+                    if (r + 4 <= a.R)
+                        __builtin_memcpy(p, &sum, 16);
+                    else
+                        for (int i = 0; r + i < a.R; ++i) p[i] = sum[i];
+                } else {
+                    put_four<X, S>(a, r, v, sum);
                 }
-                if (a.splits > 1)
-                    a.partial[(static_cast<int64_t>(split) * a.n + v0 + v) * a.R + r] = sum;
-                else
-                    put_element<X, S>(a, r, v0 + v, sum);
             }
         }
-        __syncthreads();  // the next item's vectors overwrite the parts
+        __syncthreads();  // the next pass's vectors overwrite the last block's
     }
 }
 
@@ -555,9 +580,8 @@ template <typename X, typename S, bool Z, int GS, int NT>
 void launch_wide(QuantArgs a, hipStream_t s) {
     constexpr int kVecs = NT * 16 / Unit<X>::kParts;
     a.passes = a.n / kVecs + (a.n % kVecs != 0);
-    const int64_t row_blocks = (static_cast<int64_t>(a.R) + kWideRows - 1) / kWideRows;
-    k_quant_wide<X, S, Z, GS, NT><<<groups_for(row_blocks * a.splits * a.passes, 1),
-                                    kWideWaves * kWave, 0, s>>>(a);
+    const dim3 grid(grid_for(a.R, kWideRows), a.splits, std::min(a.passes, 65535));
+    k_quant_wide<X, S, Z, GS, NT><<<grid, kWideWaves * kWave, 0, s>>>(a);
     if (a.splits > 1)
         k_quant_join<X, S><<<groups_for(static_cast<int64_t>(a.n) * a.R, 256), 256, 0, s>>>(a);
 }
@@ -566,9 +590,8 @@ template <typename X, typename S, bool Z, int GS, int RT, int NC, int W>
 void launch(QuantArgs a, hipStream_t s) {
     constexpr int kVecs = NC / Unit<X>::kParts;
     a.passes = a.n / kVecs + (a.n % kVecs != 0);
-    const int64_t row_groups = (static_cast<int64_t>(a.R) + RT * 16 - 1) / (RT * 16);
-    k_quant_mfma<X, S, Z, GS, RT, NC, W>
-        <<<groups_for(row_groups * a.passes, 1), W * kWave, 0, s>>>(a);
+    const dim3 grid(grid_for(a.R, RT * 16), std::min(a.passes, 65535));
+    k_quant_mfma<X, S, Z, GS, RT, NC, W><<<grid, W * kWave, 0, s>>>(a);
 }
 
 // The kernel and its shape by the number of columns and of row tiles.
@@ -577,11 +600,9 @@ void launch_shape(const QuantArgs &a, hipStream_t s) {
     constexpr int P = Unit<X>::kParts;
     const int64_t cols = wide_columns(a.n, P);
     if (cols > 16) {
-        if (cols <= 32)
-            launch_wide<X, S, Z, GS, 2>(a, s);
-        else
-            launch_wide<X, S, Z, GS, 3>(a, s);
-        return;
+        if constexpr (P == 1)
+            if (cols <= 32) return launch_wide<X, S, Z, GS, 2>(a, s);
+        return launch_wide<X, S, Z, GS, 3>(a, s);
     }
     const bool tall = a.R > 16 * 1024, middle = a.R > 16 * 512;
     if (cols <= 4) {

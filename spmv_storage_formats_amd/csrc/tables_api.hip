@@ -41,7 +41,8 @@ bool valid_group(int32_t g) { return g == 32 || g == 64 || (g > 0 && g % 128 == 
 // Sizes and zeroed arrays of an R x C matrix.
 spmv_status new_quant(QuantPtr &q, int32_t R, int32_t C, int32_t group, bool zeros,
                       int32_t scale_dtype, hipStream_t s) {
-    if (C > INT32_MAX - 2 * kQuantCols) return SPMV_ERR_TOO_LARGE;  // columns stay in 32 bits
+    // columns stay in 32 bits, and a launch's threads too
+    if (C > INT32_MAX - 2 * kQuantCols || R > (1 << 28)) return SPMV_ERR_TOO_LARGE;
     q.reset(new (std::nothrow) spmv_quant);
     if (!q) return SPMV_ERR_OOM;
     SPMV_HIP(hipGetDevice(&q->device));
