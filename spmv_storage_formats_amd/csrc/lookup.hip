@@ -20,7 +20,9 @@ constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------- lookup
 
-// L lanes per row, an octet each per step.
+// L lanes per row, kFlight octets each per step, all loaded before the first
+// is stored.
+constexpr int kFlight = 2;
 template <typename A, typename B, typename I>
 __global__ __launch_bounds__(kThreads) void k_lookup(int32_t V, int32_t D, int L,
                                                      const A *__restrict__ table,
@@ -28,30 +30,36 @@ __global__ __launch_bounds__(kThreads) void k_lookup(int32_t V, int32_t D, int L
                                                      const I *__restrict__ ids, float scale,
                                                      B *__restrict__ out, int64_t out_ld) {
     const int rows = kThreads / L;
-    const int octets = D / 8 + (D % 8 != 0);
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * rows + threadIdx.x / L; t < n;
          t += static_cast<int64_t>(gridDim.x) * rows) {
         const int64_t id = ids[t];
         const bool there = id >= 0 && id < V;
         const A *src = table + (there ? id : 0) * table_ld;
         B *dst = out + t * out_ld;
-        for (int o = threadIdx.x % L; o < octets; o += L) {
-            const int left = D - o * 8;
-            float v[8];
+        for (int64_t c = threadIdx.x % L * 8; c < D; c += kFlight * 8 * L) {
+            float v[kFlight][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.f;
-            if (there) {
-                if (left >= 8)
-                    load_octet(src + o * 8, v);
-                else
-                    load_octet_tail(src + o * 8, left, v);
+            for (int u = 0; u < kFlight; ++u) {
+                const int64_t at = c + u * 8 * L;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= scale;
+                for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+                if (there && at + 8 <= D)
+                    load_octet(src + at, v[u]);
+                else if (there && at < D)
+                    load_octet_tail(src + at, static_cast<int>(D - at), v[u]);
             }
-            if (left >= 8)
-                store_octet(dst + o * 8, v);
-            else
-                store_octet_tail(dst + o * 8, left, v);
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                const int64_t at = c + u * 8 * L;
+                if (there) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[u][i] *= scale;
+                }
+                if (at + 8 <= D)
+                    store_octet(dst + at, v[u]);
+                else if (at < D)
+                    store_octet_tail(dst + at, static_cast<int>(D - at), v[u]);
+            }
         }
     }
 }

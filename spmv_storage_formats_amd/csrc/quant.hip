@@ -162,41 +162,53 @@ __global__ __launch_bounds__(kThreads) void k_quant_unpack_groups(int32_t R, int
     }
 }
 
-// Rows by token: out[t] = scale * s (code - zero).  L lanes per row, an octet
-// (one word, eight values, one 16- or 32-byte store) each per step.
+// Rows by token: out[t] = scale * s (code - zero).  L lanes per row; a lane
+// takes the 16 bytes that lie together, octets q, q + 4, q + 8 and q + 12 of a
+// block of 128 columns, so that four lanes store neighbouring octets each time.
 template <typename S, typename T, typename I>
 __global__ __launch_bounds__(kThreads) void k_quant_lookup(
     int32_t R, int32_t C, int32_t group, int32_t set, int32_t sets, int32_t blocks, int L,
     const uint32_t *__restrict__ codes, const S *__restrict__ scales,
     const uint8_t *__restrict__ zeros, int64_t n, const I *__restrict__ ids, float scale,
     T *__restrict__ out, int64_t ld) {
+    using Four = uint32_t __attribute__((ext_vector_type(4)));
     const int rows = kThreads / L;
-    const int octets = C / 8 + (C % 8 != 0);
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * rows + threadIdx.x / L; t < n;
          t += static_cast<int64_t>(gridDim.x) * rows) {
         const int64_t id = ids[t];
         const bool there = id >= 0 && id < R;
         const int32_t r = there ? static_cast<int32_t>(id) : 0;
         T *row = out + t * ld;
-        for (int o = threadIdx.x % L; o < octets; o += L) {
-            float v[8];
+        for (int32_t i = threadIdx.x % L; i / 4 < blocks; i += L) {
+            const int32_t c0 = i / 4 * kQuantCols + i % 4 * 8;  // columns c0 + 32 j
+            Four w = {0, 0, 0, 0};
+            float s[4] = {}, z[4] = {8.f, 8.f, 8.f, 8.f};
             if (there) {
-                const uint32_t w = codes[word_index(r, o, blocks)];
-                const int32_t g = o * 8 / group;
-                const float s = static_cast<float>(scales[quant_scale_at(r, g, set, sets)]);
-                const float z =
-                    zeros ? static_cast<float>(zeros[quant_zero_at(r, g, set, sets)]) : 8.f;
+                w = *reinterpret_cast<const Four *>(codes + word_index(r, c0 / 8, blocks));
+                // the block's first group, and its others behind it (quant_scale_at's steps)
+                const int32_t g = set > 1 ? i / 4 * set : group > kQuantCols ? c0 / group : i / 4;
+                const int64_t s0 = quant_scale_at(r, g, set, sets);
+                const int64_t z0 = quant_zero_at(r, g, set, sets);
+                const int shift = set == 4 ? 0 : set == 2 ? 1 : 2;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[j] = static_cast<float>(scales[s0 + (j >> shift) * 4]);
+                    if (zeros) z[j] = static_cast<float>(zeros[z0 + (j >> shift)]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int32_t c = c0 + 32 * j;
+                float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[e] = (static_cast<float>(quant_code(w, e)) - z) * s * scale;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = 0.f;
+                    v[e] = there ? (static_cast<float>(quant_code(w[j], e)) - z[j]) * s[j] * scale
+                                 : 0.f;
+                if (c + 8 <= C)
+                    store_octet(row + c, v);
+                else if (c < C)
+                    store_octet_tail(row + c, C - c, v);
             }
-            if (o * 8 + 8 <= C)
-                store_octet(row + o * 8, v);
-            else
-                store_octet_tail(row + o * 8, C - o * 8, v);
         }
     }
 }
@@ -265,7 +277,7 @@ spmv_status quant_unpack(const spmv_quant *q, spmv_quant_array which, void *dst,
 
 spmv_status quant_lookup(const spmv_quant *q, int64_t n, const void *ids, int32_t id_dtype,
                          float scale, void *out, int64_t ld, int32_t dtype, hipStream_t s) {
-    const int L = lanes_for((static_cast<int64_t>(q->C) + 7) / 8, kThreads);
+    const int L = lanes_for(static_cast<int64_t>(q->blocks) * 4, kThreads);
     const unsigned grid = groups_for(n, kThreads / L);
     with_float(q->scale_dtype, [&](auto sc) {
         with_float(dtype, [&](auto t) {

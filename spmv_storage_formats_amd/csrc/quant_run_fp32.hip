@@ -9,7 +9,7 @@ void quant_run_fp32(const QuantArgs &a, int32_t scale_dtype, hipStream_t s) {
 
 namespace {
 
-// Parts of the columns of a wide product: enough for two workgroups per CU, of
+// Parts of the columns of a wide product: enough for four workgroups per CU, of
 // eight blocks at least.
 int32_t column_splits(const spmv_quant *q, int32_t n, int32_t x_dtype) {
     const int parts = x_dtype == SPMV_FP32 ? Unit<float>::kParts : 1;
@@ -17,7 +17,7 @@ int32_t column_splits(const spmv_quant *q, int32_t n, int32_t x_dtype) {
     if (cols <= 16) return 1;
     const int64_t passes = (static_cast<int64_t>(n) * parts + cols - 1) / cols;
     const int64_t groups = (static_cast<int64_t>(q->R) + kWideRows - 1) / kWideRows * passes;
-    const int64_t want = (512 + groups - 1) / groups;
+    const int64_t want = (1024 + groups - 1) / groups;
     return static_cast<int32_t>(std::max<int64_t>(
         1, std::min<int64_t>({want, int64_t{8}, static_cast<int64_t>(q->blocks / 8)})));
 }

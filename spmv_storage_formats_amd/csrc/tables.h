@@ -138,14 +138,16 @@ inline int lanes_for(int64_t octets, int most) {
     return L;
 }
 
-// Place of the scale, and of the zero point, of (row r, group g).
+// Place of the scale, and of the zero point, of (row r, group g); set is 1, 2
+// or 4.
 __device__ inline int64_t quant_scale_at(int64_t r, int32_t g, int32_t set, int32_t sets) {
-    const int64_t first = (r / kQuantRows * sets + g / set) * (kQuantRows * set);
-    return first + ((r % kQuantRows / 4) * set + g % set) * 4 + r % 4;
+    const int32_t first = g >> (set / 2), in = g & (set - 1);
+    return (r / kQuantRows * sets + first) * (kQuantRows * set) +
+           ((r % kQuantRows / 4) * set + in) * 4 + r % 4;
 }
 __device__ inline int64_t quant_zero_at(int64_t r, int32_t g, int32_t set, int32_t sets) {
-    const int64_t first = (r / kQuantRows * sets + g / set) * (kQuantRows * set);
-    return first + r % kQuantRows * set + g % set;
+    const int32_t first = g >> (set / 2), in = g & (set - 1);
+    return (r / kQuantRows * sets + first) * (kQuantRows * set) + r % kQuantRows * set + in;
 }
 
 // quant.hip: builders, export, lookup
