@@ -579,7 +579,8 @@ def _stream_of(index, stream, *made):
     one, it waits for that stream, and their memory is not reused before it is done."""
     import torch
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # makes no Stream object
+        return raw(index) if raw else torch.cuda.current_stream(index).cuda_stream
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     current = torch.cuda.current_stream(index)
     if made and handle != current.cuda_stream:

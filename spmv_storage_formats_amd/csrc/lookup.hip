@@ -20,7 +20,17 @@ constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------- lookup
 
-// L lanes per row, kFlight octets each per step, all loaded before the first
+// Columns a lane handles at a time: eight, but four of them as fp32 where it
+// pays.  A lane's 32 bytes are two accesses, in neither of which its
+// neighbour's bytes lie beside its own (one access of the vector cache per
+// lane instead of one per four), but four bf16 are only half as many bytes
+// per access.  16384 rows of 4096, fp32 to fp32: 111 us by eights, 96 by fours;
+// bf16 to fp32 99 and 94; fp32 to bf16 49 and 54.  Gradients of 16384 x 1024,
+// fp32 to fp32: 42.5 and 41.2; 32768 x 2048, bf16 to fp32: 236 and 241.
+template <typename T>
+constexpr int kPiece = sizeof(T) == 4 ? 4 : 8;
+
+// L lanes per row, kFlight pieces each per step, all loaded before the first
 // is stored.
 constexpr int kFlight = 2;
 template <typename A, typename B, typename I>
@@ -29,6 +39,7 @@ __global__ __launch_bounds__(kThreads) void k_lookup(int32_t V, int32_t D, int L
                                                      int64_t table_ld, int64_t n,
                                                      const I *__restrict__ ids, float scale,
                                                      B *__restrict__ out, int64_t out_ld) {
+    constexpr int E = kPiece<B>;
     const int rows = kThreads / L;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * rows + threadIdx.x / L; t < n;
          t += static_cast<int64_t>(gridDim.x) * rows) {
@@ -36,29 +47,29 @@ __global__ __launch_bounds__(kThreads) void k_lookup(int32_t V, int32_t D, int L
         const bool there = id >= 0 && id < V;
         const A *src = table + (there ? id : 0) * table_ld;
         B *dst = out + t * out_ld;
-        for (int64_t c = threadIdx.x % L * 8; c < D; c += kFlight * 8 * L) {
-            float v[kFlight][8];
+        for (int64_t c = threadIdx.x % L * E; c < D; c += kFlight * E * L) {
+            float v[kFlight][E];
 #pragma unroll
             for (int u = 0; u < kFlight; ++u) {
-                const int64_t at = c + u * 8 * L;
+                const int64_t at = c + u * E * L;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-                if (there && at + 8 <= D)
-                    load_octet(src + at, v[u]);
+                for (int i = 0; i < E; ++i) v[u][i] = 0.f;
+                if (there && at + E <= D)
+                    load_piece<E>(src + at, v[u]);
                 else if (there && at < D)
-                    load_octet_tail(src + at, static_cast<int>(D - at), v[u]);
+                    load_piece_tail<E>(src + at, static_cast<int>(D - at), v[u]);
             }
 #pragma unroll
             for (int u = 0; u < kFlight; ++u) {
-                const int64_t at = c + u * 8 * L;
+                const int64_t at = c + u * E * L;
                 if (there) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[u][i] *= scale;
+                    for (int i = 0; i < E; ++i) v[u][i] *= scale;
                 }
-                if (at + 8 <= D)
-                    store_octet(dst + at, v[u]);
+                if (at + E <= D)
+                    store_piece<E>(dst + at, v[u]);
                 else if (at < D)
-                    store_octet_tail(dst + at, static_cast<int>(D - at), v[u]);
+                    store_piece_tail<E>(dst + at, static_cast<int>(D - at), v[u]);
             }
         }
     }
@@ -156,6 +167,7 @@ __device__ inline void sort_tile(SortShared &s, const uint32_t *key, const uint3
         const int before = valid ? s.wrun[w][d] : 0;
         rank[j] = before + r;
         if (valid && r == 0) s.wrun[w][d] = before + __popcll(peers);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the next step reads it
         __builtin_amdgcn_wave_barrier();
     }
     __syncthreads();
@@ -233,7 +245,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_tiles(const I *__restrict
 // tile the number of tokens before it, by binary search.  kAbreast tiles at a
 // time are brought to LDS and searched side by side (searching them where they
 // lie costs one access of the vector cache per lane and step: 53 us against
-// the 9 of this for 32768 tokens).
+// the 12 of this for 32768 tokens).
 __global__ __launch_bounds__(kThreads) void k_sort_merge(int n, const uint32_t *__restrict__ keys,
                                                          const uint32_t *__restrict__ pos,
                                                          uint32_t *__restrict__ keys_out,
@@ -290,15 +302,60 @@ __global__ __launch_bounds__(kThreads) void k_sort_merge(int n, const uint32_t *
     }
 }
 
-// One pass over many tiles.  A tile's place for digit d is the tokens of all
-// smaller digits plus those of d in earlier tiles: every workgroup adds them
-// up from the count table itself (thread d, one row of the table per step).
+// A tile's place for digit d is the tokens of all smaller digits plus those of
+// d in earlier tiles.  Up to kSumTiles tiles, every workgroup of the scatter
+// adds them up from the count table itself (thread d, one row of the table per
+// step).  More tiles are taken in segments, whose places are found first:
+// segment sums, then one workgroup turns them into places.  A pass takes 22 us
+// without segments and 24 with them for 35 tiles, 75 and 32 for 245 (50 with
+// segments of 64).
+constexpr int kSumTiles = 64;
+constexpr int kSegment = 16;
+
+// Segments that the passes over so many tiles use.
+inline int32_t sort_segments(int32_t tiles) {
+    return tiles > kSumTiles ? (tiles + kSegment - 1) / kSegment : 0;
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_sort_segments(int32_t tiles, int bits,
+                                                                const int32_t *__restrict__ counts,
+                                                                int32_t *__restrict__ places) {
+    const int digits = 1 << bits, d = threadIdx.x;
+    if (d >= digits) return;
+    const int32_t first = static_cast<int32_t>(blockIdx.x) * kSegment;
+    const int32_t last = tiles - first < kSegment ? tiles : first + kSegment;
+    int32_t sum = 0;
+#pragma unroll 4
+    for (int32_t t = first; t < last; ++t) sum += counts[static_cast<int64_t>(t) * digits + d];
+    places[static_cast<int64_t>(blockIdx.x) * digits + d] = sum;
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_sort_places(int32_t segments, int bits,
+                                                              int32_t *__restrict__ places) {
+    __shared__ int wsum[kSortWaves];
+    const int digits = 1 << bits, d = threadIdx.x;
+    int total = 0;
+    if (d < digits)
+#pragma unroll 4
+        for (int32_t s = 0; s < segments; ++s) total += places[static_cast<int64_t>(s) * digits + d];
+    int at = sort_exclusive(total, wsum);
+    if (d < digits) {
+        for (int32_t s = 0; s < segments; ++s) {
+            int32_t *p = places + static_cast<int64_t>(s) * digits + d;
+            const int32_t sum = *p;
+            *p = at;
+            at += sum;
+        }
+    }
+}
+
+// One pass over many tiles; `places` null: at most kSumTiles tiles.
 template <typename I>
 __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(
     const I *__restrict__ ids, int32_t V, const uint32_t *__restrict__ keys,
     const uint32_t *__restrict__ pos_in, int64_t n, int shift, int bits, int32_t tiles,
-    const int32_t *__restrict__ counts, uint32_t *__restrict__ keys_out,
-    uint32_t *__restrict__ pos_out) {
+    const int32_t *__restrict__ counts, const int32_t *__restrict__ places,
+    uint32_t *__restrict__ keys_out, uint32_t *__restrict__ pos_out) {
     __shared__ SortShared s;
     __shared__ int goff[kSortDigits];
     const int lane = __lane_id(), w = threadIdx.x / kWave, tid = threadIdx.x;
@@ -315,16 +372,26 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(
             pos[j] = keys ? pos_in[tile0 + i] : static_cast<uint32_t>(tile0 + i);
         }
     }
-    int total = 0, before = 0;
-    if (tid < digits) {
-        for (int t = 0; t < tiles; ++t) {
-            const int c = counts[static_cast<int64_t>(t) * digits + tid];
-            before += t < static_cast<int>(blockIdx.x) ? c : 0;
-            total += c;
+    const int32_t own = static_cast<int32_t>(blockIdx.x);
+    if (places) {
+        if (tid < digits) {
+            int at = places[static_cast<int64_t>(own / kSegment) * digits + tid];
+            for (int32_t t = own / kSegment * kSegment; t < own; ++t)
+                at += counts[static_cast<int64_t>(t) * digits + tid];
+            goff[tid] = at;
         }
+    } else {
+        int total = 0, before = 0;
+        if (tid < digits) {
+            for (int32_t t = 0; t < tiles; ++t) {
+                const int c = counts[static_cast<int64_t>(t) * digits + tid];
+                before += t < own ? c : 0;
+                total += c;
+            }
+        }
+        const int smaller = sort_exclusive(total, s.wsum);
+        if (tid < digits) goff[tid] = smaller + before;
     }
-    const int smaller = sort_exclusive(total, s.wsum);
-    if (tid < digits) goff[tid] = smaller + before;
     sort_tile(s, key, pos, count, shift, bits);
     for (int p = tid; p < count; p += kSortThreads) {
         const uint32_t k = s.key[p];
@@ -339,7 +406,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(
 
 constexpr int kMaxChunk = 32;   // sorted tokens per chunk, at most
 constexpr int kMinLanes = 8;    // lanes per chunk, at least
-constexpr int kClearRows = 16;  // table rows that one wave clears
+constexpr int kClearRows = 8;   // table rows that one wave clears
 constexpr int kAhead = 8;       // gradient rows in flight per lane
 constexpr int kJoinParts = 4;   // waves that share a cut row's parts
 constexpr int kJoinThreads = kJoinParts * kWave;
@@ -364,27 +431,27 @@ __device__ inline uint32_t first_not_below(const uint32_t *keys, uint32_t lo, ui
     return lo;
 }
 
-template <typename T>
+template <int E, typename T>
 __device__ inline void put_row(T *p, int left, float scale, int accumulate, const float *sum) {
-    float v[8];
+    float v[E];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    for (int i = 0; i < E; ++i) v[i] = 0.f;
     if (accumulate) {
-        if (left >= 8)
-            load_octet(p, v);
+        if (left >= E)
+            load_piece<E>(p, v);
         else
-            load_octet_tail(p, left, v);
+            load_piece_tail<E>(p, left, v);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fmaf(scale, sum[i], v[i]);
-    if (left >= 8)
-        store_octet(p, v);
+    for (int i = 0; i < E; ++i) v[i] = fmaf(scale, sum[i], v[i]);
+    if (left >= E)
+        store_piece<E>(p, v);
     else
-        store_octet_tail(p, left, v);
+        store_piece_tail<E>(p, left, v);
 }
 
 // The sums of chunks of sorted tokens over a range of columns: a group of L
-// lanes per chunk, an octet of columns per lane.  A row whose tokens all lie
+// lanes per chunk, a piece of columns per lane.  A row whose tokens all lie
 // in the chunk is written; the part of one that goes on from the chunk before
 // goes to head[chunk], the part of one that goes on into the next to
 // tail[chunk] (one that does both: head).
@@ -396,6 +463,7 @@ __device__ inline void grad_chunk(int32_t V, int32_t D, int64_t n,
                                   T *__restrict__ out, int64_t ld, float *__restrict__ head,
                                   float *__restrict__ tail, int per_chunk, int L, int64_t first,
                                   int64_t part) {
+    constexpr int E = kPiece<G>;
     __shared__ uint32_t lds_key[kThreads / kMinLanes][kMaxChunk];
     __shared__ uint32_t lds_pos[kThreads / kMinLanes][kMaxChunk];
     const int group = threadIdx.x / L, lane = threadIdx.x % L;
@@ -412,22 +480,22 @@ __device__ inline void grad_chunk(int32_t V, int32_t D, int64_t n,
     const uint32_t prev = count > 0 && base > 0 ? keys[base - 1] : none;
     const uint32_t next = base + count < n ? keys[base + count] : none;
     __syncthreads();
-    const int64_t col = (part * L + lane) * 8;
+    const int64_t col = (part * L + lane) * E;
     if (col >= D || count == 0) return;
-    const int left = static_cast<int>(D - col < 8 ? D - col : 8);
-    float sum[8] = {};
+    const int left = static_cast<int>(D - col < E ? D - col : E);
+    float sum[E] = {};
     bool from_before = s_key[0] == prev;
     for (int k0 = 0; k0 < count; k0 += kAhead) {
-        Octet<G> g[kAhead];
+        Piece<G, E> g[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int k = k0 + j < count ? k0 + j : count - 1;
             const G *p = grad + static_cast<int64_t>(s_pos[k]) * grad_ld + col;
-            if (left == 8) {
+            if (left == E) {
                 __builtin_memcpy(&g[j], p, sizeof(g[j]));
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) g[j].v[i] = i < left ? p[i] : static_cast<G>(0.f);
+                for (int i = 0; i < E; ++i) g[j].v[i] = i < left ? p[i] : static_cast<G>(0.f);
             }
         }
 #pragma unroll
@@ -437,22 +505,22 @@ __device__ inline void grad_chunk(int32_t V, int32_t D, int64_t n,
             const uint32_t key = s_key[k];
             if (key >= static_cast<uint32_t>(V)) return;  // tokens that name no row come last
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += static_cast<float>(g[j].v[i]);
+            for (int i = 0; i < E; ++i) sum[i] += static_cast<float>(g[j].v[i]);
             const bool last = k + 1 == count;
             const uint32_t after = last ? next : s_key[k + 1];
             if (!last && after == key) continue;
             if (from_before || (last && after == key)) {
                 float *p = (from_before ? head : tail) + chunk * D + col;
-                if (left == 8)
-                    store_octet(p, sum);
+                if (left == E)
+                    store_piece<E>(p, sum);
                 else
-                    store_octet_tail(p, left, sum);
+                    store_piece_tail<E>(p, left, sum);
             } else {
-                put_row(out + static_cast<int64_t>(key) * ld + col, left, scale, accumulate, sum);
+                put_row<E>(out + static_cast<int64_t>(key) * ld + col, left, scale, accumulate, sum);
             }
             from_before = false;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+            for (int i = 0; i < E; ++i) sum[i] = 0.f;
         }
     }
 }
@@ -477,13 +545,13 @@ __device__ inline void grad_clear(int32_t V, int32_t D, uint32_t n,
         at = first_not_below(keys, at + kWave, n, first + last + 1);
     }
     constexpr int kPer = 16 / sizeof(T);
-    using Piece = uint32_t __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+    using Zeros = uint32_t __attribute__((ext_vector_type(4), aligned(sizeof(T))));
     for (uint32_t i = 0; i < rows; ++i) {
         if ((named >> i) & 1) continue;
         T *p = out + (r0 + i) * ld;
         for (int64_t c = static_cast<int64_t>(lane) * kPer; c < D; c += kWave * kPer) {
             if (c + kPer <= D) {
-                *reinterpret_cast<Piece *>(p + c) = Piece{0, 0, 0, 0};
+                *reinterpret_cast<Zeros *>(p + c) = Zeros{0, 0, 0, 0};
             } else {
                 for (int64_t e = c; e < D; ++e) p[e] = static_cast<T>(0.f);
             }
@@ -568,15 +636,15 @@ __global__ __launch_bounds__(kJoinThreads) void k_grad_join(
     }
 }
 
-// Lanes per chunk, a power of two.
-int chunk_lanes(int32_t D) {
-    return std::max(kMinLanes, lanes_for((static_cast<int64_t>(D) + 7) / 8, kThreads));
+// Lanes per chunk, a power of two, for pieces of `piece` columns.
+int chunk_lanes(int32_t D, int piece) {
+    return std::max(kMinLanes, lanes_for((static_cast<int64_t>(D) + piece - 1) / piece, kThreads));
 }
 
 // Sorted tokens per chunk: short chunks while there are few, so that the sums
 // have 2048 waves (8 per CU); long ones leave fewer cut rows to join.
 int chunk_length(int32_t D, int64_t n) {
-    const int64_t octets = (static_cast<int64_t>(D) + 7) / 8, L = chunk_lanes(D);
+    const int64_t octets = (static_cast<int64_t>(D) + 7) / 8, L = chunk_lanes(D, 8);
     const int64_t lanes = (octets + L - 1) / L * L;
     int k = 8;
     while (k < kMaxChunk && n * lanes > int64_t{2048} * kWave * k) k *= 2;
@@ -586,7 +654,7 @@ int chunk_length(int32_t D, int64_t n) {
 // Parts of the gradient's workspace, each 256-byte aligned.
 struct GradWorkspace {
     uint32_t *keys[2], *pos[2];
-    int32_t *counts;
+    int32_t *counts, *places;
     float *head, *tail;
     size_t bytes;
 };
@@ -599,14 +667,16 @@ GradWorkspace grad_workspace(int32_t D, int64_t n, void *base) {
         at += (bytes + 255) & ~size_t{255};
         return p;
     };
-    const size_t tiles = static_cast<size_t>((n + kSortTile - 1) / kSortTile);
+    const int32_t tiles = static_cast<int32_t>((n + kSortTile - 1) / kSortTile);
     const int per_chunk = chunk_length(D, n);
     const size_t chunks = static_cast<size_t>((n + per_chunk - 1) / per_chunk);
     for (int i = 0; i < 2; ++i) {
         w.keys[i] = reinterpret_cast<uint32_t *>(take(static_cast<size_t>(n) * 4));
         w.pos[i] = reinterpret_cast<uint32_t *>(take(static_cast<size_t>(n) * 4));
     }
-    w.counts = reinterpret_cast<int32_t *>(take(n > kMergeMost ? tiles * kSortDigits * 4 : 0));
+    const size_t row = kSortDigits * 4;
+    w.counts = reinterpret_cast<int32_t *>(take(n > kMergeMost ? tiles * row : 0));
+    w.places = reinterpret_cast<int32_t *>(take(sort_segments(tiles) * row));
     const size_t part = chunks > 1 ? chunks * static_cast<size_t>(D) * 4 : 0;
     w.head = reinterpret_cast<float *>(take(part));
     w.tail = reinterpret_cast<float *>(take(part));
@@ -637,12 +707,21 @@ spmv_status sort_tokens(int32_t V, int64_t n, const I *ids, const GradWorkspace 
         *pos = w.pos[last];
         return SPMV_OK;
     }
+    const int32_t segments = sort_segments(tiles);
+    int32_t *places = segments > 0 ? w.places : nullptr;
     const uint32_t *k = nullptr, *p = nullptr;
     for (int i = 0; i < passes; ++i) {
         k_sort_count<I><<<tiles, kSortThreads, 0, s>>>(ids, V, k, n, i * bits, bits, w.counts);
         SPMV_HIP(hipGetLastError());
+        if (places) {
+            k_sort_segments<<<segments, kSortThreads, 0, s>>>(tiles, bits, w.counts, places);
+            SPMV_HIP(hipGetLastError());
+            k_sort_places<<<1, kSortThreads, 0, s>>>(segments, bits, places);
+            SPMV_HIP(hipGetLastError());
+        }
         k_sort_scatter<I><<<tiles, kSortThreads, 0, s>>>(ids, V, k, p, n, i * bits, bits, tiles,
-                                                         w.counts, w.keys[i & 1], w.pos[i & 1]);
+                                                         w.counts, places, w.keys[i & 1],
+                                                         w.pos[i & 1]);
         SPMV_HIP(hipGetLastError());
         k = w.keys[i & 1];
         p = w.pos[i & 1];
@@ -657,7 +736,8 @@ spmv_status sort_tokens(int32_t V, int64_t n, const I *ids, const GradWorkspace 
 spmv_status lookup_rows(int32_t V, int32_t D, const void *table, int64_t table_ld, int32_t dtype,
                         int64_t n, const void *ids, int32_t id_dtype, float scale, void *out,
                         int64_t out_ld, int32_t out_dtype, hipStream_t s) {
-    const int L = lanes_for((static_cast<int64_t>(D) + 7) / 8, kThreads);
+    const int piece = out_dtype == SPMV_FP32 ? kPiece<float> : kPiece<f16>;
+    const int L = lanes_for((static_cast<int64_t>(D) + piece - 1) / piece, kThreads);
     const unsigned grid = groups_for(n, kThreads / L);
     with_float(dtype, [&](auto a) {
         with_float(out_dtype, [&](auto b) {
@@ -693,9 +773,9 @@ spmv_status lookup_grad(int32_t V, int32_t D, int64_t n, const void *ids, int32_
         else
             SPMV_TRY(sort_tokens(V, n, static_cast<const int32_t *>(ids), w, &keys, &pos, s));
     }
-    const int64_t octets = (static_cast<int64_t>(D) + 7) / 8;
-    const int L = chunk_lanes(D);
-    const int64_t parts = (octets + L - 1) / L;
+    const int piece = grad_dtype == SPMV_FP32 ? kPiece<float> : kPiece<f16>;
+    const int L = chunk_lanes(D, piece);
+    const int64_t parts = (static_cast<int64_t>(D) + L * piece - 1) / (L * piece);
     const int per_chunk = chunk_length(D, n);
     const int64_t chunks = (n + per_chunk - 1) / per_chunk;
     const int64_t sums = (chunks + kThreads / L - 1) / (kThreads / L) * parts;

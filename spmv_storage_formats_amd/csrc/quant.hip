@@ -54,7 +54,7 @@ __global__ __launch_bounds__(kThreads) void k_quant_build(
         bool bad = false;
         for (int o = sub; o < octets; o += L) {
             float v[8];
-            load_octet_tail(row + c0 + o * 8, c1 - c0 - o * 8, v);
+            load_piece_tail<8>(row + c0 + o * 8, c1 - c0 - o * 8, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 bad |= !(fabsf(v[i]) <= 3.402823466e38f);
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(kThreads) void k_quant_build(
         }
         for (int o = sub; o < octets; o += L) {
             float v[8];
-            load_octet_tail(row + c0 + o * 8, c1 - c0 - o * 8, v);
+            load_piece_tail<8>(row + c0 + o * 8, c1 - c0 - o * 8, v);
             uint32_t word = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -205,9 +205,9 @@ __global__ __launch_bounds__(kThreads) void k_quant_lookup(
                     v[e] = there ? (static_cast<float>(quant_code(w[j], e)) - z[j]) * s[j] * scale
                                  : 0.f;
                 if (c + 8 <= C)
-                    store_octet(row + c, v);
+                    store_piece<8>(row + c, v);
                 else if (c < C)
-                    store_octet_tail(row + c, C - c, v);
+                    store_piece_tail<8>(row + c, C - c, v);
             }
         }
     }

@@ -97,8 +97,8 @@ struct XOctet {
 template <>
 struct XOctet<float> {
     float v[8];
-    __device__ inline void load(const float *p) { load_octet(p, v); }
-    __device__ inline void load_tail(const float *p, int count) { load_octet_tail(p, count, v); }
+    __device__ inline void load(const float *p) { load_piece<8>(p, v); }
+    __device__ inline void load_tail(const float *p, int count) { load_piece_tail<8>(p, count, v); }
     __device__ inline void split(u32x4 *part) const {
         uint32_t w[3][8];
 #pragma unroll

@@ -84,40 +84,40 @@ auto with_float(int32_t d, F f) {
     return d == SPMV_FP32 ? f(float{}) : d == SPMV_FP16 ? f(f16{}) : f(bf16{});
 }
 
-// Eight consecutive elements.  Rows start at any element, so the vectors
-// carry their element's alignment; gfx950 loads and stores them whole.
-template <typename T>
-struct alignas(sizeof(T)) Octet {
-    T v[8];
+// E consecutive elements.  Rows start at any element, so the vectors carry
+// their element's alignment; gfx950 loads and stores them whole.
+template <typename T, int E>
+struct alignas(sizeof(T)) Piece {
+    T v[E];
 };
 
-template <typename T>
-__device__ inline void load_octet(const T *p, float *out) {
-    Octet<T> o;
+template <int E, typename T>
+__device__ inline void load_piece(const T *p, float *out) {
+    Piece<T, E> o;
     __builtin_memcpy(&o, p, sizeof(o));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = static_cast<float>(o.v[i]);
+    for (int i = 0; i < E; ++i) out[i] = static_cast<float>(o.v[i]);
 }
 
 // Elements i < count; the others are zero.
-template <typename T>
-__device__ inline void load_octet_tail(const T *p, int count, float *out) {
+template <int E, typename T>
+__device__ inline void load_piece_tail(const T *p, int count, float *out) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = i < count ? static_cast<float>(p[i]) : 0.f;
+    for (int i = 0; i < E; ++i) out[i] = i < count ? static_cast<float>(p[i]) : 0.f;
 }
 
-template <typename T>
-__device__ inline void store_octet(T *p, const float *in) {
-    Octet<T> o;
+template <int E, typename T>
+__device__ inline void store_piece(T *p, const float *in) {
+    Piece<T, E> o;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o.v[i] = static_cast<T>(in[i]);
+    for (int i = 0; i < E; ++i) o.v[i] = static_cast<T>(in[i]);
     __builtin_memcpy(p, &o, sizeof(o));
 }
 
-template <typename T>
-__device__ inline void store_octet_tail(T *p, int count, const float *in) {
+template <int E, typename T>
+__device__ inline void store_piece_tail(T *p, int count, const float *in) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < E; ++i)
         if (i < count) p[i] = static_cast<T>(in[i]);
 }
 
