@@ -47,7 +47,8 @@ using f16x8 = f16 __attribute__((ext_vector_type(8)));
 // 16-bit types: a column of the product is a vector.  A code becomes the float
 // 16 + code by placing it in the mantissa's top bits (or'ed into the bits of 16).
 // fp32: a vector is three columns, bf16 parts of 8 bits each (the leading bits,
-// the next, the rest), which add up to x exactly.
+// the next, the rest), which add up to x exactly.  The second and third are
+// kept times 2^16, so that they are bf16 numbers for the smallest x, too.
 template <typename X>
 struct Unit;
 template <>
@@ -66,6 +67,10 @@ struct Unit<bf16> {
 template <>
 struct Unit<float> : Unit<bf16> {
     static constexpr int kParts = 3;
+    static constexpr float kUp = 65536.f;
+    static __device__ inline float join(float lead, float next, float rest) {
+        return fmaf(next + rest, 1 / kUp, lead);
+    }
 };
 template <>
 struct Unit<f16> {
@@ -103,7 +108,7 @@ struct XOctet<float> {
         uint32_t w[3][8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float r = v[i] - lead(v[i]);
+            const float r = (v[i] - lead(v[i])) * Unit<float>::kUp;
             w[0][i] = __builtin_bit_cast(uint32_t, v[i]);
             w[1][i] = __builtin_bit_cast(uint32_t, r);
             w[2][i] = __builtin_bit_cast(uint32_t, r - lead(r));
@@ -119,24 +124,32 @@ struct XOctet<float> {
     }
 };
 
-// One element of the product, in plain arithmetic.
+// One element of the product, in plain arithmetic, an octet of codes at a time
+// (groups are whole octets).
 template <typename X, typename S>
 __device__ float plain_dot(const QuantArgs &a, int32_t r, int32_t v) {
     const X *x = static_cast<const X *>(a.x) + v * a.x_ld;
-    const int64_t tile = r / kQuantRows;
+    const uint32_t *codes =
+        a.codes + static_cast<int64_t>(r / kQuantRows) * a.blocks * kQuantBlockWords;
     float sum = 0.f;
-    for (int c = 0; c < a.C; ++c) {
+    for (int c = 0; c < a.C; c += 8) {
         const int o = c / 8;
-        const uint32_t w =
-            a.codes[(tile * a.blocks + o / kQuantOctets) * kQuantBlockWords +
-                    quant_word(r % kQuantRows, o % kQuantOctets)];
+        const uint32_t w = codes[static_cast<int64_t>(o / kQuantOctets) * kQuantBlockWords +
+                                 quant_word(r % kQuantRows, o % kQuantOctets)];
         const int32_t g = c / a.group;
         const float s = static_cast<float>(
             static_cast<const S *>(a.scales)[quant_scale_at(r, g, a.set, a.sets)]);
         const float z =
             a.zeros ? static_cast<float>(a.zeros[quant_zero_at(r, g, a.set, a.sets)]) : 8.f;
-        sum = fmaf((static_cast<float>(quant_code(w, c & 7)) - z) * s, static_cast<float>(x[c]),
-                   sum);
+        float xs[8];
+        if (c + 8 <= a.C)
+            load_piece<8>(x + c, xs);
+        else
+            load_piece_tail<8>(x + c, a.C - c, xs);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < a.C)
+                sum = fmaf((static_cast<float>(quant_code(w, e)) - z) * s, xs[e], sum);
     }
     return sum;
 }
@@ -270,8 +283,8 @@ struct Lane {
 };
 
 // The product's element (r, v) to memory.  Infinities among the moved codes'
-// products cancel to NaN, and moved codes may pass the range where the codes
-// do not: such an element is computed plainly.
+// products cancel to NaN, and moved codes (and the lower parts of fp32 vectors)
+// may pass the range where the codes do not: such an element is computed plainly.
 template <typename X, typename S>
 __device__ inline void put_element(const QuantArgs &a, int64_t r, int32_t v, float sum) {
     if (!(fabsf(sum) <= 3.402823466e38f)) sum = plain_dot<X, S>(a, static_cast<int32_t>(r), v);
@@ -427,17 +440,16 @@ __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
             const int row = e % (RT * 16), v = e / (RT * 16);
             const int64_t r = static_cast<int64_t>(tile0) * 16 + row;
             if (r >= a.R || v0 + v >= a.n) continue;
-            float sum = 0.f;
+            float sum[U::kParts] = {};
 #pragma unroll
-            for (int p = U::kParts - 1; p >= 0; --p) {
+            for (int p = 0; p < U::kParts; ++p) {
                 const int c = v * U::kParts + p;
-                float s = 0.f;
 #pragma unroll
                 for (int w = 0; w < W; ++w)
-                    s += part(w, row / 16, c / 16, row % 4, (row % 16 / 4) * 16 + c % 16);
-                sum += s;
+                    sum[p] += part(w, row / 16, c / 16, row % 4, (row % 16 / 4) * 16 + c % 16);
             }
-            put_element<X, S>(a, r, v0 + v, sum);
+            if constexpr (U::kParts == 3) sum[0] = U::join(sum[0], sum[1], sum[2]);
+            put_element<X, S>(a, r, v0 + v, sum[0]);
         }
         __syncthreads();  // the next pass's vectors overwrite the parts
     }
@@ -539,14 +551,17 @@ __global__ __launch_bounds__(kWideWaves *kWave) void k_quant_wide(QuantArgs a) {
         }
 
         // A lane holds four neighbouring rows of one column; fp32: the parts of
-        // one vector in its NT tiles, which add up from the smallest.
+        // one vector in its NT tiles.
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             const int64_t r = (static_cast<int64_t>(tile0) + t) * 16 + me.quad * 4;
 #pragma unroll
             for (int u = 0; u < NT / U::kParts; ++u) {
                 f32x4 sum = y[t][u];
-                if constexpr (U::kParts == 3) sum = y[t][2] + y[t][1] + y[t][0];
+                if constexpr (U::kParts == 3)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sum[i] = U::join(y[t][0][i], y[t][1][i], y[t][2][i]);
                 const int32_t v = v0 + u * 16 + me.r16;
                 if (v >= a.n) continue;
                 if (a.splits > 1) {
@@ -594,32 +609,39 @@ void launch(QuantArgs a, hipStream_t s) {
     k_quant_mfma<X, S, Z, GS, RT, NC, W><<<grid, W * kWave, 0, s>>>(a);
 }
 
-// The kernel and its shape by the number of columns and of row tiles.
+// The kernel and its shape by the number of columns and of rows.  Two tiles per
+// workgroup halve what is read of the vectors, one tile makes twice the
+// workgroups, of which each of the 256 CUs wants one or more: up to 4096 rows
+// one tile and eight waves, up to 8192 two tiles and eight waves (one workgroup
+// per CU), up to 16384 one tile and four waves, beyond that two and four.
+//   4096 x 4096, 1 vector     1 x 8: 4.9 us   2 x 8: 5.9
+//   4096 x 4096, 16 vectors   1 x 8: 6.1      2 x 8: 7.4     1 x 4: 6.5
+//   8192 x 8192, 1 vector     1 x 8: 9.3      2 x 8: 9.0
+//   8192 x 11000, 16 vectors  1 x 8: 19.4     2 x 8: 15.7    1 x 4: 18.9
+//   12288 x 8192, 16 vectors  2 x 8: 20.1     1 x 4: 17.5
+//   28672 x 8192, 16 vectors  2 x 8: 37.7     1 x 4: 44.7    2 x 4: 34.9
+// (bf16 and fp16 vectors; tiles x waves).
+template <typename X, typename S, bool Z, int GS, int NC>
+void launch_narrow(const QuantArgs &a, hipStream_t s) {
+    if (a.R <= 16 * 256)
+        launch<X, S, Z, GS, 1, NC, 8>(a, s);
+    else if (a.R <= 16 * 512)
+        launch<X, S, Z, GS, 2, NC, 8>(a, s);
+    else if (a.R <= 16 * 1024)
+        launch<X, S, Z, GS, 1, NC, 4>(a, s);
+    else
+        launch<X, S, Z, GS, 2, NC, 4>(a, s);
+}
+
 template <typename X, typename S, bool Z, int GS>
 void launch_shape(const QuantArgs &a, hipStream_t s) {
     constexpr int P = Unit<X>::kParts;
     const int64_t cols = wide_columns(a.n, P);
-    if (cols > 16) {
-        if constexpr (P == 1)
-            if (cols <= 32) return launch_wide<X, S, Z, GS, 2>(a, s);
-        return launch_wide<X, S, Z, GS, 3>(a, s);
-    }
-    const bool tall = a.R > 16 * 1024, middle = a.R > 16 * 512;
-    if (cols <= 4) {
-        if (tall)
-            launch<X, S, Z, GS, 2, 4, 4>(a, s);
-        else if (middle)
-            launch<X, S, Z, GS, 1, 4, 4>(a, s);
-        else
-            launch<X, S, Z, GS, 1, 4, 8>(a, s);
-    } else {
-        if (tall)
-            launch<X, S, Z, GS, 2, 16, 4>(a, s);
-        else if (middle)
-            launch<X, S, Z, GS, 1, 16, 4>(a, s);
-        else
-            launch<X, S, Z, GS, 1, 16, 8>(a, s);
-    }
+    if (cols <= 4) return launch_narrow<X, S, Z, GS, 4>(a, s);
+    if (cols <= 16) return launch_narrow<X, S, Z, GS, 16>(a, s);
+    if constexpr (P == 1)
+        if (cols <= 32) return launch_wide<X, S, Z, GS, 2>(a, s);
+    launch_wide<X, S, Z, GS, 3>(a, s);
 }
 
 template <typename X>

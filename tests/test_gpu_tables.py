@@ -181,6 +181,60 @@ def test_product_infinities_and_nan(dev, x_dtype):
     assert np.array_equal(got[ok], want[ok])
 
 
+@pytest.mark.parametrize("R", [4096, 4097, 5001, 8192, 8193, 9999, 16384, 16390])
+def test_product_exact_over_heights(dev, R):
+    """Whole numbers as in test_product_exact, over matrices of few and many row tiles, odd
+    ones among them, for one vector up to several passes of them."""
+    rng = np.random.default_rng(R)
+    for C, group, zeros, dtype, n in ((300, 32, True, "fp32", 1), (131, 64, False, "bf16", 3),
+                                      (640, 128, True, "fp16", 9), (1030, 32, False, "fp32", 5),
+                                      (257, 32, True, "bf16", 40), (2100, 64, True, "fp32", 19)):
+        p = Packed(R, C, group, zeros, "bf16", R + C, exact=True)
+        x = rng.integers(-4, 5, (n, C)).astype(np.float64)
+        y0 = rng.integers(-8, 9, (n, R)).astype(np.float64)
+        y = torch.from_numpy(y0).float().to(dev)
+        q = p.build(dev)
+        q.run(torch.from_numpy(x).to(F[dtype]).to(dev), y)
+        assert np.array_equal(y.double().cpu().numpy(), x @ p.w.T + y0), (C, dtype, n)
+        q.close()
+
+
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+def test_product_subnormal_vectors(dev, dtype, n):
+    """Vectors of whole multiples (up to 100) of the type's smallest number keep their bits:
+    in those units every sum is a whole number below 31 * 100 * 130 < 2^24, and for the wide
+    types (smallest 2^-133, 2^-149) the scale of 2^4 keeps y among fp32's own numbers."""
+    R, C = 70, 130
+    unit = {"fp16": 2.0 ** -24, "bf16": 2.0 ** -133, "fp32": 2.0 ** -149}[dtype]
+    p = Packed(R, C, 32, True, "fp32", 4, exact=True)
+    p.scales = torch.full((R, p.G), 16.0)
+    w = 16.0 * (p.q - p.z[:, np.arange(C) // 32])
+    rng = np.random.default_rng(5)
+    k = rng.integers(-100, 101, (n, C)).astype(np.float64)
+    xt = torch.from_numpy(k * unit).to(F[dtype])
+    assert np.array_equal(xt.double().numpy(), k * unit)
+    q = p.build(dev)
+    y = torch.full((n, R), float("nan"), device=dev)
+    q.run(xt.to(dev), y, accumulate=False)
+    assert np.array_equal(y.double().cpu().numpy(), (k @ w.T) * unit)
+
+
+def test_product_nowhere_finite(dev):
+    """Every result infinite or NaN, by one vector and by many."""
+    p = Packed(300, 700, 64, True, "fp16", 6, exact=True)
+    q = p.build(dev)
+    for dtype in ("fp32", "fp16", "bf16"):
+        for n in (1, 33):
+            x = torch.ones(n, 700, dtype=F[dtype])
+            x[:, 5], x[n // 2, 9] = float("inf"), float("nan")
+            y = torch.zeros(n, 300, dtype=F[dtype], device=dev)
+            q.run(x.to(dev), y)
+            with np.errstate(all="ignore"):
+                want = np.stack([(p.w * v).sum(1) for v in x.double().numpy()])
+            assert np.array_equal(y.double().cpu().numpy(), want, equal_nan=True)
+
+
 def test_product_strides_and_rows_behind(dev):
     """Row strides beyond the row, bases at odd elements; what lies between rows stays."""
     p = Packed(37, 301, 32, True, "fp16", 8, exact=True)
@@ -692,6 +746,78 @@ def test_step_captured_and_replayed(dev):
             ws = torch.empty(spmv.lookup_grad_workspace(n, V, D), dtype=torch.uint8, device=dev)
             r2 = token_step(table, q, ids, y2, out2, ws)
             assert torch.equal(rows, r2) and torch.equal(y, y2) and torch.equal(out, out2)
+
+
+def test_split_products_captured_and_at_once(dev):
+    """Products whose columns are split: two streams at once with workspaces of their own, and
+    two graphs with theirs (one allocated while it is captured), replayed in turn with eager
+    products between."""
+    rng = np.random.default_rng(31)
+    p = Packed(150, 9000, 128, True, "bf16", 31, exact=True)
+    q = p.build(dev)
+    assert q.run_workspace(24, torch.bfloat16) > 0
+    xs = [torch.empty(24, 9000, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    ys = [torch.empty(24, 150, device=dev) for _ in range(2)]
+    ws = [torch.empty(q.run_workspace(24, torch.bfloat16), dtype=torch.uint8, device=dev), None]
+
+    def renew():
+        want = []
+        for x, y in zip(xs, ys):
+            v = rng.integers(-4, 5, (24, 9000)).astype(np.float64)
+            x.copy_(torch.from_numpy(v))
+            y.fill_(float("nan"))
+            want.append(torch.from_numpy(v @ p.w.T).float().to(dev))
+        torch.cuda.synchronize()
+        return want
+
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        want = renew()
+        for x, y, w, s in zip(xs, ys, ws, streams):
+            q.run(x, y, accumulate=False, workspace=w, stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, w) for y, w in zip(ys, want))
+    graphs = []
+    for x, y, w in zip(xs, ys, ws):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            q.run(x, y, accumulate=False, workspace=w)
+        graphs.append(g)
+    for _ in range(3):
+        want = renew()
+        for g in graphs:
+            g.replay()
+            eager = torch.zeros(24, 150, device=dev)
+            q.run(xs[0], eager)
+            torch.cuda.synchronize()
+            assert torch.equal(eager, want[0])
+        assert all(torch.equal(y, w) for y, w in zip(ys, want))
+
+
+def test_gradient_of_many_tokens_captured(dev):
+    """The sort's passes over several segments of tiles, replayed on other tokens."""
+    rng = np.random.default_rng(32)
+    V, D, n = 60_000, 3, 300_000
+    ids = torch.empty(n, dtype=torch.int64, device=dev)
+    g = torch.from_numpy(rng.integers(-3, 4, (n, D)).astype(np.float32)).to(dev)
+    out = torch.empty(V, D, device=dev)
+    ws = torch.empty(spmv.lookup_grad_workspace(n, V, D), dtype=torch.uint8, device=dev)
+    ids.copy_(torch.from_numpy(rng.integers(0, V, n)))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        spmv.lookup_grad(g, ids, V, out, workspace=ws)
+    for kind in ("uniform", "language", "runs"):
+        h = skewed_ids(rng, V, n, kind)
+        ids.copy_(torch.from_numpy(h))
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        ok = (h >= 0) & (h < V)
+        want = np.zeros((V, D))
+        np.add.at(want, h[ok], g.double().cpu().numpy()[ok])
+        assert np.array_equal(out.double().cpu().numpy(), want)
+        assert torch.equal(spmv.lookup_grad(g, ids, V), out)
 
 
 def test_streams(dev):
