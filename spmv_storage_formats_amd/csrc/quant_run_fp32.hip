@@ -10,7 +10,9 @@ void quant_run_fp32(const QuantArgs &a, int32_t scale_dtype, hipStream_t s) {
 namespace {
 
 // Parts of the columns of a wide product: enough for four workgroups per CU, of
-// eight blocks at least.
+// eight blocks at least, at most eight (their sums are written and read once
+// more).  8192 x 11000 with 48 vectors: 78 us in one part, 25 + 5 in eight, 26 + 7
+// in sixteen.
 int32_t column_splits(const spmv_quant *q, int32_t n, int32_t x_dtype) {
     const int parts = x_dtype == SPMV_FP32 ? Unit<float>::kParts : 1;
     const int64_t cols = wide_columns(n, parts);

@@ -603,11 +603,13 @@ def test_gradient_random(dev, V, D, n, kind):
 
 
 def test_gradient_many_tokens_and_large_tables(dev):
-    """Merged tiles up to 65,536 tokens; radix passes beyond, in one segment of tiles and in
-    several; three passes with 2^20 + 1 rows and more; ids at the top of the range."""
+    """Merged tiles up to 65,536 tokens (16,384 for up to 1023 rows); radix passes beyond, in
+    one segment of tiles and in several; three passes with 2^20 + 1 rows and more; ids at the
+    top of the range."""
     rng = np.random.default_rng(0)
     for V, D, n in ((2 ** 20 + 1, 4, 150_000), (2 ** 21, 3, 50_000), (131072, 8, 300_001),
-                    (70, 2, 65_536), (70, 2, 65_537), (2 ** 25, 1, 1_000_000)):
+                    (70, 2, 16_384), (70, 2, 16_385), (1023, 2, 20_000), (1024, 2, 20_000),
+                    (5000, 2, 65_536), (5000, 2, 65_537), (2 ** 25, 1, 1_000_000)):
         ids = skewed_ids(rng, V, n, "language")
         ids[::7] = V - 1
         g = rng.integers(-4, 5, (n, D)).astype(np.float32)
