@@ -510,6 +510,13 @@ def _kind(dtype, allowed, name):
     return hit
 
 
+def _fits(what, *sizes):
+    """Refuse sizes that the ABI's int32 arguments would wrap."""
+    for n in sizes:
+        if n > 0x7fffffff:
+            raise SpmvError(5, what)
+
+
 def _rows(t, name, index, rows, cols):
     """A cuda matrix [rows, cols] whose rows are contiguous (rows None: any number), on
     device `index` (None: any): (pointer, row stride, spmv_dtype, end of its memory)."""
@@ -638,6 +645,7 @@ class QuantHandle:
         kind = _kind(dtype, _FLOATS, "dtype")
         hit = self._need.get((n, kind))
         if hit is None:
+            _fits("spmv_quant_run_workspace", n)
             size = ctypes.c_size_t()
             _check(load_library().spmv_quant_run_workspace(self._live(), n, kind,
                                                            ctypes.byref(size)),
@@ -777,6 +785,7 @@ def build_quant(weights, *, group_size: int = 128, zero_points: bool = False, sc
     if not isinstance(weights, torch.Tensor) or weights.dim() != 2:
         raise ValueError("weights must be a matrix")
     R, C = weights.shape
+    _fits("spmv_quant_build", R, C, int(group_size))
     wp, ld, wk, _ = _rows(weights, "weights", None, R, C)
     scale_dtype = scale_dtype or weights.dtype
     sk = _kind(scale_dtype, _FLOATS, "scale_dtype")
@@ -795,10 +804,12 @@ def build_quant_packed(codes, scales, num_cols: int, *, group_size: int = 128, z
     (fp32, fp16 or bf16) and zero_points uint8 like scales (None: 8 everywhere)."""
     import torch
     num_cols, group_size = int(num_cols), int(group_size)
+    _fits("spmv_quant_build_packed", num_cols, group_size)
     cp = _dev(codes, torch.uint8, "codes")
     if codes.dim() != 2 or num_cols < 0 or codes.shape[1] != (num_cols + 1) // 2:
         raise ValueError(f"codes must be [R, {(num_cols + 1) // 2}], got {tuple(codes.shape)}")
     R = codes.shape[0]
+    _fits("spmv_quant_build_packed", R)
     if group_size <= 0:
         raise ValueError("group_size must be positive")
     shape = (R, -(-num_cols // group_size))
@@ -820,11 +831,13 @@ def build_quant_packed(codes, scales, num_cols: int, *, group_size: int = 128, z
 def lookup(table, ids, out=None, *, scale: float = 1.0, dtype=None, stream=None):
     """Rows of a dense table [V, D] by token: out[t, :] = scale * table[ids[t], :], zeros for
     ids outside [0, V) (padded positions).  Returns `out` (default: a new tensor
-    ids.shape + [D] of `dtype`, the table's unless given)."""
+    ids.shape + [D] of `dtype`, the table's unless given).  Records no autograd graph:
+    lookup_grad is its backward pass."""
     import torch
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be a matrix")
     V, D = table.shape
+    _fits("spmv_lookup", V, D)
     tp, t_ld, tk, te = _rows(table, "table", None, V, D)
     index = table.get_device()
     if _elsewhere(index):
@@ -854,6 +867,7 @@ def lookup_grad_workspace(num_tokens: int, num_rows: int, num_cols: int) -> int:
 
 @functools.lru_cache(maxsize=64)
 def _workspace_bytes(n, rows, cols):
+    _fits("spmv_lookup_grad_workspace", rows, cols)
     size = ctypes.c_size_t()
     _check(load_library().spmv_lookup_grad_workspace(rows, cols, n, ctypes.byref(size)),
            "spmv_lookup_grad_workspace")
@@ -881,6 +895,7 @@ def lookup_grad(grad, ids, num_rows: int, out=None, *, scale: float = 1.0,
     gp, g_ld, gk, ge = _rows(_by_token(grad, ids, D, "grad"), "grad", index, n, D)
     if num_rows < 0:
         raise ValueError("num_rows must not be negative")
+    _fits("spmv_lookup_grad", num_rows, D)
     made = []
     if out is None:
         if accumulate:

@@ -451,6 +451,22 @@ def test_binding_refusals(dev):
         q.run(x, y)
 
 
+def test_binding_refuses_sizes_beyond_int32(dev):
+    """2^32 + 5 rows, which an int32 argument would take for 5."""
+    wrap = 2 ** 32 + 5
+    q = Packed(10, 64, 32, False, "fp32", 1).build(dev)
+    ids = torch.zeros(3, dtype=torch.int64, device=dev)
+    one = torch.zeros(1, dtype=torch.bfloat16, device=dev)
+    many = one.as_strided((wrap, 1), (0, 1))
+    for call in (lambda: spmv.lookup(many, ids),
+                 lambda: spmv.lookup_grad(torch.zeros(3, 1, device=dev), ids, wrap),
+                 lambda: spmv.build_quant(many),
+                 lambda: q.run_workspace(wrap, torch.float32)):
+        with pytest.raises(spmv.SpmvError) as e:
+            call()
+        assert e.value.name == "SPMV_ERR_TOO_LARGE"
+
+
 # ------------------------------------------------------------------- lookups
 
 IDS = {"int32": torch.int32, "int64": torch.int64}

@@ -132,6 +132,25 @@ def test_binding_rejects_host_tensors():
         spmv.lookup_grad(torch.zeros(3, 64), ids, 10)
 
 
+def test_binding_refuses_sizes_beyond_int32():
+    """Sizes that an int32 argument would wrap (to 5 rows, a group of 32) are refused."""
+    torch = pytest.importorskip("torch")
+    wrap = 2**32 + 5
+    many = torch.zeros(1, 1).expand(wrap, 1)
+    ids = torch.zeros(3, dtype=torch.int64)
+    for call in (lambda: spmv.lookup_grad_workspace(5, wrap, 8),
+                 lambda: spmv.lookup_grad_workspace(5, 8, wrap),
+                 lambda: spmv.lookup_grad_workspace(wrap, 8, 8),
+                 lambda: spmv.lookup(many, ids),
+                 lambda: spmv.build_quant(many),
+                 lambda: spmv.build_quant(torch.zeros(4, 64), group_size=2**32 + 32),
+                 lambda: spmv.build_quant_packed(None, None, wrap),
+                 lambda: spmv.build_quant_packed(None, None, 64, group_size=2**32 + 32)):
+        with pytest.raises(spmv.SpmvError) as e:
+            call()
+        assert e.value.status == TOO_LARGE
+
+
 def test_binding_overlap_rule():
     """Spans that meet are refused; column ranges of one buffer side by side are not."""
     torch = pytest.importorskip("torch")
