@@ -598,7 +598,8 @@ spmv_status spmv_lookup(int32_t num_rows, int32_t num_cols, const void *table_de
  *   table_dtype.  Without `accumulate` every row is written, zeros where no
  *   token names it; with it, rows that no token names are left untouched.
  *   Tokens outside [0, num_rows) contribute nothing.  The tokens are sorted
- *   (stable radix sort) and each row's gradients summed in token order.
+ *   stably; a row's gradients are summed in an order that depends on the ids
+ *   alone.
  *   n is below 2^31 (SPMV_ERR_TOO_LARGE); n * num_cols may pass it.
  *   workspace_dev: at least spmv_lookup_grad_workspace() bytes, 16-byte
  *   aligned, used until the work on `stream` is done; calls that may overlap

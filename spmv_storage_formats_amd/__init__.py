@@ -684,10 +684,11 @@ class QuantHandle:
                 import torch
                 workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
                 made = (workspace,)
+                wp, size = workspace.data_ptr(), need
             else:
                 _apart(workspace, x, "workspace and x")
                 _apart(workspace, y, "workspace and y")
-            wp, size = _workspace(workspace, need, index)
+                wp, size = _workspace(workspace, need, index)
         _check(load_library().spmv_quant_run(ptr, n, xp, x_ld, xk, yp, y_ld, yk,
                                              1 if accumulate else 0, wp, size,
                                              _stream_of(index, stream, *made)),
@@ -912,10 +913,11 @@ def lookup_grad(grad, ids, num_rows: int, out=None, *, scale: float = 1.0,
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=grad.device)
         made.append(workspace)
+        wp, size = workspace.data_ptr(), need
     else:
         for t, name in ((out, "out"), (grad, "grad"), (ids, "ids")):
             _apart(workspace, t, f"workspace and {name}")
-    wp, size = _workspace(workspace, need, index)
+        wp, size = _workspace(workspace, need, index)
     _check(load_library().spmv_lookup_grad(
         num_rows, D, n, ip, ik, gp, g_ld, gk, scale, 1 if accumulate else 0, op, o_ld, ok, wp,
         size, _stream_of(index, stream, *made)), "spmv_lookup_grad")

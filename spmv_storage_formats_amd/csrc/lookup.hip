@@ -5,9 +5,8 @@
 //   dtable[v, :] = scale * sum over t with ids[t] = v of grad[t, :]
 //
 // The gradient is the product of the transposed selection matrix with the
-// rows of grad.  The tokens are sorted as the COO -> CSR builder sorts row
-// indices (stable radix sort), so that the tokens of one row are neighbours
-// in their own order; the sorted list is cut into chunks of equal length
+// rows of grad.  The tokens are sorted stably, as the COO -> CSR builder sorts
+// row indices, so that the tokens of one row are neighbours in their own order; the sorted list is cut into chunks of equal length
 // whatever its rows, as a segmented sum, and the parts of a row that chunk
 // borders cut are joined in order afterwards.  No atomics: the sums are the
 // same from run to run.

@@ -476,6 +476,9 @@ __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
 // 8192 x 11000, 48 bf16 vectors, 25 us and 5 for the join, of which the matrix unit
 // is busy 7 (three passes of 16 through the kernel above: 34 us; 32 vectors 20 + 5
 // against 25).  Two to four blocks of loads ahead in registers measured 24 to 26 us.
+// Waves x tiles, 48, 32 and 96 vectors, without the join: 4 x 2 24.3, 19.5 and 38.8
+// us; 8 x 1 24.0, 18.4, 42.0; 8 x 2 24.8, 18.9, 43.7; 4 x 4 27.0, 21.7, 48.7; 8 x 4
+// 36.8, 27.6, 40.9.
 constexpr int kWideWaves = 4;
 constexpr int kWideTiles = 2;
 constexpr int kWideRows = kWideWaves * kWideTiles * 16;
