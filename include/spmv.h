@@ -551,6 +551,7 @@ spmv_status spmv_quant_build_packed(spmv_quant **out, int32_t num_rows, int32_t 
 /*
  * spmv_quant_run -- y <- W x + y (accumulate nonzero) or y <- W x, for `n`
  * vectors: row v of x_dev [n, C] gives row v of y_dev [n, R].
+ *   n is at most 2^31 - 49 (SPMV_ERR_TOO_LARGE).
  *   y_dtype is x_dtype or SPMV_FP32.  Products of fp32 vectors keep all 24 bits
  *   of x.  Infinities and NaN in x reach exactly the vectors that hold them.
  *   workspace_dev: at least spmv_quant_run_workspace() bytes, 16-byte aligned

@@ -32,9 +32,9 @@ struct QuantArgs {
 };
 
 // Matrix-unit columns of one pass over n vectors of `parts` columns each: at
-// most 48, the passes even.
+// most kMostPass, the passes even.
 inline int64_t wide_columns(int32_t n, int parts) {
-    const int64_t vecs = 48 / parts;
+    const int64_t vecs = kMostPass / parts;
     const int64_t passes = (n + vecs - 1) / vecs;
     return (n + passes - 1) / passes * parts;
 }
@@ -491,6 +491,7 @@ __global__ __launch_bounds__(kWideWaves *kWave) void k_quant_wide(QuantArgs a) {
     constexpr int NX = kVecs / 16;  // octets of the vectors per thread and block
     constexpr int kBufBytes = NT * 16 * kColBytes;
     static_assert(U::kParts == 1 || U::kParts == NT, "part p of a vector is column p * 16 + v");
+    static_assert(kVecs <= kMostPass, "v0 + kVecs, for any n, is an int32");
     __shared__ __attribute__((aligned(16))) char lds[2 * kBufBytes];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);

@@ -46,6 +46,11 @@ constexpr int kQuantCols = 128;
 constexpr int kQuantOctets = kQuantCols / 8;                 // 16
 constexpr int kQuantBlockWords = kQuantRows * kQuantOctets;  // 256
 
+// Vectors of a product, at most: kernels take them in passes of up to kMostPass
+// and form the indexes of a whole pass, past the last vector, in 32 bits.
+constexpr int kMostPass = 48;
+constexpr int32_t kMostVectors = INT32_MAX - kMostPass;
+
 using bf16 = __bf16;
 using f16 = _Float16;
 

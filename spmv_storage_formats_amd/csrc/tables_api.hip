@@ -149,6 +149,7 @@ spmv_status spmv_quant_build_packed(spmv_quant **out, int32_t R, int32_t C, int3
 spmv_status spmv_quant_run_workspace(const spmv_quant *q, int32_t n, spmv_dtype x_dtype,
                                      size_t *bytes) {
     if (!q || !bytes || n < 0 || !float_dtype(x_dtype)) return SPMV_ERR_INVALID_ARG;
+    if (n > kMostVectors) return SPMV_ERR_TOO_LARGE;
     *bytes = n == 0 || q->R == 0 ? 0 : quant_run_bytes(q, n, x_dtype);
     return SPMV_OK;
 }
@@ -159,6 +160,7 @@ spmv_status spmv_quant_run(const spmv_quant *q, int32_t n, const void *x, int64_
                            void *stream) {
     if (!q || n < 0 || !float_dtype(x_dtype) || (y_dtype != x_dtype && y_dtype != SPMV_FP32))
         return SPMV_ERR_INVALID_ARG;
+    if (n > kMostVectors) return SPMV_ERR_TOO_LARGE;
     if (n == 0 || q->R == 0 || (q->C == 0 && accumulate)) return SPMV_OK;
     if ((q->C > 0 && !x) || !y || (n > 1 && (x_ld < q->C || y_ld < q->R)))
         return SPMV_ERR_INVALID_ARG;

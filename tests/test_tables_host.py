@@ -66,6 +66,21 @@ def test_null_quant_handles(lib):
     assert lib.spmv_quant_destroy(None) == 0
 
 
+@pytest.mark.parametrize("n,status", [
+    (2**31 - 50, 0), (2**31 - 49, 0), (2**31 - 48, TOO_LARGE), (2**31 - 1, TOO_LARGE)])
+def test_products_refuse_vectors_that_a_pass_would_wrap(lib, n, status):
+    """The last pass of up to 48 vectors begins at most at n - 1, and the kernels form the
+    index of its last vector, there or not, in 32 bits.  The handle is a zeroed one: an empty
+    matrix, for which an accepted call does nothing."""
+    empty = ctypes.create_string_buffer(512)
+    size = ctypes.c_size_t(7)
+    assert lib.spmv_quant_run_workspace(empty, n, BF16, ctypes.byref(size)) == status
+    assert size.value == (7 if status else 0)
+    assert lib.spmv_quant_run(empty, n, P, 1, BF16, P, 1, BF16, 1, None, 0, None) == status
+    if status == 0:
+        assert n - 1 + 48 <= 2**31 - 1
+
+
 @pytest.mark.parametrize("change", [
     {"V": -1}, {"D": -1}, {"n": -1}, {"table_dtype": INT32}, {"id": FP32}, {"out_dtype": INT64},
     {"table": None}, {"ids": None}, {"out": None}, {"table_ld": 7}, {"out_ld": 7}])
