@@ -515,6 +515,8 @@ def _fits(what, *sizes):
     for n in sizes:
         if n > 0x7fffffff:
             raise SpmvError(5, what)
+        if n < -0x80000000:
+            raise SpmvError(1, what)
 
 
 def _rows(t, name, index, rows, cols):
@@ -868,7 +870,7 @@ def lookup_grad_workspace(num_tokens: int, num_rows: int, num_cols: int) -> int:
 
 @functools.lru_cache(maxsize=64)
 def _workspace_bytes(n, rows, cols):
-    _fits("spmv_lookup_grad_workspace", rows, cols)
+    _fits("spmv_lookup_grad_workspace", rows, cols, n)    # n: 64 bits there, 31 allowed
     size = ctypes.c_size_t()
     _check(load_library().spmv_lookup_grad_workspace(rows, cols, n, ctypes.byref(size)),
            "spmv_lookup_grad_workspace")

@@ -166,6 +166,23 @@ def test_binding_refuses_sizes_beyond_int32():
         assert e.value.status == TOO_LARGE
 
 
+def test_binding_refuses_sizes_below_int32():
+    """Sizes that an int32 argument would wrap from below (to 5 tokens, 8 rows, a group of 32)
+    are refused as negative ones are; so is a count of tokens that 64 bits would wrap."""
+    torch = pytest.importorskip("torch")
+    wrap = -2**32 + 8
+    for call in (lambda: spmv.lookup_grad_workspace(5, wrap, 8),
+                 lambda: spmv.lookup_grad_workspace(5, 8, wrap),
+                 lambda: spmv.lookup_grad_workspace(-2**64 + 5, 8, 8),
+                 lambda: spmv.build_quant(torch.zeros(4, 64), group_size=-2**32 + 32)):
+        with pytest.raises(spmv.SpmvError) as e:
+            call()
+        assert e.value.status == INVALID
+    with pytest.raises(spmv.SpmvError) as e:
+        spmv.lookup_grad_workspace(2**64 + 5, 8, 8)
+    assert e.value.status == TOO_LARGE
+
+
 def test_binding_overlap_rule():
     """Spans that meet are refused; column ranges of one buffer side by side are not."""
     torch = pytest.importorskip("torch")
