@@ -662,7 +662,11 @@ class QuantHandle:
         run_workspace() bytes, for this call alone until its work is done (default:
         allocated for the call where it needs one)."""
         ptr = self._live()
-        if x.dim() == 1 and y.dim() == 1:
+        try:
+            one = x.dim() == 1 and y.dim() == 1
+        except AttributeError:
+            raise TypeError("x and y must be cuda tensors") from None
+        if one:
             self.run(x[None], y[None], accumulate=accumulate, workspace=workspace,
                      stream=stream)
             return y
@@ -688,9 +692,9 @@ class QuantHandle:
                 made = (workspace,)
                 wp, size = workspace.data_ptr(), need
             else:
+                wp, size = _workspace(workspace, need, index)
                 _apart(workspace, x, "workspace and x")
                 _apart(workspace, y, "workspace and y")
-                wp, size = _workspace(workspace, need, index)
         _check(load_library().spmv_quant_run(ptr, n, xp, x_ld, xk, yp, y_ld, yk,
                                              1 if accumulate else 0, wp, size,
                                              _stream_of(index, stream, *made)),
@@ -905,7 +909,7 @@ def lookup_grad(grad, ids, num_rows: int, out=None, *, scale: float = 1.0,
             raise ValueError("accumulate needs out")
         out = torch.empty(num_rows, D, dtype=dtype or grad.dtype, device=grad.device)
         made.append(out)
-    elif dtype is not None and out.dtype != dtype:
+    elif dtype is not None and isinstance(out, torch.Tensor) and out.dtype != dtype:
         raise TypeError(f"out is {out.dtype}, dtype says {dtype}")
     op, o_ld, ok, oe = _rows(out, "out", index, num_rows, D)
     if not made:
@@ -917,9 +921,9 @@ def lookup_grad(grad, ids, num_rows: int, out=None, *, scale: float = 1.0,
         made.append(workspace)
         wp, size = workspace.data_ptr(), need
     else:
+        wp, size = _workspace(workspace, need, index)
         for t, name in ((out, "out"), (grad, "grad"), (ids, "ids")):
             _apart(workspace, t, f"workspace and {name}")
-        wp, size = _workspace(workspace, need, index)
     _check(load_library().spmv_lookup_grad(
         num_rows, D, n, ip, ik, gp, g_ld, gk, scale, 1 if accumulate else 0, op, o_ld, ok, wp,
         size, _stream_of(index, stream, *made)), "spmv_lookup_grad")

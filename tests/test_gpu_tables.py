@@ -451,6 +451,28 @@ def test_binding_refusals(dev):
         q.run(x, y)
 
 
+def test_binding_refuses_what_is_no_tensor(dev):
+    """Outputs and workspaces that are no cuda tensors are of a wrong type, as inputs are."""
+    p = Packed(90, 6000, 64, True, "bf16", 21)
+    q = p.build(dev)
+    x = torch.zeros(40, 6000, dtype=torch.bfloat16, device=dev)
+    y = torch.zeros(40, 90, device=dev)
+    ids = torch.zeros(4, dtype=torch.int32, device=dev)
+    g = torch.zeros(4, 8, device=dev)
+    need = spmv.lookup_grad_workspace(4, 5, 8)
+    for call in (lambda: q.run(x, y, workspace=bytearray(1 << 20)),
+                 lambda: q.run(x, y, workspace=torch.zeros(1 << 20, dtype=torch.uint8)),
+                 lambda: q.run(x, y.cpu()),
+                 lambda: q.run(x, None),
+                 lambda: spmv.lookup_grad(g, ids, 5, [0.0], dtype=torch.float32),
+                 lambda: spmv.lookup_grad(g, ids, 5, torch.zeros(5, 8)),
+                 lambda: spmv.lookup_grad(g, ids, 5, workspace=bytearray(need)),
+                 lambda: spmv.lookup_grad(g, None, 5),
+                 lambda: spmv.lookup(g, [0, 1])):
+        with pytest.raises(TypeError):
+            call()
+
+
 def test_binding_refuses_sizes_beyond_int32(dev):
     """2^32 + 5 rows, which an int32 argument would take for 5."""
     wrap = 2 ** 32 + 5

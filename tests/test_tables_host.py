@@ -147,6 +147,18 @@ def test_binding_rejects_host_tensors():
         spmv.lookup_grad(torch.zeros(3, 64), ids, 10)
 
 
+def test_product_refuses_what_is_no_tensor():
+    torch = pytest.importorskip("torch")
+    q = spmv.QuantHandle.__new__(spmv.QuantHandle)     # refused before the handle is used
+    q._ptr, q.device = P, torch.device("cuda:0")
+    try:
+        for x, y in ((None, None), ([1.0], torch.zeros(1)), (torch.zeros(1), 3)):
+            with pytest.raises(TypeError):
+                q.run(x, y)
+    finally:
+        q._ptr = None
+
+
 def test_binding_refuses_sizes_beyond_int32():
     """Sizes that an int32 argument would wrap (to 5 rows, a group of 32) are refused."""
     torch = pytest.importorskip("torch")
