@@ -72,6 +72,9 @@ def sum_bound(p, x):
     return (p.C + p.C / 32 + 64) * 2.0 ** -24 * (p.wide @ np.abs(x).T).T
 
 
+# matrix heights at which the kernel's shape changes: few rows, and odd ones past each bound
+HEIGHTS = [48, 4097, 8193, 16390]
+
 SHAPES = [(1, 1, 32), (1, 7, 32), (3, 32, 32), (16, 128, 32), (17, 130, 64), (15, 255, 128),
           (33, 256, 64), (64, 257, 32), (100, 1000, 128), (48, 4096, 128), (31, 2750, 32),
           (130, 777, 256), (20, 5000, 384), (300, 515, 64), (5, 3000, 4096)]
@@ -150,6 +153,71 @@ def test_product_fp32_keeps_all_bits_of_x(dev):
     q.run(torch.from_numpy(x).to(dev), y)
     want = np.stack([val[i].astype(np.float64) * p.s64[:, c // 32] for i, c in enumerate(at)])
     assert np.array_equal(y.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("n", [1, 3, 5])
+@pytest.mark.parametrize("R", HEIGHTS)
+def test_product_fp32_keeps_all_bits_of_few_vectors(dev, R, n):
+    """As above, for the numbers of vectors whose parts are 3, 9 and 15 columns of one pass, at
+    the matrix heights of every kernel shape."""
+    C = 420
+    p = Packed(R, C, 32, False, "bf16", 3, exact=True)
+    p.codes = torch.full((R, C // 2), 0x99, dtype=torch.uint8)
+    q = p.build(dev)
+    rng = np.random.default_rng(R + n)
+    for turn in range(6):
+        at = rng.integers(0, C, n)
+        val = (1 + rng.random(n)) * 2.0 ** rng.integers(-80, 81, n) * rng.choice([-1, 1], n)
+        x = np.zeros((n, C), np.float32)
+        x[np.arange(n), at] = val
+        y = q.run(torch.from_numpy(x).to(dev), torch.zeros(n, R, device=dev))
+        want = x[np.arange(n), at].astype(np.float64)[:, None] * p.s64[:, at // 32].T
+        assert np.array_equal(y.double().cpu().numpy(), want), (turn, at)
+
+
+@pytest.mark.parametrize("n", [1, 3, 5, 6, 16, 17])
+@pytest.mark.parametrize("R", HEIGHTS)
+def test_product_fp32_of_24_bit_vectors(dev, R, n):
+    """Dense vectors of all 24 bits, with only the join of their parts rounded.  |x| = 2^23 +
+    2^16 a + 2^15 + b, a < 2^7, b < 2^15: the parts are whole multiples below 2^8 of 2^16, 2^8
+    and 1.  In those units a group's moved sums are below 31 * 2^8 * 128 < 2^20, and in a
+    quarter of them (scales 2^-2..2^2) every sum over the columns is below 16 * 15 * 2^8 * C <=
+    2^24 for C <= 273: exact.  What is left are the additions of the second to the third part
+    (together below 2^-7 |x|) and of both to the first, 2^-24 of their results each."""
+    C, u = 270, 2.0 ** -24
+    rng = np.random.default_rng(R + n)
+    for group, zeros in ((32, True), (64, False), (128, True)):
+        p = Packed(R, C, group, zeros, "fp32", R + group, exact=True)
+        x = (2.0 ** 23 + 2.0 ** 16 * rng.integers(0, 2 ** 7, (n, C)) + 2 ** 15
+             + rng.integers(0, 2 ** 15, (n, C))) * rng.choice([-1, 1], (n, C))
+        q = p.build(dev)
+        y = torch.full((n, R), float("nan"), device=dev)
+        q.run(torch.from_numpy(x).float().to(dev), y, accumulate=False)
+        want = x @ p.w.T
+        tol = u * (np.abs(want) + 2.0 ** -7 * (np.abs(x) @ np.abs(p.w).T)) * (1 + 2 * u)
+        err = np.abs(y.double().cpu().numpy() - want)
+        assert np.all(err <= tol), (group, np.max(err / tol))
+        q.close()
+
+
+@pytest.mark.parametrize("n", [1, 4, 16, 17, 33, 48])
+@pytest.mark.parametrize("R", HEIGHTS)
+def test_product_exact_with_all_bits_of_16_bit_vectors(dev, R, n):
+    """Whole numbers of all 8 bits (bf16) and 11 bits (fp16), scales of 1: a group's moved sums
+    are below 31 * 2047 * 128 < 2^23, y below 15 * 2047 * C < 2^24 for C <= 546."""
+    C = 530
+    rng = np.random.default_rng(R + n)
+    for dtype, low in (("bf16", 128), ("fp16", 1024)):
+        for group, zeros in ((32, False), (64, True), (128, True)):
+            p = Packed(R, C, group, zeros, "fp16", R + group, exact=True)
+            p.scales = torch.ones_like(p.scales)
+            x = rng.integers(low, 2 * low, (n, C)) * rng.choice([-1.0, 1.0], (n, C))
+            q = p.build(dev)
+            y = torch.full((n, R), float("nan"), device=dev)
+            q.run(torch.from_numpy(x).to(F[dtype]).to(dev), y, accumulate=False)
+            want = x @ (p.q - p.z[:, np.arange(C) // group]).T.astype(np.float64)
+            assert np.array_equal(y.double().cpu().numpy(), want), (dtype, group)
+            q.close()
 
 
 @pytest.mark.parametrize("x_dtype", ["fp32", "fp16", "bf16"])
