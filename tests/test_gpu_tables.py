@@ -221,6 +221,37 @@ def test_product_exact_with_all_bits_of_16_bit_vectors(dev, R, n):
 
 
 @pytest.mark.parametrize("x_dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("R,C,group", [(50, 33, 32), (70, 1000, 64), (4100, 640, 128),
+                                       (30, 5000, 384)])
+def test_product_of_codes_equal_to_their_zero_points(dev, R, C, group, x_dtype):
+    """W = 0: the moved codes' sums and the moved zero points' cancel.  Exactly where they are
+    whole numbers below 2^24; else up to the roundings (as many as at sum_bound) of sums of
+    |s| (32 + code + zero) |x|.  A row whose codes differ in one column is that column's."""
+    rng = np.random.default_rng(R + C)
+    p = Packed(R, C, group, True, "fp32", R + C)
+    cols = np.arange(C) // group
+    q = p.z[:, cols].copy()
+    q[3, C // 2] = (q[3, C // 2] + 5) % 16
+    w3 = p.s64[3, C // 2 // group] * (q[3, C // 2] - p.z[3, C // 2 // group])
+    full = np.zeros((R, C + (C & 1)), np.uint8)
+    full[:, :C] = q
+    p.codes = torch.from_numpy(full[:, 0::2] | (full[:, 1::2] << 4))
+    h = p.build(dev)
+    for n in (1, 5, 16, 20, 40):
+        x = torch.from_numpy(rng.integers(-4, 5, (n, C))).to(F[x_dtype])
+        y = h.run(x.to(dev), torch.full((n, R), float("nan"), device=dev), accumulate=False)
+        y[:, 3] = 0
+        assert (y == 0).all()
+        x = torch.from_numpy(rng.standard_normal((n, C))).to(F[x_dtype])
+        y = h.run(x.to(dev), y, accumulate=False).double().cpu().numpy()
+        x = x.double().numpy()
+        moved = p.s64[:, cols] * (32 + q + p.z[:, cols])
+        tol = (C + C / 32 + 64) * 2.0 ** -24 * (np.abs(x) @ moved.T)
+        y[:, 3] -= w3 * x[:, C // 2]
+        assert np.all(np.abs(y) <= tol), np.max(np.abs(y) / tol)
+
+
+@pytest.mark.parametrize("x_dtype", ["fp32", "fp16", "bf16"])
 def test_product_infinities_and_nan(dev, x_dtype):
     """An infinity in x gives rows +-inf by its weight's sign, NaN where the weight is zero; a
     NaN gives NaN; the other vectors do not see them; nor do overflowing moved codes (31 * x)
