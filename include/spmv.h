@@ -604,8 +604,10 @@ spmv_status spmv_lookup(int32_t num_rows, int32_t num_cols, const void *table_de
  *   table_dtype.  Without `accumulate` every row is written, zeros where no
  *   token names it; with it, rows that no token names are left untouched.
  *   Tokens outside [0, num_rows) contribute nothing.  The tokens are sorted
- *   stably; a row's gradients are summed in an order that depends on the ids
- *   alone.
+ *   stably; the order in which a row's gradients are summed depends on the ids,
+ *   num_rows and num_cols alone, not on types, strides or the workspace.  (The
+ *   sums are taken in parts whose length follows from n and num_cols: the same
+ *   columns in a narrower table may round differently.)
  *   n is below 2^31 (SPMV_ERR_TOO_LARGE); n * num_cols may pass it.
  *   workspace_dev: at least spmv_lookup_grad_workspace() bytes, 16-byte
  *   aligned, used until the work on `stream` is done; calls that may overlap

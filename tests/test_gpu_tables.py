@@ -739,6 +739,34 @@ def test_gradient_random(dev, V, D, n, kind):
         assert torch.equal(again, out)          # the same from run to run
 
 
+@pytest.mark.parametrize("V,D,n", [(9, 40, 500), (50, 301, 3000), (2000, 70, 20000),
+                                   (700, 12, 70000)])
+def test_gradient_order_does_not_depend_on_types_or_strides(dev, V, D, n):
+    """Values that all three types hold, whose fp32 sums are rounded: the sums are equal bit for
+    bit whatever the types of gradients and ids, the strides, and what the workspace held."""
+    rng = np.random.default_rng(n)
+    h = skewed_ids(rng, V, n, "language")
+    ids = torch.from_numpy(h).to(dev)
+    # 8 bits, exponents far apart: in bf16, fp16 (2^-14 and above) and fp32 alike
+    g = (rng.integers(128, 256, (n, D)) * 2.0 ** rng.integers(-21, 5, (n, D))
+         * rng.choice([-1, 1], (n, D)))
+    first = spmv.lookup_grad(torch.from_numpy(g).float().to(dev), ids, V)
+    want, mag, cnt = grad64(g, h, V, 1.0)
+    assert np.all(np.abs(first.double().cpu().numpy() - want)
+                  <= (cnt[:, None] + 2) * 2.0 ** -24 * mag)
+    need = spmv.lookup_grad_workspace(n, V, D)
+    for gd, idd, fill, pad in (("fp16", "int32", 255, 0), ("bf16", "int64", 1, 3),
+                               ("fp32", "int32", 7, 5)):
+        buf = torch.zeros(n, D + 2 * pad, dtype=F[gd], device=dev)
+        gt = buf[:, pad:pad + D]
+        gt.copy_(torch.from_numpy(g))
+        assert torch.equal(gt.double().cpu(), torch.from_numpy(g))
+        out = torch.empty(V, D + pad, device=dev)[:, :D]
+        ws = torch.full((need,), fill, dtype=torch.uint8, device=dev)
+        spmv.lookup_grad(gt, ids.to(IDS[idd]), V, out, workspace=ws)
+        assert torch.equal(out, first), gd
+
+
 def test_gradient_many_tokens_and_large_tables(dev):
     """Merged tiles up to 65,536 tokens (16,384 for up to 1023 rows); radix passes beyond, in
     one segment of tiles and in several; three passes with 2^20 + 1 rows and more; ids at the
