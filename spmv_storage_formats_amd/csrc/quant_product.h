@@ -25,7 +25,7 @@ struct QuantArgs {
     int64_t y_ld;
     int32_t accumulate;
     int32_t y_fp32;
-    int32_t passes;       // groups of vectors
+    int32_t passes;       // groups of vectors (wide products)
     int32_t splits;       // parts of the columns, each a workgroup's (wide products)
     float *partial;       // their sums [splits][n][R], where there are several
     int32_t group_shift;  // log2 of the group, or -1
@@ -352,7 +352,7 @@ template <typename X, typename S, bool Z, int GS, int RT, int NC, int W>
 __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
     using U = Unit<X>;
     constexpr int NT = (NC + 15) / 16;
-    constexpr int kVecs = NC / U::kParts;       // vectors per pass
+    constexpr int kVecs = NC / U::kParts;       // vectors, at most: a.n <= kVecs
     constexpr int NX = (kVecs + 3) / 4;         // octets of them per lane and block
     constexpr int kWaveBytes = NT * 16 * kColBytes;
     static_assert(kWaveBytes >= RT * NT * 4 * kWave * 4, "the sums reuse the vectors' part");
@@ -363,107 +363,102 @@ __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
     const int r16 = me.r16, quad = me.quad;
     char *const mine = lds + wave * kWaveBytes;
     const int32_t tiles = (a.R - 1) / 16 + 1;
-    for (int32_t pass = blockIdx.y; pass < a.passes; pass += gridDim.y) {
-        const int32_t tile0 = static_cast<int32_t>(blockIdx.x) * RT;
-        const int32_t v0 = pass * kVecs;
-        // This lane's share of the vectors.  Slots past the last repeat it: the
-        // sums of their columns go nowhere.
-        const X *xp[NX];
+    const int32_t tile0 = static_cast<int32_t>(blockIdx.x) * RT;
+    // This lane's share of the vectors.  Slots past the last repeat it: the
+    // sums of their columns go nowhere.
+    const X *xp[NX];
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+        int32_t v = i * 4 + quad;
+        v = v < kVecs && v < a.n ? v : a.n - 1;
+        xp[i] = static_cast<const X *>(a.x) + v * a.x_ld + r16 * 8;
+    }
+    int64_t tile[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) tile[t] = tile0 + t < tiles ? tile0 + t : tiles - 1;
+    f32x4 y[RT][NT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int u = 0; u < NT; ++u) y[t][u] = f32x4{0, 0, 0, 0};
+
+    using B = Block<X, S, GS, RT, NX>;
+    // The vectors' octets to LDS: octet r16 of vector i * 4 + quad.
+    auto stage = [&](const B &b) {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-            int32_t v = i * 4 + quad;
-            v = v < kVecs ? v0 + v : v0;
-            v = v < a.n ? v : a.n - 1;
-            xp[i] = static_cast<const X *>(a.x) + v * a.x_ld + r16 * 8;
+            if (i * 4 + quad >= kVecs) continue;
+            u32x4 part[U::kParts];
+            b.x[i].split(part);
+#pragma unroll
+            for (int p = 0; p < U::kParts; ++p)
+                *reinterpret_cast<u32x4 *>(
+                    mine + ((i * 4 + quad) * U::kParts + p) * kColBytes + r16 * 16) = part[p];
         }
-        int64_t tile[RT];
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    };
+    const int full = a.C / kQuantCols;  // blocks with all their columns
+    const int count = wave < full ? (full - wave + W - 1) / W : 0;
+    if (count > 0) {
+        // No branch around a load: the last block is loaded again instead.
+        B cur, nxt;
+        int block = wave;
+        me.load(a, tile, block, cur);
 #pragma unroll
-        for (int t = 0; t < RT; ++t) tile[t] = tile0 + t < tiles ? tile0 + t : tiles - 1;
-        f32x4 y[RT][NT];
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-            for (int u = 0; u < NT; ++u) y[t][u] = f32x4{0, 0, 0, 0};
-
-        using B = Block<X, S, GS, RT, NX>;
-        // The vectors' octets to LDS: octet r16 of vector i * 4 + quad.
-        auto stage = [&](const B &b) {
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int i = 0; i < NX; ++i) {
-                if (i * 4 + quad >= kVecs) continue;
-                u32x4 part[U::kParts];
-                b.x[i].split(part);
-#pragma unroll
-                for (int p = 0; p < U::kParts; ++p)
-                    *reinterpret_cast<u32x4 *>(
-                        mine + ((i * 4 + quad) * U::kParts + p) * kColBytes + r16 * 16) = part[p];
-            }
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        };
-        const int full = a.C / kQuantCols;  // blocks with all their columns
-        const int count = wave < full ? (full - wave + W - 1) / W : 0;
-        if (count > 0) {
-            // No branch around a load: the last block is loaded again instead.
-            B cur, nxt;
-            int block = wave;
-            me.load(a, tile, block, cur);
-#pragma unroll
-            for (int i = 0; i < NX; ++i) cur.x[i].load(xp[i] + block * kQuantCols);
+        for (int i = 0; i < NX; ++i) cur.x[i].load(xp[i] + block * kQuantCols);
 #pragma unroll 1
-            for (int i = 1; i <= count; ++i) {
-                stage(cur);
-                block += i < count ? W : 0;
-                me.load(a, tile, block, nxt);
+        for (int i = 1; i <= count; ++i) {
+            stage(cur);
+            block += i < count ? W : 0;
+            me.load(a, tile, block, nxt);
 #pragma unroll
-                for (int u = 0; u < NX; ++u) nxt.x[u].load(xp[u] + block * kQuantCols);
-                __builtin_amdgcn_sched_barrier(0);
-                me.multiply(cur, mine, y);
-                cur = nxt;
-            }
+            for (int u = 0; u < NX; ++u) nxt.x[u].load(xp[u] + block * kQuantCols);
+            __builtin_amdgcn_sched_barrier(0);
+            me.multiply(cur, mine, y);
+            cur = nxt;
         }
-        if (a.C % kQuantCols && full % W == wave) {
-            int left = a.C - full * kQuantCols - r16 * 8;
-            asm volatile("" : "+v"(left));  // keeps the tail's comparisons out of the item loop
-            B b;
-            me.load(a, tile, full, b);
+    }
+    if (a.C % kQuantCols && full % W == wave) {
+        int left = a.C - full * kQuantCols - r16 * 8;
+        asm volatile("" : "+v"(left));  // keeps the tail's comparisons out of the item loop
+        B b;
+        me.load(a, tile, full, b);
 #pragma unroll
-            for (int i = 0; i < NX; ++i) b.x[i].load_tail(xp[i] + full * kQuantCols, left);
-            stage(b);
-            me.multiply(b, mine, y);
-        }
+        for (int i = 0; i < NX; ++i) b.x[i].load_tail(xp[i] + full * kQuantCols, left);
+        stage(b);
+        me.multiply(b, mine, y);
+    }
 
-        // the waves' parts, then each element's sum
-        auto part = [&](int w, int t, int u, int i, int l) -> float & {
-            return reinterpret_cast<float *>(lds + w * kWaveBytes)[((t * NT + u) * 4 + i) * kWave +
-                                                                   l];
-        };
-        __syncthreads();
+    // the waves' parts, then each element's sum
+    auto part = [&](int w, int t, int u, int i, int l) -> float & {
+        return reinterpret_cast<float *>(lds + w * kWaveBytes)[((t * NT + u) * 4 + i) * kWave +
+                                                               l];
+    };
+    __syncthreads();
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
-            for (int u = 0; u < NT; ++u)
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) part(wave, t, u, i, lane) = y[t][u][i];
-        __syncthreads();
-        for (int e = threadIdx.x; e < kVecs * RT * 16; e += W * kWave) {
-            const int row = e % (RT * 16), v = e / (RT * 16);
-            const int64_t r = static_cast<int64_t>(tile0) * 16 + row;
-            if (r >= a.R || v0 + v >= a.n) continue;
-            float sum[U::kParts] = {};
+            for (int i = 0; i < 4; ++i) part(wave, t, u, i, lane) = y[t][u][i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < kVecs * RT * 16; e += W * kWave) {
+        const int row = e % (RT * 16), v = e / (RT * 16);
+        const int64_t r = static_cast<int64_t>(tile0) * 16 + row;
+        if (r >= a.R || v >= a.n) continue;
+        float sum[U::kParts] = {};
 #pragma unroll
-            for (int p = 0; p < U::kParts; ++p) {
-                const int c = v * U::kParts + p;
+        for (int p = 0; p < U::kParts; ++p) {
+            const int c = v * U::kParts + p;
 #pragma unroll
-                for (int w = 0; w < W; ++w)
-                    sum[p] += part(w, row / 16, c / 16, row % 4, (row % 16 / 4) * 16 + c % 16);
-            }
-            if constexpr (U::kParts == 3) sum[0] = U::join(sum[0], sum[1], sum[2]);
-            put_element<X, S>(a, r, v0 + v, sum[0]);
+            for (int w = 0; w < W; ++w)
+                sum[p] += part(w, row / 16, c / 16, row % 4, (row % 16 / 4) * 16 + c % 16);
         }
-        __syncthreads();  // the next pass's vectors overwrite the parts
+        if constexpr (U::kParts == 3) sum[0] = U::join(sum[0], sum[1], sum[2]);
+        put_element<X, S>(a, r, v, sum[0]);
     }
 }
 
@@ -622,11 +617,8 @@ void launch_wide(QuantArgs a, hipStream_t s) {
 }
 
 template <typename X, typename S, bool Z, int GS, int RT, int NC, int W>
-void launch(QuantArgs a, hipStream_t s) {
-    constexpr int kVecs = NC / Unit<X>::kParts;
-    a.passes = a.n / kVecs + (a.n % kVecs != 0);
-    const dim3 grid(grid_for(a.R, RT * 16), std::min(a.passes, 65535));
-    k_quant_mfma<X, S, Z, GS, RT, NC, W><<<grid, W * kWave, 0, s>>>(a);
+void launch(const QuantArgs &a, hipStream_t s) {
+    k_quant_mfma<X, S, Z, GS, RT, NC, W><<<grid_for(a.R, RT * 16), W * kWave, 0, s>>>(a);
 }
 
 // The kernel and its shape by the number of columns and of rows.  Two tiles per
@@ -656,6 +648,7 @@ void launch_narrow(const QuantArgs &a, hipStream_t s) {
 template <typename X, typename S, bool Z, int GS>
 void launch_shape(const QuantArgs &a, hipStream_t s) {
     constexpr int P = Unit<X>::kParts;
+    // 16 or fewer are those of one pass: where there are several, each has 25 at least
     const int64_t cols = wide_columns(a.n, P);
     if (cols <= 4) return launch_narrow<X, S, Z, GS, 4>(a, s);
     if (cols <= 16) return launch_narrow<X, S, Z, GS, 16>(a, s);

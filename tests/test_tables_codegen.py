@@ -71,3 +71,17 @@ def test_conditions_are_read_where_they_were_set(listings, name):
 @pytest.mark.parametrize("name", SOURCES[1:])
 def test_no_global_atomics(listings, name):
     assert not re.search(r"\b(global|flat|buffer)_atomic_", listings[name])
+
+
+@pytest.mark.parametrize("name", SOURCES[1:4])
+def test_narrow_products_have_a_grid_of_tiles_alone(listings, name):
+    """One pass covers the vectors of every product that k_quant_mfma serves, so its code
+    reads no second index of a workgroup; k_quant_wide's reads all three."""
+    found = re.findall(r"\.amdhsa_kernel (\S+)(.*?)\.end_amdhsa_kernel", listings[name], re.S)
+    ids = {"k_quant_mfma": "100", "k_quant_wide": "111"}
+    for kernel, want in ids.items():
+        bodies = [b for k, b in found if kernel in k]
+        assert bodies
+        for b in bodies:
+            got = [re.search(rf"workgroup_id_{d} (\d)", b).group(1) for d in "xyz"]
+            assert "".join(got) == want
