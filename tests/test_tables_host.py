@@ -133,6 +133,25 @@ def test_workspace_size(lib):
         spmv.lookup_grad_workspace(-1, 10, 8)
 
 
+def test_committed_profile_matches_the_kernel_sources():
+    """The kernel times and counters of profiles/weight_tables_kernel_trace.md were taken on
+    the committed code: the hash that it carries is that of the sources that the weight
+    tables' kernels are compiled from, comments and whitespace removed."""
+    import hashlib
+    import os
+    import re
+    package = os.path.dirname(spmv.__file__)
+    h = hashlib.sha256()
+    for f in ("internal.h", "tables.h", "quant.hip", "quant_product.h", "quant_run_bf16.hip",
+              "quant_run_fp16.hip", "quant_run_fp32.hip", "lookup.hip"):
+        text = open(os.path.join(package, "csrc", f), encoding="utf-8").read()
+        text = re.sub(r"//[^\n]*", " ", re.sub(r"/\*.*?\*/", " ", text, flags=re.S))
+        h.update(" ".join(text.split()).encode())
+    profile = open(os.path.join(package, "..", "profiles", "weight_tables_kernel_trace.md"),
+                   encoding="utf-8").read()
+    assert f"kernel_source_sha: {h.hexdigest()[:16]}" in profile
+
+
 def test_binding_rejects_host_tensors():
     torch = pytest.importorskip("torch")
     w = torch.zeros(4, 64)
