@@ -6,10 +6,11 @@
 //
 // The gradient is the product of the transposed selection matrix with the
 // rows of grad.  The tokens are sorted stably, as the COO -> CSR builder sorts
-// row indices, so that the tokens of one row are neighbours in their own order; the sorted list is cut into chunks of equal length
-// whatever its rows, as a segmented sum, and the parts of a row that chunk
-// borders cut are joined in order afterwards.  No atomics: the sums are the
-// same from run to run.
+// row indices, so that the tokens of one row are neighbours in their own order;
+// the sorted list is cut into chunks of equal length whatever its rows, as a
+// segmented sum, and the parts of a row that chunk borders cut are joined in
+// order afterwards.  No sum is made by atomics (only the sort's counts of
+// tokens are, in LDS): the sums are the same from run to run.
 #include "tables.h"
 
 namespace spmv {
@@ -594,7 +595,10 @@ __global__ __launch_bounds__(kThreads) void k_grad_chunks(
 // following chunks up to the one where the row ends.  kJoinParts waves take
 // consecutive shares of the parts, which are then added in order.  Bound by
 // the latency of a frequent token's many parts: 12 us for 32768 tokens of a
-// natural-language spread, 2048 columns.
+// natural-language spread, 2048 columns.  A row's parts are one workgroup's per
+// 256 columns: the whole gradient of 65536 tokens of a single row, 2048
+// columns, takes 138 us (126 where the tokens spread by rank over 1000 rows), of
+// 2^20 such tokens 1.85 ms (1.43).
 template <typename T>
 __global__ __launch_bounds__(kJoinThreads) void k_grad_join(
     int32_t V, int32_t D, int64_t n, const uint32_t *__restrict__ keys, float scale,

@@ -345,9 +345,11 @@ __device__ inline void put_four(const QuantArgs &a, int64_t r, int32_t v, f32x4 
 // loaded along their length (neighbouring lanes, neighbouring bytes), read as
 // matrix operands.  GS: columns per scale, at most 128.  Z: zero points.
 // Bound by memory where the matrix is large: 128000 x 4096, one bf16 vector, 271
-// MB in 47 us, 5.8 TB/s (the matrix unit, 16 columns wide, is busy a quarter of
-// that).  Smaller ones have too few bytes in flight for the time that a load takes:
-// 12288 x 8192, 16 vectors, 56 MB in 16 us; 4096 x 4096, one vector, 5 us.
+// MB in 45 us, 6.0 TB/s (vector instructions busy 24 us of that, the matrix unit,
+// 16 columns wide, 12).  Smaller ones have too few bytes in flight for the time
+// that a load takes: 12288 x 8192, 16 vectors, 56 MB in 22 us (14 where the
+// last-level cache holds the matrix), half of its waves' time waiting; 4096 x
+// 4096, one vector, four blocks per wave one after another, 5.4 us, 72 %.
 template <typename X, typename S, bool Z, int GS, int RT, int NC, int W>
 __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
     using U = Unit<X>;
@@ -466,10 +468,11 @@ __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
 // block's vectors, which all threads bring to LDS (two buffers, one barrier per
 // block): a vector is read once per kWideRows rows instead of once per 16 RT.
 // Where that leaves too few workgroups, the matrix's columns are split among
-// `splits` of them, whose sums meet in the workspace.  Bound by the matrix unit
-// and the vector instructions together, which two waves per SIMD overlap little:
-// 8192 x 11000, 48 bf16 vectors, 25 us and 5 for the join, of which the matrix unit
-// is busy 7 (three passes of 16 through the kernel above: 34 us; 32 vectors 20 + 5
+// `splits` of them, whose sums meet in the workspace.  8192 x 11000, 48 bf16
+// vectors: 26 us and 5 for the join, of which vector instructions are busy 8 and the
+// matrix unit 7, so bound by neither: waves wait 38 % of their time for loads and at
+// the block's barrier, and two waves per SIMD hide little (three passes of 16
+// through the kernel above: 34 us; 32 vectors 20 + 5
 // against 25).  Two to four blocks of loads ahead in registers measured 24 to 26 us.
 // Waves x tiles, 48, 32 and 96 vectors, without the join: 4 x 2 24.3, 19.5 and 38.8
 // us; 8 x 1 24.0, 18.4, 42.0; 8 x 2 24.8, 18.9, 43.7; 4 x 4 27.0, 21.7, 48.7; 8 x 4
@@ -626,13 +629,37 @@ void launch(const QuantArgs &a, hipStream_t s) {
 // workgroups, of which each of the 256 CUs wants one or more: up to 4096 rows
 // one tile and eight waves, up to 8192 two tiles and eight waves (one workgroup
 // per CU), up to 16384 one tile and four waves, beyond that two and four.
-//   4096 x 4096, 1 vector     1 x 8: 4.9 us   2 x 8: 5.9
-//   4096 x 4096, 16 vectors   1 x 8: 6.1      2 x 8: 7.4     1 x 4: 6.5
-//   8192 x 8192, 1 vector     1 x 8: 9.3      2 x 8: 9.0
-//   8192 x 11000, 16 vectors  1 x 8: 19.4     2 x 8: 15.7    1 x 4: 18.9
-//   12288 x 8192, 16 vectors  2 x 8: 20.1     1 x 4: 17.5
-//   28672 x 8192, 16 vectors  2 x 8: 37.7     1 x 4: 44.7    2 x 4: 34.9
-// (bf16 and fp16 vectors; tiles x waves).
+// us per call in a captured graph, from memory (tiles x waves):
+//                               1 x 8  2 x 8  1 x 4  2 x 4
+//   4096 x 4096   bf16,  1        5.2    5.5    7.0    7.3   vector
+//                 fp16, 16        6.4    7.7    7.9    8.8
+//                 fp32,  3        7.3    9.5    9.8   10.9
+//   5001 x 2750   fp16, 16        9.0    8.0    8.0    8.5
+//                 fp32,  3        9.4    8.8    9.5    9.9
+//   8192 x 8192   bf16,  1        9.8    9.5   12.8   13.0
+//                 fp16, 16       16.7   12.9   14.8   15.1
+//                 fp32,  3       19.2   16.3   20.0   19.5
+//   11008 x 4096  bf16,  1        7.8    8.2    9.2    8.7
+//                 fp16, 16       13.3   14.0   11.7   11.7
+//                 fp32,  3       15.7   17.1   15.0   15.8
+//   12288 x 8192  bf16,  1       13.0   13.8   16.6   15.5
+//                 fp16, 16       23.3   22.4   21.3   20.5
+//                 fp32,  3       27.6   28.5   26.8   27.8
+//   14336 x 5120  bf16,  1       11.8   10.4   11.6   12.1
+//                 fp16, 16       21.0   18.3   20.4   16.5
+//                 fp32,  3       23.2   21.0   23.1   19.9
+//   16384 x 4096  bf16,  1       10.4    9.3   10.1   10.0
+//                 fp16, 16       17.3   15.8   16.6   13.3
+//                 fp32,  3       20.7   18.8   19.9   17.4
+//   28672 x 8192  bf16,  1       27.3   27.1   28.4   25.7
+//                 fp16, 16       49.8   43.6   51.4   42.4
+//                 fp32,  3       59.5   55.9   56.7   53.8
+// (bf16 without zero points, groups of 128; fp16 and fp32 with, of 64 and 32.)  The
+// rule is the best of the four, or within 4 % of it, up to 8192 rows and from 16385
+// on, in all types.  Between, no shape is best throughout: one tile and four waves are
+// for several vectors up to 12288 rows (within 5 % of the best) and for matrices that
+// the last-level cache holds (12288 x 8192, one vector 13.2 against 15.2 with two
+// tiles); from there to 16384 rows two tiles are up to a quarter faster.
 template <typename X, typename S, bool Z, int GS, int NC>
 void launch_narrow(const QuantArgs &a, hipStream_t s) {
     if (a.R <= 16 * 256)

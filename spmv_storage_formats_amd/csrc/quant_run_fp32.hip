@@ -11,8 +11,18 @@ namespace {
 
 // Parts of the columns of a wide product: enough for four workgroups per CU, of
 // eight blocks at least, at most eight (their sums are written and read once
-// more).  8192 x 11000 with 48 vectors: 78 us in one part, 25 + 5 in eight, 26 + 7
-// in sixteen.
+// more).  us per call, join included, by the number of parts:
+//                              1     2     4     8    16    rule
+//   1024 x 8192    bf16, 48   53.4  31.4  20.1  15.1  14.1  8   vectors
+//   4096 x 4096    bf16, 48   29.3  19.7  14.5  13.3  15.7  4
+//   8192 x 8192    bf16, 20   47.4  29.5  20.0  18.1  21.7  8
+//   8192 x 11000   bf16, 48   73.7  44.8  30.8  31.2  36.2  8
+//   16384 x 4096   bf16, 48   30.8  24.3  24.8  30.3  38.8  4
+//   28672 x 8192   bf16, 64   70.0  73.8  76.1  94.2   110  3
+//                  fp32, 16   70.2  56.8  54.5  52.2  61.1  5
+// Of 24 such cases (20, 48 and 64 bf16 and 16 fp32 vectors over the six matrices)
+// the rule is within 8 % of the best count in 21, and 9, 12 and 15 % from it at
+// 4096 x 4096, whose 32 blocks would rather be cut in eight parts of four.
 int32_t column_splits(const spmv_quant *q, int32_t n, int32_t x_dtype) {
     const int parts = x_dtype == SPMV_FP32 ? Unit<float>::kParts : 1;
     const int64_t cols = wide_columns(n, parts);
