@@ -558,7 +558,7 @@ spmv_status spmv_quant_build_packed(spmv_quant **out, int32_t num_rows, int32_t 
  *   the fp32 roundings of y[v, r] are relative to the sum over its columns of
  *   |scale| (32 + code + zero) |x|, not to that of |W x|.  So codes equal to their
  *   zero points may leave a rest of that rounding instead of 0 (exactly 0 where
- *   the sums are exact, as with whole numbers).
+ *   the sums are exact, as with small whole numbers).
  *   workspace_dev: at least spmv_quant_run_workspace() bytes, 16-byte aligned
  *   (none for few vectors), used until the work on `stream` is done; calls that
  *   may overlap in time need workspaces of their own.

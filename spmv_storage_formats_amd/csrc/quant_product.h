@@ -472,8 +472,8 @@ __global__ __launch_bounds__(W *kWave) void k_quant_mfma(QuantArgs a) {
 // vectors: 26 us and 5 for the join, of which vector instructions are busy 8 and the
 // matrix unit 7, so bound by neither: waves wait 38 % of their time for loads and at
 // the block's barrier, and two waves per SIMD hide little (three passes of 16
-// through the kernel above: 34 us; 32 vectors 20 + 5
-// against 25).  Two to four blocks of loads ahead in registers measured 24 to 26 us.
+// through the kernel above: 34 us; 32 vectors 20 + 5 against 25).  Two to four
+// blocks of loads ahead in registers measured 24 to 26 us.
 // Waves x tiles, 48, 32 and 96 vectors, without the join: 4 x 2 24.3, 19.5 and 38.8
 // us; 8 x 1 24.0, 18.4, 42.0; 8 x 2 24.8, 18.9, 43.7; 4 x 4 27.0, 21.7, 48.7; 8 x 4
 // 36.8, 27.6, 40.9.
