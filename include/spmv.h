@@ -621,6 +621,66 @@ spmv_status spmv_lookup_grad(int32_t num_rows, int32_t num_cols, int64_t n, cons
                              void *dtable_dev, int64_t dtable_ld, spmv_dtype table_dtype,
                              void *workspace_dev, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Rows of a step: log probabilities of given tokens, and their gradient.
+ *
+ * Types, row strides, alignment, streams and reproducibility as for the weight
+ * tables above.  Nothing is allocated, nothing synchronises, every call can be
+ * captured in a HIP graph.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * spmv_token_logprobs -- for each row x of logits_dev [n, V], with its token id:
+ *     largest = max x,  z = scale * (x - largest),  total = log sum exp(z),
+ *     logprob = z[id] - total,       entropy = -sum p log p,  p = exp(z - total),
+ *     the `top` largest logits by falling value, equal ones by rising index.
+ *   scale (the reciprocal of a temperature) is positive and finite; 0 <= top <= 64
+ *   (SPMV_TOKEN_TOP_MOST).  V is at most 2^31 - 65537 (SPMV_ERR_TOO_LARGE).
+ *   Logits of -inf are masked: probability 0, no share in the entropy, never an
+ *   alternative.  Other logits, the type's lowest value among them, count as they are;
+ *   a log probability below fp32's range is -inf.
+ *   logprobs_dev: fp32 [n]; 0 for a token outside [0, V) (a padded position).
+ *   entropy_dev: fp32 [n], stats_dev: fp32 [n, 2], (largest, total) of each row;
+ *   either may be NULL.
+ *   top_ids_dev: [n, top] of id_dtype, top_logprobs_dev: fp32 [n, top]; where fewer
+ *   than `top` logits are unmasked the last are -1 and -inf.  Not read if top is 0.
+ *   A row that is masked everywhere (or V = 0) has entropy 0, stats of -inf and
+ *   log probabilities of -inf.  A row with a NaN or +inf has NaN in every number
+ *   (0 for a padded position) and -1 for every alternative.
+ *   workspace_dev: at least spmv_token_logprobs_workspace() bytes, 16-byte aligned
+ *   (none where rows are many or short), used until the work on `stream` is done;
+ *   calls that may overlap in time need workspaces of their own.
+ */
+#define SPMV_TOKEN_TOP_MOST 64
+spmv_status spmv_token_logprobs_workspace(int32_t num_cols, int64_t n, int32_t top,
+                                          size_t *bytes);
+spmv_status spmv_token_logprobs(int32_t num_cols, int64_t n, const void *logits_dev, int64_t ld,
+                                spmv_dtype logits_dtype, const void *ids_dev,
+                                spmv_dtype id_dtype, float scale, int32_t top,
+                                float *logprobs_dev, float *entropy_dev, float *stats_dev,
+                                void *top_ids_dev, float *top_logprobs_dev, void *workspace_dev,
+                                size_t workspace_bytes, void *stream);
+
+/*
+ * spmv_token_logprobs_grad -- the gradient of spmv_token_logprobs' logprobs and
+ * entropy with respect to its logits:
+ *     out[t, v] = scale * (gl * ([v = id] - p[v]) - gh * p[v] * (log p[v] + entropy)),
+ *   gl = grad_logprobs_dev[t] (0 for a padded position), gh = grad_entropy_dev[t].
+ *   stats_dev and entropy_dev (the latter only with grad_entropy_dev): as
+ *   spmv_token_logprobs wrote them for the same logits and scale.
+ *   grad_logprobs_dev, grad_entropy_dev: fp32 [n], NULL: zeros.
+ *   out_dev: [n, V] of logits_dtype or SPMV_FP32; it may be logits_dev itself
+ *   (same type and stride), and must not overlap it otherwise.
+ *   Rows with gl = gh = 0, and rows that are masked everywhere, are zeros whatever
+ *   their logits hold.
+ */
+spmv_status spmv_token_logprobs_grad(int32_t num_cols, int64_t n, const void *logits_dev,
+                                     int64_t ld, spmv_dtype logits_dtype, const void *ids_dev,
+                                     spmv_dtype id_dtype, float scale, const float *stats_dev,
+                                     const float *grad_logprobs_dev, const float *entropy_dev,
+                                     const float *grad_entropy_dev, void *out_dev,
+                                     int64_t out_ld, spmv_dtype out_dtype, void *stream);
+
 const char *spmv_status_string(spmv_status status);
 const char *spmv_format_name(spmv_format format);
 

@@ -17,9 +17,15 @@ Weight tables (fp32, fp16 and bf16; token ids int32 or int64):
     rows = q.lookup(ids)                             # rows of W by token
     rows = spmv.lookup(table, ids, scale=1.0)        # rows of a dense table by token
     dtable = spmv.lookup_grad(drows, ids, num_rows)  # its gradient, by sorted tokens
+
+Rows of a step (one request's or sequence's each):
+
+    r = spmv.token_logprobs(logits, ids, top=5)      # log probabilities, entropies, alternatives
+    dlogits = spmv.token_logprobs_grad(dlogprobs, logits, ids, r.stats)
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import functools
 import os
@@ -32,7 +38,8 @@ import numpy as np
 __all__ = ["SpmvError", "Handle", "FORMATS", "ARRAYS", "load_library", "analyze", "select",
            "build", "build_coo", "build_tuned", "coo_to_csr", "library_path",
            "declared_functions", "QuantHandle", "build_quant", "build_quant_packed", "lookup",
-           "lookup_grad", "lookup_grad_workspace"]
+           "lookup_grad", "lookup_grad_workspace", "TokenLogprobs", "token_logprobs",
+           "token_logprobs_grad", "token_logprobs_workspace"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_PKG)
@@ -194,6 +201,15 @@ def load_library():
             "spmv_lookup_grad": (ctypes.c_int, [_i32, _i32, _i64, _vp, ctypes.c_int, _vp, _i64,
                                                 ctypes.c_int, ctypes.c_float, _i32, _vp, _i64,
                                                 ctypes.c_int, _vp, ctypes.c_size_t, _vp]),
+            "spmv_token_logprobs_workspace": (ctypes.c_int, [_i32, _i64, _i32,
+                                                             P(ctypes.c_size_t)]),
+            "spmv_token_logprobs": (ctypes.c_int, [_i32, _i64, _vp, _i64, ctypes.c_int, _vp,
+                                                   ctypes.c_int, ctypes.c_float, _i32, _vp, _vp,
+                                                   _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+            "spmv_token_logprobs_grad": (ctypes.c_int, [_i32, _i64, _vp, _i64, ctypes.c_int,
+                                                        _vp, ctypes.c_int, ctypes.c_float, _vp,
+                                                        _vp, _vp, _vp, _vp, _i64, ctypes.c_int,
+                                                        _vp]),
             "spmv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "spmv_format_name": (ctypes.c_char_p, [ctypes.c_int]),
         }
@@ -927,4 +943,167 @@ def lookup_grad(grad, ids, num_rows: int, out=None, *, scale: float = 1.0,
     _check(load_library().spmv_lookup_grad(
         num_rows, D, n, ip, ik, gp, g_ld, gk, scale, 1 if accumulate else 0, op, o_ld, ok, wp,
         size, _stream_of(index, stream, *made)), "spmv_lookup_grad")
+    return out
+
+
+# ------------------------------------------------------------ rows of a step
+
+TOKEN_TOP_MOST = 64     # SPMV_TOKEN_TOP_MOST in include/spmv.h
+
+TokenLogprobs = collections.namedtuple(
+    "TokenLogprobs", "logprobs entropy stats top_ids top_logprobs")
+TokenLogprobs.__doc__ = """Results of token_logprobs: logprobs and entropy (ids.shape), stats
+(ids.shape + [2]: the largest logit, and the logarithm of the sum over exp(scale * (x - largest))),
+top_ids and top_logprobs (ids.shape + [top]; None without alternatives).  fp32, top_ids of the
+ids' type."""
+
+
+def token_logprobs_workspace(num_rows: int, num_cols: int, top: int = 0) -> int:
+    """Bytes of workspace that token_logprobs needs for these sizes (0 for many rows)."""
+    return _logprobs_bytes(int(num_rows), int(num_cols), int(top))
+
+
+@functools.lru_cache(maxsize=64)
+def _logprobs_bytes(n, cols, top):
+    _fits("spmv_token_logprobs_workspace", cols, top, n)
+    size = ctypes.c_size_t()
+    _check(load_library().spmv_token_logprobs_workspace(cols, n, top, ctypes.byref(size)),
+           "spmv_token_logprobs_workspace")
+    return size.value
+
+
+def _logit_rows(logits, ids):
+    """(device, ids' pointer, count, spmv_dtype, end, logits' pointer, row stride, spmv_dtype,
+    end, columns)."""
+    import torch
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() < 1:
+        raise TypeError("logits must be a cuda tensor")
+    index, V = logits.get_device(), logits.shape[-1]
+    _fits("spmv_token_logprobs", V)
+    ip, n, ik, ie = _token_ids(ids, index)
+    _fits("spmv_token_logprobs", n)
+    xp, x_ld, xk, xe = _rows(_by_token(logits, ids, V, "logits"), "logits", index, n, V)
+    return index, ip, n, ik, ie, xp, x_ld, xk, xe, V
+
+
+def _like(t, shape, dtype, index, name):
+    """Pointer of a contiguous cuda tensor of this shape and dtype."""
+    p = _dev(t, dtype, name)
+    if t.shape != shape or t.get_device() != index:
+        raise ValueError(f"{name} must be {tuple(shape)} on cuda:{index}, got "
+                         f"{tuple(t.shape)} on {t.device}")
+    return p
+
+
+def token_logprobs(logits, ids, out=None, *, scale: float = 1.0, top: int = 0, workspace=None,
+                   stream=None) -> TokenLogprobs:
+    """Log probability of each row's token under softmax(scale * logits), each row's entropy,
+    and its `top` likeliest alternatives (at most 64) by falling value, equal ones by rising
+    index.  logits: ids.shape + [V], fp32, fp16 or bf16; logits of -inf are masked.  ids
+    outside [0, V) (padded positions) have a log probability of 0.  Rows masked everywhere have
+    an entropy of 0, log probabilities of -inf and alternatives of -1; rows with NaN or +inf
+    have NaN.  Returns `out` (default: a new TokenLogprobs).  `workspace`: a contiguous uint8
+    cuda tensor of at least token_logprobs_workspace() bytes, for this call alone until its
+    work is done (default: allocated where the call needs one).  Records no autograd graph:
+    token_logprobs_grad is its backward pass."""
+    import torch
+    index, ip, n, ik, ie, xp, x_ld, xk, xe, V = _logit_rows(logits, ids)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return token_logprobs(logits, ids, out, scale=scale, top=top, workspace=workspace,
+                                  stream=stream)
+    need = _logprobs_bytes(n, V, top)
+    made = []
+    shape = ids.shape
+    if out is None:
+        # one allocation for the numbers of all rows
+        every = torch.empty(n * (4 + top), dtype=torch.float32, device=logits.device)
+        made.append(every)
+        one, two, stats, rest = every.split((n, n, 2 * n, n * top))
+        if len(shape) != 1:
+            one, two = one.view(shape), two.view(shape)
+        at = None
+        if top:
+            at = torch.empty((*shape, top), dtype=ids.dtype, device=logits.device)
+            made.append(at)
+        out = TokenLogprobs(one, two, stats.view(*shape, 2), at,
+                            rest.view(*shape, top) if top else None)
+        lp = every.data_ptr()
+        hp, sp, tp = lp + 4 * n, lp + 8 * n, lp + 16 * n
+        kp = at.data_ptr() if top else None
+    else:
+        f32 = torch.float32
+        lp = _like(out.logprobs, shape, f32, index, "logprobs")
+        hp = _like(out.entropy, shape, f32, index, "entropy")
+        sp = _like(out.stats, (*shape, 2), f32, index, "stats")
+        parts = [out.logprobs, out.entropy, out.stats]
+        kp = tp = None
+        if top:
+            kp = _like(out.top_ids, (*shape, top), ids.dtype, index, "top_ids")
+            tp = _like(out.top_logprobs, (*shape, top), f32, index, "top_logprobs")
+            parts += [out.top_ids, out.top_logprobs]
+        elif out.top_ids is not None or out.top_logprobs is not None:
+            raise ValueError("out has alternatives, top says none")
+        for i, t in enumerate(parts):
+            _apart(logits, t, "logits and out")
+            _apart(ids, t, "ids and out")
+            for u in parts[:i]:
+                _apart(t, u, "the tensors of out")
+    wp, size = None, 0
+    if need:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+            made.append(workspace)
+            wp, size = workspace.data_ptr(), need
+        else:
+            wp, size = _workspace(workspace, need, index)
+            for t in (logits, ids, *out):
+                if t is not None:
+                    _apart(workspace, t, "workspace and other tensors")
+    _check(load_library().spmv_token_logprobs(
+        V, n, xp, x_ld, xk, ip, ik, scale, top, lp, hp, sp, kp, tp, wp, size,
+        _stream_of(index, stream, *made)), "spmv_token_logprobs")
+    return out
+
+
+def token_logprobs_grad(grad, logits, ids, stats, out=None, *, entropy=None, grad_entropy=None,
+                        scale: float = 1.0, dtype=None, stream=None):
+    """Gradient of token_logprobs' logprobs (weights `grad`, or None) and entropy (weights
+    `grad_entropy`, or None) with respect to its logits.  stats, and entropy where
+    grad_entropy is given, are what token_logprobs returned for the same logits and scale; all
+    four are fp32 and contiguous.  Padded positions and masked logits get zeros, and so do rows
+    whose weights are 0 and rows masked everywhere.  Returns `out`, ids.shape + [V] (default: a
+    new tensor of `dtype`, fp32 or the logits' type, which it is unless given); `out` may be
+    `logits` itself."""
+    import torch
+    index, ip, n, ik, ie, xp, x_ld, xk, xe, V = _logit_rows(logits, ids)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return token_logprobs_grad(grad, logits, ids, stats, out, entropy=entropy,
+                                       grad_entropy=grad_entropy, scale=scale, dtype=dtype,
+                                       stream=stream)
+    f32, shape = torch.float32, ids.shape
+    sp = _like(stats, (*shape, 2), f32, index, "stats")
+    gp = None if grad is None else _like(grad, shape, f32, index, "grad")
+    ep = None if entropy is None else _like(entropy, shape, f32, index, "entropy")
+    hp = None if grad_entropy is None else _like(grad_entropy, shape, f32, index, "grad_entropy")
+    if hp and not ep:
+        raise ValueError("grad_entropy needs entropy")
+    made = ()
+    if out is None:
+        out = torch.empty(logits.shape, dtype=dtype or logits.dtype, device=logits.device)
+        made = (out,)
+    flat = _by_token(out, ids, V, "out", dtype)
+    op, o_ld, ok, oe = _rows(flat, "out", index, n, V)
+    if ok != xk and ok != 0:
+        raise TypeError(f"out must be {logits.dtype} or torch.float32, got {out.dtype}")
+    if not made:
+        if op != xp or ok != xk or (o_ld != x_ld and n > 1):
+            _apart(_by_token(logits, ids, V, "logits"), flat, "logits and out")
+        for t in (ids, stats, grad, entropy, grad_entropy):
+            if t is not None:
+                _apart(t, flat, "out and other tensors")
+    _check(load_library().spmv_token_logprobs_grad(
+        V, n, xp, x_ld, xk, ip, ik, scale, sp, gp, ep, hp, op, o_ld, ok,
+        _stream_of(index, stream, *made)), "spmv_token_logprobs_grad")
     return out

@@ -1,0 +1,546 @@
+// Log probabilities of given tokens, entropies and likeliest alternatives of
+// rows of logits, and the gradient of the first two.
+//
+//   m = max x,  z = scale * (x - m),  L = log sum e^z,
+//   logprob = z[id] - L,  entropy = L - sum e^z z / sum e^z,
+//   dx[v] = scale * (gl * ([v = id] - p[v]) - gh * p[v] (log p[v] + entropy)),
+//   p[v] = e^(z[v] - L).
+//
+// One pass over the logits keeps, per thread, the running maximum m, the sum s
+// of 2^y, y = (x - m) scale log2 e, and w, the sum of 2^y y; a larger maximum
+// rescales both.  The sums that are handed on are r = s - 1, the rest beside
+// one largest logit: L = log1p(r) keeps its bits where a row is sure of a token.
+// -inf (a masked logit) has 2^y = 0 and must not meet y = -inf in w, so y is
+// held at kLowest there.  NaN and +inf reach s as NaN.
+//
+// Alternatives: every thread's own maximum, kept anyway, is one element of the
+// row, so the top-th largest of the threads' maxima is a bound that at least
+// `top` elements reach.  Only threads whose maximum reaches it look at their
+// elements again.  Elements are compared as whole numbers (key()) that order by
+// value, then by the lower index: no two are equal, so nothing depends on the
+// order in which they are found.
+#include <type_traits>
+
+#include "requests.h"
+
+namespace spmv {
+namespace {
+
+using u64 = unsigned long long;
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kFlight = 4;            // pieces of a row in flight per thread
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLowest = -160.f;     // 2^kLowest is 0 in fp32
+constexpr float kSure = 1.f / 64;     // rest beside the largest logit that is added up again
+constexpr float kFirst = -3.402823466e38f;  // below every finite logit, or equal
+
+template <typename T>
+constexpr int kPer = sizeof(T) == 4 ? 4 : 8;   // elements of a 16-byte piece
+
+template <int N>
+using Whole = std::integral_constant<int, N>;
+
+// A row's statistics: largest logit, sum of 2^y beside one largest logit (-1:
+// nothing but masked logits), sum of 2^y y.
+struct Stat {
+    float m, r, w;
+};
+
+__device__ inline Stat merge(Stat a, Stat b, float c) {
+    if (b.m > a.m) {
+        const Stat t = a;
+        a = b;
+        b = t;
+    }
+    const float d = fmaxf((b.m - a.m) * c, kLowest);
+    const float f = __builtin_amdgcn_exp2f((b.m - a.m) * c);
+    const float s = b.r + 1.f;
+    a.r += s * f;
+    a.w += f * (b.w + d * s);
+    return a;
+}
+
+// Order of an element: its value, then the lower index.  0 for masked ones.
+__device__ inline u64 key(float x, int32_t at) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.f);  // -0 counts as 0
+    const uint32_t up = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+    const u64 k = (static_cast<u64>(up) << 32) | static_cast<uint32_t>(~at);
+    return x > -__builtin_huge_valf() ? k : 0;
+}
+__device__ inline float key_value(u64 k) {
+    const uint32_t up = static_cast<uint32_t>(k >> 32);
+    const uint32_t b = up & 0x80000000u ? up ^ 0x80000000u : ~up;
+    return __builtin_bit_cast(float, b);
+}
+__device__ inline int32_t key_index(u64 k) { return static_cast<int32_t>(~static_cast<uint32_t>(k)); }
+
+__device__ inline u64 larger(u64 a, u64 b, bool larger_one) {
+    return (a > b) == larger_one ? a : b;
+}
+
+// The wave's 64 keys in falling order, lane 0 the largest (bitonic).
+__device__ inline u64 sort_wave(u64 k, int lane) {
+#pragma unroll
+    for (int size = 2; size <= kWave; size *= 2)
+#pragma unroll
+        for (int j = size / 2; j >= 1; j /= 2) {
+            const u64 other = __shfl_xor(k, j);
+            k = larger(k, other, ((lane & j) == 0) == ((lane & size) == 0));
+        }
+    return k;
+}
+
+// The 64 largest of two lists in falling order, in falling order.
+__device__ inline u64 merge_wave(u64 a, u64 b, int lane) {
+    const u64 back = __shfl(b, kWave - 1 - lane);
+    u64 k = a > back ? a : back;
+#pragma unroll
+    for (int j = kWave / 2; j >= 1; j /= 2) {
+        const u64 other = __shfl_xor(k, j);
+        k = larger(k, other, (lane & j) == 0);
+    }
+    return k;
+}
+
+// The 64 largest of the waves' lists, in wave 0.  Begins and ends with a barrier.
+template <int W>
+__device__ inline u64 merge_waves(u64 k, u64 (*lists)[kWave], int wave, int lane) {
+    __syncthreads();
+    lists[wave][lane] = k;
+    __syncthreads();
+#pragma unroll
+    for (int step = 1; step < W; step *= 2) {
+        if (wave % (2 * step) == 0) {
+            k = merge_wave(k, lists[wave + step][lane], lane);
+            lists[wave][lane] = k;
+        }
+        __syncthreads();
+    }
+    return k;
+}
+
+__device__ inline Stat merge_lanes(Stat a, float c) {
+#pragma unroll
+    for (int j = 1; j < kWave; j *= 2)
+        a = merge(a, {__shfl_xor(a.m, j), __shfl_xor(a.r, j), __shfl_xor(a.w, j)}, c);
+    return a;
+}
+
+struct Place {
+    const LogprobsArgs a;
+    int32_t parts;     // of a row
+    int32_t part;      // columns of one
+    float *stat;       // [n * parts][3]
+    u64 *best;         // [n * parts][top]
+};
+
+// A row's results, by the first lanes of a wave: the statistics, and the best
+// keys in falling order by lane.
+template <typename T, typename I>
+__device__ inline void finish(const LogprobsArgs &a, int64_t t, Stat st, u64 best, int lane) {
+    const float nan = __builtin_nanf("");
+    const bool bad = !(st.r >= -1.f);      // NaN
+    const bool none = st.r == -1.f;        // masked everywhere
+    const float L = none ? -__builtin_huge_valf() : log1pf(st.r);
+    const float m = bad ? nan : none ? -__builtin_huge_valf() : st.m;
+    if (lane == 0) {
+        if (a.stats) {
+            a.stats[2 * t] = m;
+            a.stats[2 * t + 1] = L;
+        }
+        if (a.entropy) a.entropy[t] = none ? 0.f : L - kLn2 * st.w / (1.f + st.r);
+        if (a.logprobs) {
+            const int64_t id = static_cast<const I *>(a.ids)[t];
+            float lp = 0.f;
+            if (id >= 0 && id < a.V) {
+                const float x = static_cast<float>(static_cast<const T *>(a.logits)[t * a.ld + id]);
+                lp = none ? L : (x - m) * a.scale - L;
+            }
+            a.logprobs[t] = lp;
+        }
+    }
+    if (lane < a.top) {
+        const bool there = best != 0 && !bad;
+        const int64_t to = t * a.top + lane;
+        static_cast<I *>(a.top_ids)[to] = there ? static_cast<I>(key_index(best)) : I(-1);
+        a.top_logprobs[to] = there  ? (key_value(best) - m) * a.scale - L
+                             : bad ? nan
+                                   : -__builtin_huge_valf();
+    }
+}
+
+// A workgroup takes one part of a row; with one part per row it writes the
+// row's results, otherwise the part's, which k_join puts together.
+template <typename T, typename I, bool kTop>
+__global__ __launch_bounds__(kThreads) void k_logprobs(Place p) {
+    constexpr int E = kPer<T>;
+    constexpr int kStep = kThreads * E;
+    const LogprobsArgs &a = p.a;
+    __shared__ Stat s_stat[kWaves];
+    __shared__ u64 s_list[kTop ? kWaves : 1][kWave];
+    __shared__ u64 s_found[kTop ? kWaves : 1][kWave * (E + 1)];
+    __shared__ u64 s_bound;
+    const int lane = threadIdx.x % kWave, tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const float c = a.scale * kLog2e;
+    const int64_t items = a.n * p.parts;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int64_t t = item / p.parts;
+        const int32_t first = static_cast<int32_t>(item % p.parts) * p.part;
+        const int32_t count = a.V - first < p.part ? a.V - first : p.part;
+        const T *row = static_cast<const T *>(a.logits) + t * a.ld + first;
+        float m = kFirst, s = 0.f, w = 0.f;
+        int32_t last = -1;  // last column of the piece that holds the first maximum
+        // `many` pieces of E, kStep apart, the first at column `at`
+        auto take = [&](const float *v, auto many, int32_t at) {
+            constexpr int M = decltype(many)::value;
+            float pm[M], cm;
+#pragma unroll
+            for (int u = 0; u < M; ++u) {
+                pm[u] = v[u * E];
+#pragma unroll
+                for (int i = 1; i < E; ++i) pm[u] = fmaxf(pm[u], v[u * E + i]);
+                cm = u == 0 ? pm[0] : fmaxf(cm, pm[u]);
+            }
+            if (cm > m || (last < 0 && cm >= m)) {
+                const float d = fmaxf((m - cm) * c, kLowest);
+                const float f = __builtin_amdgcn_exp2f((m - cm) * c);
+                w = f * (w + d * s);
+                s *= f;
+                m = cm;
+                if constexpr (kTop) {
+#pragma unroll
+                    for (int u = M - 1; u >= 0; --u)
+                        if (pm[u] == cm) last = at + u * kStep + E - 1;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < M * E; ++i) {
+                const float y = (v[i] - m) * c;
+                const float e = __builtin_amdgcn_exp2f(y);
+                s += e;
+                w += e * fmaxf(y, kLowest);
+            }
+        };
+        int32_t at = tid * E;
+        const int32_t full = count - count % (kFlight * kStep);
+        for (; at < full; at += kFlight * kStep) {
+            float v[kFlight * E];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) load_piece<E>(row + at + u * kStep, v + u * E);
+            take(v, Whole<kFlight>{}, at);
+        }
+        for (; at < count; at += kStep) {
+            float v[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[i] = -__builtin_huge_valf();
+            if (at + E <= count) {
+                load_piece<E>(row + at, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (at + i < count) v[i] = static_cast<float>(row[at + i]);
+            }
+            take(v, Whole<1>{}, at);
+        }
+        Stat st = merge_lanes({m, s - 1.f, w}, c);
+        u64 best = 0;
+        if constexpr (kTop) {
+            const u64 own = last >= 0 ? key(m, last) : 0;
+            const u64 sorted = merge_waves<kWaves>(sort_wave(own, lane), s_list, wave, lane);
+            if (wave == 0 && lane == a.top - 1) s_bound = sorted;
+            __syncthreads();
+            const u64 bound = s_bound;
+            u64 *found = s_found[wave];
+            int have = 0;
+            const int pieces = (count + kStep - 1) / kStep;
+            const u64 below = (1ull << lane) - 1ull;
+            u64 again = __ballot(own != 0 && own >= bound);
+            while (again) {
+                const int src = __builtin_ctzll(again);
+                again &= again - 1;
+                for (int i0 = 0; i0 < pieces; i0 += kWave) {
+                    const int64_t from = static_cast<int64_t>(i0 + lane) * kStep +
+                                         (wave * kWave + src) * E;
+                    float v[E];
+#pragma unroll
+                    for (int i = 0; i < E; ++i) v[i] = -__builtin_huge_valf();
+                    if (from + E <= count) {
+                        load_piece<E>(row + from, v);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < E; ++i)
+                            if (from + i < count) v[i] = static_cast<float>(row[from + i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        const u64 k = key(v[i], static_cast<int32_t>(from) + i);
+                        const bool in = k != 0 && k >= bound;
+                        const u64 who = __ballot(in);
+                        if (in) found[have + __popcll(who & below)] = k;
+                        have += __popcll(who);
+                    }
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
+                    while (have >= kWave) {
+                        have -= kWave;
+                        best = merge_wave(best, sort_wave(found[have + lane], lane), lane);
+                    }
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
+                }
+            }
+            if (have > 0) best = merge_wave(best, sort_wave(lane < have ? found[lane] : 0, lane), lane);
+            best = merge_waves<kWaves>(best, s_list, wave, lane);
+            // keys count from the part's first column
+            if (best != 0) best -= static_cast<u64>(static_cast<uint32_t>(first));
+        }
+        if (lane == 0) s_stat[wave] = st;
+        __syncthreads();
+        auto merged = [&] {
+            Stat all = s_stat[0];
+#pragma unroll
+            for (int i = 1; i < kWaves; ++i) all = merge(all, s_stat[i], c);
+            return all;
+        };
+        st = merged();
+        // The thread that holds the largest logit adds its other elements to 1.
+        // Where the rest is small its wave adds them up again beside the 1.
+        if (st.r < kSure && st.m > kFirst) {
+            int owner = 0;
+            while (owner < kWaves - 1 && s_stat[owner].m != st.m) ++owner;
+            __syncthreads();
+            if (wave == owner) {
+                const int src = __builtin_ctzll(__ballot(m == st.m));
+                float rest = 0.f;
+                int equal = 0;
+                for (int64_t from = (static_cast<int64_t>(lane) * kThreads + wave * kWave + src) * E;
+                     from < count; from += static_cast<int64_t>(kWave) * kStep) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        if (from + i >= count) continue;
+                        const float x = static_cast<float>(row[from + i]);
+                        if (x == st.m)
+                            ++equal;
+                        else
+                            rest += __builtin_amdgcn_exp2f((x - st.m) * c);
+                    }
+                }
+#pragma unroll
+                for (int j = 1; j < kWave; j *= 2) {
+                    rest += __shfl_xor(rest, j);
+                    equal += __shfl_xor(equal, j);
+                }
+                const float r = lane == src ? rest + static_cast<float>(equal - 1) : s - 1.f;
+                const Stat again = merge_lanes({m, r, w}, c);
+                if (lane == 0) s_stat[wave] = again;
+            }
+            __syncthreads();
+            st = merged();
+        }
+        if (wave == 0) {
+            if (p.parts == 1) {
+                finish<T, I>(a, t, st, best, lane);
+            } else {
+                if (lane == 0) {
+                    p.stat[3 * item] = st.m;
+                    p.stat[3 * item + 1] = st.r;
+                    p.stat[3 * item + 2] = st.w;
+                }
+                if (kTop && lane < a.top) p.best[item * a.top + lane] = best;
+            }
+        }
+        __syncthreads();  // the next row reuses the shared arrays
+    }
+}
+
+// The parts of a row joined in their order.
+constexpr int kJoinWaves = 16;
+template <typename T, typename I, bool kTop>
+__global__ __launch_bounds__(kJoinWaves *kWave) void k_join(Place p) {
+    const LogprobsArgs &a = p.a;
+    __shared__ u64 s_list[kTop ? kJoinWaves : 1][kWave];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const float c = a.scale * kLog2e;
+    for (int64_t t = blockIdx.x; t < a.n; t += gridDim.x) {
+        u64 best = 0;
+        if constexpr (kTop) {
+            const int32_t keys = p.parts * a.top;
+            const u64 *from = p.best + t * p.parts * a.top;
+            for (int32_t i = wave * kWave; i < keys; i += kJoinWaves * kWave)
+                best = merge_wave(best, sort_wave(i + lane < keys ? from[i + lane] : 0, lane), lane);
+            best = merge_waves<kJoinWaves>(best, s_list, wave, lane);
+        }
+        if (wave == 0) {
+            Stat st{kFirst, -1.f, 0.f};
+            const float *from = p.stat + 3 * t * p.parts;
+            for (int32_t i = lane; i < p.parts; i += kWave)
+                st = merge(st, {from[3 * i], from[3 * i + 1], from[3 * i + 2]}, c);
+            finish<T, I>(a, t, merge_lanes(st, c), best, lane);
+        }
+        if (kTop) __syncthreads();
+    }
+}
+
+// Parts of a row: few rows are cut, so that kGroups workgroups run, into parts
+// of no less than one step of a workgroup and a whole number of them.
+constexpr int64_t kGroups = 1024;
+constexpr int kMostParts = 64;
+void cut(int32_t V, int64_t n, int32_t *parts, int32_t *part) {
+    constexpr int32_t kUnit = kThreads * 8;
+    const int64_t units = std::max<int64_t>(1, (static_cast<int64_t>(V) + kUnit - 1) / kUnit);
+    const int64_t want = std::min<int64_t>({units, kMostParts, (kGroups + n - 1) / n});
+    const int64_t per = (units + want - 1) / want;
+    *parts = static_cast<int32_t>((units + per - 1) / per);
+    *part = *parts == 1 ? V : static_cast<int32_t>(per * kUnit);
+}
+
+size_t stat_bytes(int64_t items) { return (static_cast<size_t>(items) * 12 + 15) / 16 * 16; }
+
+// ------------------------------------------------------------------ gradient
+
+// A workgroup's threads take kFlight pieces each of one row.  Reads and writes
+// as a copy does; a row whose two weights are 0 is not read.
+template <typename T, typename B, typename I, bool kEntropy>
+__global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a, int32_t blocks) {
+    constexpr int E = kPer<B>;
+    constexpr int kStep = kThreads * E;
+    const float c = a.scale * kLog2e;
+    const int64_t items = a.n * blocks;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int64_t t = item / blocks;
+        const int32_t first = static_cast<int32_t>(item % blocks) * (kFlight * kStep);
+        const int64_t token = static_cast<const I *>(a.ids)[t];
+        const bool given = token >= 0 && token < a.V;
+        const int32_t id = given ? static_cast<int32_t>(token) : -1;
+        const float gl = given && a.grad_logprobs ? a.grad_logprobs[t] * a.scale : 0.f;
+        const float gh = kEntropy ? a.grad_entropy[t] * a.scale : 0.f;
+        const float m = a.stats[2 * t], L = a.stats[2 * t + 1];
+        // nothing to hand back, or no logit that the mask left
+        const bool zero = (gl == 0.f && gh == 0.f) || m == -__builtin_huge_valf();
+        const float h = kEntropy ? a.entropy[t] : 0.f;
+        const float L2 = L * kLog2e;
+        const T *src = static_cast<const T *>(a.logits) + t * a.ld;
+        B *dst = static_cast<B *>(a.out) + t * a.out_ld;
+        float v[kFlight][E];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const int32_t at = first + u * kStep + static_cast<int32_t>(threadIdx.x) * E;
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[u][i] = 0.f;
+            if (zero) continue;
+            if (at + E <= a.V)
+                load_piece<E>(src + at, v[u]);
+            else if (at < a.V)
+                load_piece_tail<E>(src + at, static_cast<int>(a.V - at), v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const int32_t at = first + u * kStep + static_cast<int32_t>(threadIdx.x) * E;
+            if (at >= a.V) continue;
+            if (!zero) {
+                float own = 0.f;  // the given token's logit, where this piece holds it
+                const bool mine = given && id >= at && id < at + E;
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i) own = at + i == id ? v[u][i] : own;
+                }
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const float y = (v[u][i] - m) * c - L2;  // log2 p
+                    const float q = __builtin_amdgcn_exp2f(y);
+                    float d = -gl * q;
+                    if constexpr (kEntropy) d -= gh * q * (fmaxf(y, kLowest) * kLn2 + h);
+                    v[u][i] = d;
+                }
+                if (mine) {
+                    const float y = (own - m) * c - L2;
+                    // 1 - p, with its bits where p is nearly 1
+                    float d = -gl * expm1f(y * kLn2);
+                    if constexpr (kEntropy)
+                        d -= gh * __builtin_amdgcn_exp2f(y) * (fmaxf(y, kLowest) * kLn2 + h);
+#pragma unroll
+                    for (int i = 0; i < E; ++i) v[u][i] = at + i == id ? d : v[u][i];
+                }
+            }
+            if (at + E <= a.V)
+                store_piece<E>(dst + at, v[u]);
+            else
+                store_piece_tail<E>(dst + at, static_cast<int>(a.V - at), v[u]);
+        }
+    }
+}
+
+template <typename F>
+auto with_ids(int32_t d, F f) {
+    return d == SPMV_INT32 ? f(int32_t{}) : f(int64_t{});
+}
+
+}  // namespace
+
+size_t logprobs_bytes(int32_t V, int64_t n, int32_t top) {
+    if (n == 0) return 0;
+    int32_t parts, part;
+    cut(V, n, &parts, &part);
+    if (parts == 1) return 0;
+    return stat_bytes(n * parts) + static_cast<size_t>(n) * parts * top * sizeof(u64);
+}
+
+spmv_status logprobs(const LogprobsArgs &a, hipStream_t s) {
+    Place p{a, 1, 0, nullptr, nullptr};
+    cut(a.V, a.n, &p.parts, &p.part);
+    p.stat = static_cast<float *>(a.workspace);
+    if (p.parts > 1)
+        p.best = reinterpret_cast<u64 *>(static_cast<char *>(a.workspace) +
+                                         stat_bytes(a.n * p.parts));
+    const unsigned grid = groups_for(a.n * p.parts, 1);
+    with_float(a.dtype, [&](auto x) {
+        with_ids(a.id_dtype, [&](auto i) {
+            using T = decltype(x);
+            using I = decltype(i);
+            if (a.top > 0)
+                k_logprobs<T, I, true><<<grid, kThreads, 0, s>>>(p);
+            else
+                k_logprobs<T, I, false><<<grid, kThreads, 0, s>>>(p);
+            if (p.parts == 1) return;
+            if (a.top > 0)
+                k_join<T, I, true><<<groups_for(a.n, 1), kJoinWaves * kWave, 0, s>>>(p);
+            else
+                k_join<T, I, false><<<groups_for(a.n, 1), kWave, 0, s>>>(p);
+        });
+    });
+    SPMV_HIP(hipGetLastError());
+    return SPMV_OK;
+}
+
+spmv_status logprobs_grad(const LogprobsGradArgs &a, hipStream_t s) {
+    with_float(a.dtype, [&](auto x) {
+        with_ids(a.id_dtype, [&](auto i) {
+            using T = decltype(x);
+            using I = decltype(i);
+            auto go = [&](auto to) {
+                using B = decltype(to);
+                constexpr int kRun = kFlight * kThreads * kPer<B>;
+                const int32_t blocks =
+                    static_cast<int32_t>((static_cast<int64_t>(a.V) + kRun - 1) / kRun);
+                const unsigned grid = groups_for(a.n * blocks, 1);
+                if (a.grad_entropy)
+                    k_logprobs_grad<T, B, I, true><<<grid, kThreads, 0, s>>>(a, blocks);
+                else
+                    k_logprobs_grad<T, B, I, false><<<grid, kThreads, 0, s>>>(a, blocks);
+            };
+            if (a.out_dtype == SPMV_FP32)
+                go(float{});
+            else
+                go(T{});
+        });
+    });
+    SPMV_HIP(hipGetLastError());
+    return SPMV_OK;
+}
+
+}  // namespace spmv

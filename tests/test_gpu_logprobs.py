@@ -1,0 +1,475 @@
+"""Log probabilities, entropies, alternatives and their gradient on the GPU, against plain
+implementations in 64 bits.
+
+`U` is half a step of fp32.  With D = scale * (largest - x) >= 0 and p the probabilities, a
+kernel's power of two errs by at most (4 D + 3) U relative to itself: three roundings and that of
+the factor lie in its exponent, one unit in the last place (2 U) and one more in the result.  An
+element passes at most A = V/256 + 64 additions and rescalings, of three roundings each.  So the
+sum s is off by at most S = U (4 E[D] + 3 A + 3), relative; its logarithm, total, by S + 4 U total;
+a log probability lp by that and U (4 |z| + |lp|), z = -D of its token; the entropy, total + E[D], by
+that and U (4 E[D^2] + (3 A + 8) E[D]) + E[D] S + 2 U entropy."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import spmv_storage_formats_amd as spmv  # noqa: E402
+
+F = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
+U = 2.0 ** -24
+INF = float("inf")
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    spmv.load_library()
+    return torch.device("cuda:0")
+
+
+class Want:
+    """The definition in 64 bits (numpy) and the bounds above, for rows of finite or masked
+    logits, at least one finite in each row."""
+
+    def __init__(self, logits, ids, scale, top):
+        x = logits.double().cpu().numpy()
+        ids = ids.cpu().numpy().astype(np.int64)
+        scale = float(np.float32(scale))
+        n, V = x.shape
+        self.there = (ids >= 0) & (ids < V)
+        at = np.where(self.there, ids, 0)
+        self.m = x.max(1)
+        with np.errstate(all="ignore"):
+            d = (self.m[:, None] - x) * scale
+            e = np.exp(-d)
+            s = e.sum(1)
+            self.p = e / s[:, None]
+            self.total = np.log(s)
+            dp = np.where(self.p > 0, d, 0)
+            self.lpv = -d - self.total[:, None]
+            ed, ed2 = (self.p * dp).sum(1), (self.p * dp * dp).sum(1)
+            self.entropy = self.total + ed
+            lp = self.lpv[np.arange(n), at]
+            self.lp = np.where(self.there, lp, 0)
+            A = V / 256 + 64
+            S = U * (4 * ed + 3 * A + 3)
+            self.total_tol = S + 4 * U * self.total
+            z = np.where(np.isfinite(self.lp), np.abs(self.lp) + self.total, 0)
+            self.lp_tol = self.total_tol + U * (4 * z + np.abs(np.where(z, self.lp, 0)))
+            self.entropy_tol = (self.total_tol + U * (4 * ed2 + (3 * A + 8) * ed) + ed * S
+                                + 2 * U * self.entropy)
+            order = np.lexsort((np.broadcast_to(np.arange(V), x.shape), -x))[:, :top]
+            best = np.take_along_axis(x, order, 1)
+            self.top_ids = np.where(best > -INF, order, -1)
+            self.top_lp = np.take_along_axis(self.lpv, order, 1)
+            if order.shape[1] < top:
+                pad = ((0, 0), (0, top - order.shape[1]))
+                self.top_ids = np.pad(self.top_ids, pad, constant_values=-1)
+                self.top_lp = np.pad(self.top_lp, pad, constant_values=-INF)
+            zt = np.where(np.isfinite(self.top_lp), -self.top_lp, 0)
+            self.top_tol = self.total_tol[:, None] + U * (5 * zt + 4 * self.total[:, None])
+        self.x, self.ids, self.scale = x, at, scale
+
+
+def close(got, want, tol, what):
+    got = got.double().cpu().numpy()
+    same = (got == want) | (np.isnan(got) & np.isnan(want))
+    with np.errstate(all="ignore"):
+        off = np.where(same, 0, np.abs(got - want))
+        assert np.all(off <= tol), (what, np.nanmax(off / np.maximum(tol, 1e-300)),
+                                    np.argmax(off / np.maximum(tol, 1e-300)))
+
+
+def check(r, w, top):
+    close(r.logprobs, w.lp, w.lp_tol, "logprobs")
+    close(r.entropy, w.entropy, w.entropy_tol, "entropy")
+    assert np.array_equal(r.stats[:, 0].double().cpu().numpy(), w.m)
+    close(r.stats[:, 1], w.total, w.total_tol, "total")
+    if top:
+        assert np.array_equal(r.top_ids.cpu().numpy(), w.top_ids)
+        close(r.top_logprobs, w.top_lp, w.top_tol, "alternatives")
+    else:
+        assert r.top_ids is None and r.top_logprobs is None
+
+
+def make(n, V, dtype, seed, keep=1.0, pad=0.0, ids="int64"):
+    rng = np.random.default_rng(seed)
+    x = rng.normal(0, 2.5, (n, V))
+    at = rng.integers(0, V, n)
+    x[np.arange(n), at] += rng.uniform(0, 20, n)
+    if keep < 1:
+        gone = rng.random((n, V)) >= keep
+        gone[np.arange(n), at] = False
+        x[gone] = -INF
+    at = np.where(rng.random(n) < pad, rng.choice([-1, V, -2**31 + 5], n), at)
+    return (torch.from_numpy(x).to(F[dtype]),
+            torch.from_numpy(at).to(torch.int64 if ids == "int64" else torch.int32))
+
+
+# rows of less than a piece, odd ones, one workgroup's step and around it, several parts
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 63, 257, 1000, 2047, 2048, 2049, 5001, 8192, 16387,
+                               50001])
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+def test_sizes_and_types(dev, V, dtype):
+    for n, top, scale in ((1, 5, 1.0), (3, 64, 0.7), (5, 0, 1.25), (2, 1, 3.0)):
+        x, ids = make(n, V, dtype, V * 10 + n, pad=0.2)
+        w = Want(x, ids, scale, top)
+        check(spmv.token_logprobs(x.to(dev), ids.to(dev), scale=scale, top=top), w, top)
+
+
+@pytest.mark.parametrize("n,V,top", [(300, 3001, 20), (1500, 700, 3), (1100, 9000, 64),
+                                     (40, 128000, 20), (1, 131072, 64)])
+@pytest.mark.parametrize("keep", [1.0, 0.02])
+def test_many_rows_masks_and_padding(dev, n, V, top, keep):
+    """Masked logits have no share and are no alternatives; fewer than `top` may be left."""
+    x, ids = make(n, V, "bf16", n + V, keep=keep, pad=0.1, ids="int32")
+    w = Want(x, ids, 1.25, top)
+    r = spmv.token_logprobs(x.to(dev), ids.to(dev), scale=1.25, top=top)
+    assert r.top_ids.dtype == torch.int32
+    check(r, w, top)
+
+
+def test_largest_scores(dev):
+    """The largest sizes of a scoring step, checked by rows in 64 bits on the GPU."""
+    n, V = 4096, 128000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(n, V, generator=g, device=dev, dtype=torch.bfloat16)
+    ids = torch.randint(0, V, (n,), generator=g, device=dev)
+    r = spmv.token_logprobs(x, ids, top=2)
+    for t in (0, 1, 2047, n - 1):
+        one = Want(x[t:t + 1], ids[t:t + 1], 1.0, 2)
+        check(spmv.TokenLogprobs(*(f[t:t + 1] for f in r)), one, 2)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+def test_ties_go_to_the_lowest_index(dev, dtype):
+    """Constant rows, rows of two values, both zeros, falling and rising rows: orders that put
+    many equal or many large elements into one thread's share."""
+    V, top = 9000, 64
+    i = np.arange(V)
+    rows = [np.full(V, 3.0), np.zeros(V), np.where(i % 3 == 1, 0.0, -0.0), (i % 5 == 4) * 1.0,
+            (i // 70) * -0.5, (i // 70) * 0.5, np.where(i < 8990, -5.0, 1.0),
+            np.where(i == 8999, 2.0, 0.0), (i * 7919 % 64) * 1.0, -(i * 7919 % 8) * 1.0,
+            np.where((i // 8) % 256 == 5, 4.0 + (i % 97) / 128, -4.0)]
+    x = torch.from_numpy(np.stack(rows)).to(F[dtype])
+    ids = torch.zeros(len(rows), dtype=torch.int64)
+    w = Want(x, ids, 1.0, top)
+    check(spmv.token_logprobs(x.to(dev), ids.to(dev), top=top), w, top)
+    # and as many rows, one workgroup each
+    many = x.repeat(100, 1)
+    w = Want(many, ids.repeat(100), 1.0, top)
+    check(spmv.token_logprobs(many.to(dev), ids.repeat(100).to(dev), top=top), w, top)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("n", [1, 1200])
+def test_masks_of_the_lowest_value(dev, dtype, n):
+    """A mask of the type's lowest value leaves a finite logit: a row of nothing else is
+    uniform, beside others it has no weight but its order."""
+    V = 2100
+    low = torch.finfo(F[dtype]).min
+    x = torch.full((n, V), low, dtype=F[dtype])
+    ids = torch.full((n,), 7)
+    for few in (0, 3):
+        x[:, 100:100 + few] = 1.0
+        r = spmv.token_logprobs(x.to(dev), ids.to(dev), top=8)
+        if few == 0:
+            assert (r.logprobs.cpu() + np.log(V)).abs().max() < 1e-4
+            assert (r.entropy.cpu() - np.log(V)).abs().max() < 1e-4
+            assert r.top_ids.cpu().tolist() == [list(range(8))] * n
+        else:
+            assert (r.entropy.cpu() - np.log(few)).abs().max() < 1e-5
+            assert r.top_ids.cpu().tolist() == [[100, 101, 102, 0, 1, 2, 3, 4]] * n
+            assert (r.logprobs < -60000).all()
+        assert (r.stats[:, 0] == (low if few == 0 else 1.0)).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("n", [1, 1200])
+@pytest.mark.parametrize("V", [70, 9001])
+def test_rows_without_a_distribution(dev, dtype, n, V):
+    """Rows masked everywhere, rows with NaN or +inf, and sound rows between them."""
+    rng = np.random.default_rng(3)
+    x = torch.from_numpy(rng.normal(0, 1, (5, V))).to(F[dtype])
+    x[1] = -INF
+    x[2, V // 2] = float("nan")
+    x[3, V - 1] = INF
+    x[3, 0] = INF
+    ids = torch.tensor([3, 3, 3, -1, V - 1])
+    w = Want(x[[0, 4]], ids[[0, 4]], 1.0, 4)
+    if n > 5:
+        x, ids = x.repeat(n // 5, 1), ids.repeat(n // 5)
+    r = spmv.token_logprobs(x.to(dev), ids.to(dev), top=4)
+    g = torch.ones(len(ids), device=dev)
+    dx = spmv.token_logprobs_grad(g, x.to(dev), ids.to(dev), r.stats, entropy=r.entropy,
+                                  grad_entropy=g)
+    pad = spmv.token_logprobs_grad(g, x.to(dev), ids.to(dev), r.stats)
+    r = spmv.TokenLogprobs(*(f[-5:] for f in r))
+    check(spmv.TokenLogprobs(*(f[[0, 4]] for f in r)), w, 4)
+    assert r.logprobs[1] == -INF and r.entropy[1] == 0 and (r.stats[1] == -INF).all()
+    assert r.top_ids[1:4].eq(-1).all() and (r.top_logprobs[1] == -INF).all()
+    assert r.logprobs[2].isnan() and r.logprobs[3] == 0
+    for t in (2, 3):
+        assert r.entropy[t].isnan() and r.stats[t].isnan().all()
+        assert r.top_logprobs[t].isnan().all()
+    dx, pad = dx[-5:], pad[-5:]
+    assert (dx[1] == 0).all() and dx[2].isnan().all() and dx[3].isnan().all()
+    assert dx[[0, 4]].isfinite().all()
+    assert (pad[3] == 0).all()          # no weight reaches a padded row, whatever it holds
+
+
+def test_sure_rows_keep_their_bits(dev):
+    """A row that is nearly sure of its token: the log probability is the small rest itself."""
+    for gap in (12.0, 20.0, 40.0, 80.0):
+        x = torch.zeros(1, 4000)
+        x[0, 1234] = gap
+        r = spmv.token_logprobs(x.to(dev), torch.tensor([1234], device=dev))
+        rest = 3999 * np.exp(-gap)
+        want, got = -np.log1p(rest), r.logprobs.item()
+        assert abs(got - want) <= 1e-4 * abs(want)
+        h = np.log1p(rest) + rest / (1 + rest) * gap
+        assert abs(r.entropy.item() - h) <= 1e-4 * h
+        d = spmv.token_logprobs_grad(torch.ones(1, device=dev), x.to(dev),
+                                     torch.tensor([1234], device=dev), r.stats)
+        assert abs(d[0, 1234].item() - rest / (1 + rest)) <= 1e-4 * rest
+
+
+def test_extreme_logits(dev):
+    """Differences that pass fp32's range, and logits far from zero."""
+    x = torch.zeros(3, 300)
+    x[0, 5], x[0, 6] = 3e38, -3e38
+    x[1] = 1e6
+    x[1, 9] += 2
+    x[2] = -1e30
+    ids = torch.tensor([5, 9, 0])
+    r = spmv.token_logprobs(x.to(dev), ids.to(dev), scale=2.0, top=2)
+    w = Want(x, ids, 2.0, 2)
+    # twice 3e38 is past fp32's largest number, 3.4e38: the nearest fp32 value is -inf
+    assert w.top_lp[0, 1] < -torch.finfo(torch.float32).max
+    w.top_lp[0, 1] = -INF
+    check(r, w, 2)
+
+
+# ------------------------------------------------------------------ gradient
+
+def grad_want(w, gl, gh, dtype):
+    """The formula, and its bound: p errs by D = U (4 |z| + 5 total + |lp| + 4) relative (its
+    exponent and the statistics' roundings), log p + entropy by D + 2 U (|lp| + 2 entropy), the
+    products by four roundings; 1 - p at the token by D p + 4 U; then the output's rounding."""
+    n, V = w.x.shape
+    gl = np.where(w.there, gl, 0.0)
+    with np.errstate(all="ignore"):
+        lp = np.where(w.p > 0, w.lpv, 0)
+        z = np.where(w.p > 0, -w.lpv - w.total[:, None], 0)
+        at = np.zeros((n, V))
+        at[np.arange(n), w.ids] = 1
+        inner = lp + w.entropy[:, None]
+        d = w.scale * (gl[:, None] * (at - w.p) - gh[:, None] * w.p * inner)
+        err = U * (4 * np.abs(z) + 5 * w.total[:, None] + np.abs(lp) + 8)
+        mag = (np.abs(gl)[:, None] * (w.p * err + 4 * U * at)
+               + np.abs(gh)[:, None] * w.p * (np.abs(inner) * (err + 4 * U) + err
+                                              + 2 * U * (np.abs(lp) + 2 * w.entropy[:, None])))
+    info = torch.finfo(F[dtype])
+    tol = w.scale * mag * (1 + 1e-3) + info.eps / 2 * np.abs(d) + info.eps * info.tiny + 1e-37
+    return d, tol
+
+
+def stats_of(w, dev):
+    st = torch.from_numpy(np.stack([w.m, w.total], 1)).float().to(dev)
+    return st, torch.from_numpy(w.entropy).float().to(dev)
+
+
+@pytest.mark.parametrize("V", [1, 3, 8, 100, 1000, 2049, 8195, 40001])
+@pytest.mark.parametrize("dtype,out", [("fp32", "fp32"), ("fp16", "fp16"), ("bf16", "bf16"),
+                                       ("fp16", "fp32"), ("bf16", "fp32")])
+def test_gradient(dev, V, dtype, out):
+    for n, scale, keep in ((1, 1.0, 1.0), (9, 0.7, 0.3), (4, 1.25, 1.0)):
+        rng = np.random.default_rng(V + n)
+        x, ids = make(n, V, dtype, V + n, keep=keep, pad=0.2, ids="int32")
+        w = Want(x, ids, scale, 0)
+        gl = rng.normal(0, 1, n).astype(np.float32)
+        gh = rng.normal(0, 0.3, n).astype(np.float32)
+        st, h = stats_of(w, dev)
+        t = lambda a: torch.from_numpy(a).to(dev)
+        zero = np.zeros(n)
+        for a, b in ((gl, None), (gl, gh), (None, gh)):
+            d = spmv.token_logprobs_grad(
+                None if a is None else t(a), x.to(dev), ids.to(dev), st, scale=scale,
+                entropy=None if b is None else h, grad_entropy=None if b is None else t(b),
+                dtype=F[out])
+            assert d.dtype == F[out]
+            want, tol = grad_want(w, zero if a is None else a, zero if b is None else b, out)
+            close(d, want, tol, "gradient")
+
+
+def test_gradient_is_the_difference(dev):
+    """Central differences of the forward operator itself, step 2^-5: their error is at most
+    h^2 / 6 of the third derivative, below scale^3 (|gl| / 8 + |gh| (entropy + |lp| + 3)), and
+    the two results' bounds over h."""
+    n, V, scale, h = 2, 13, 1.5, 2.0 ** -5
+    rng = np.random.default_rng(8)
+    x = torch.from_numpy(rng.normal(0, 1, (n, V))).float()
+    ids = torch.tensor([4, 11])
+    gl, gh = np.array([1.0, -2.0]), np.array([0.5, 0.25])
+    w = Want(x, ids, scale, 0)
+    r = spmv.token_logprobs(x.to(dev), ids.to(dev), scale=scale)
+    d = spmv.token_logprobs_grad(torch.tensor(gl).float().to(dev), x.to(dev), ids.to(dev),
+                                 r.stats, entropy=r.entropy, scale=scale,
+                                 grad_entropy=torch.tensor(gh).float().to(dev)).cpu()
+
+    def loss(t):
+        s = spmv.token_logprobs(t.to(dev), ids.to(dev), scale=scale)
+        return (s.logprobs.double().cpu().numpy() * gl
+                + s.entropy.double().cpu().numpy() * gh).sum()
+
+    worst = scale ** 3 * (np.abs(gl) / 8 + gh * (w.entropy + np.abs(w.lpv).max(1) + 3))
+    noise = (np.abs(gl) * w.lp_tol + gh * w.entropy_tol).sum()
+    for t in range(n):
+        for v in range(V):
+            a, b = x.clone(), x.clone()
+            a[t, v] += h
+            b[t, v] -= h
+            diff = (loss(a) - loss(b)) / (a[t, v].double() - b[t, v].double()).item()
+            assert abs(diff - d[t, v].item()) <= h * h / 6 * worst[t] + 2 * noise / h + 1e-6
+
+
+def test_gradient_in_place_and_strides(dev):
+    """`out` may be the logits; rows at any stride and offset; what lies beside them stays."""
+    rng = np.random.default_rng(4)
+    n, V = 37, 5003
+    x, ids = make(n, V, "bf16", 77)
+    w = Want(x, ids, 1.0, 3)
+    gl = rng.normal(0, 1, n).astype(np.float32)
+    g = torch.from_numpy(gl).to(dev)
+    buf = torch.full((n, V + 20), 9.0, dtype=torch.bfloat16, device=dev)
+    view = buf[:, 7:7 + V]
+    view.copy_(x)
+    r = spmv.token_logprobs(view, ids.to(dev), top=3)
+    check(r, w, 3)
+    plain = spmv.token_logprobs_grad(g, x.to(dev), ids.to(dev), r.stats)
+    got = spmv.token_logprobs_grad(g, view, ids.to(dev), r.stats, view)
+    assert got is view and torch.equal(view, plain)
+    assert (buf[:, :7] == 9).all() and (buf[:, 7 + V:] == 9).all()
+    # as a batch has them: [sequences, positions, V]
+    x3, i3 = x[:36].reshape(4, 9, V).to(dev), ids[:36].reshape(4, 9).to(dev)
+    r3 = spmv.token_logprobs(x3, i3, top=3)
+    assert r3.logprobs.shape == (4, 9) and r3.stats.shape == (4, 9, 2)
+    assert r3.top_ids.shape == (4, 9, 3)
+    for a, b in zip(r3, r):
+        assert torch.equal(a.reshape(36, -1), b[:36].reshape(36, -1))
+    d3 = spmv.token_logprobs_grad(g[:36].view(4, 9), x3, i3, r3.stats)
+    assert torch.equal(d3.view(36, V), plain[:36])
+    # outputs that the caller keeps; a row of length zero; no rows
+    again = spmv.TokenLogprobs(*(torch.empty_like(f) for f in r))
+    assert spmv.token_logprobs(view.copy_(x), ids.to(dev), again, top=3) is again
+    assert all(torch.equal(a, b) for a, b in zip(again, r))
+    e = spmv.token_logprobs(x.to(dev)[:, :0], ids.to(dev), top=2)
+    assert (e.logprobs == 0).all() and (e.top_ids == -1).all() and (e.entropy == 0).all()
+    e = spmv.token_logprobs(x.to(dev)[:0], ids.to(dev)[:0], top=2)
+    assert e.logprobs.shape == (0,) and e.top_ids.shape == (0, 2)
+
+
+def test_refusals(dev):
+    x, ids = make(4, 50, "fp16", 1)
+    x, ids = x.to(dev), ids.to(dev)
+    r = spmv.token_logprobs(x, ids)
+    g = torch.ones(4, device=dev)
+    for bad in (0.0, -1.0, float("nan"), INF):
+        with pytest.raises(spmv.SpmvError):
+            spmv.token_logprobs(x, ids, scale=bad)
+    for k in (-1, 65, 2**32 + 1):
+        with pytest.raises(spmv.SpmvError):
+            spmv.token_logprobs(x, ids, top=k)
+    with pytest.raises(ValueError):
+        spmv.token_logprobs(x, ids[:3])
+    with pytest.raises(TypeError):
+        spmv.token_logprobs(x, ids.float())
+    with pytest.raises(TypeError):
+        spmv.token_logprobs(x.double(), ids)
+    with pytest.raises(ValueError):
+        spmv.token_logprobs(x.t(), torch.zeros(50, dtype=torch.int64, device=dev))
+    with pytest.raises(TypeError):
+        spmv.token_logprobs(x, ids, r, top=2)
+    with pytest.raises(ValueError):
+        spmv.token_logprobs(x, ids, spmv.TokenLogprobs(r.logprobs[:2], *r[1:]))
+    with pytest.raises(ValueError):
+        spmv.token_logprobs(x, ids, spmv.TokenLogprobs(r.logprobs, r.logprobs, *r[2:]))
+    with pytest.raises(ValueError):
+        spmv.token_logprobs_grad(g, x, ids, r.stats, grad_entropy=g)
+    with pytest.raises(TypeError):
+        spmv.token_logprobs_grad(g, x, ids, r.stats, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        spmv.token_logprobs_grad(g.half(), x, ids, r.stats)
+    with pytest.raises(ValueError):
+        spmv.token_logprobs_grad(g, x, ids, r.stats[:3])
+    wide = torch.empty(5, 50, dtype=torch.float16, device=dev)
+    with pytest.raises(ValueError):
+        spmv.token_logprobs_grad(g, wide[1:], ids, r.stats, wide[:4])
+    with pytest.raises(ValueError):
+        spmv.token_logprobs(torch.zeros(1, 128000, device=dev), ids[:1],
+                            workspace=torch.empty(16, dtype=torch.uint8, device=dev))
+
+
+def test_streams_and_graphs(dev):
+    """Two steps at once on streams of their own; a captured step replayed on other inputs."""
+    sets = [make(n, 30011, "bf16", n) for n in (2, 5)]
+    want = [spmv.token_logprobs(x.to(dev), i.to(dev), top=7) for x, i in sets]
+    on = [(x.to(dev), i.to(dev)) for x, i in sets]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        got = [spmv.token_logprobs(*on[0], top=7, stream=a),
+               spmv.token_logprobs(*on[1], top=7, stream=b.cuda_stream)]
+        junk = torch.full((1 << 20,), 7.0, device=dev)
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(g, w))
+        del junk
+    graphs = []
+    for x, i in on:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            spmv.token_logprobs(x, i, top=7)
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        weight = torch.ones(len(i), device=dev)
+        with torch.cuda.graph(g):
+            r = spmv.token_logprobs(x, i, top=7)
+            d = spmv.token_logprobs_grad(weight, x, i, r.stats, entropy=r.entropy,
+                                         grad_entropy=weight)
+        graphs.append((g, x, i, r, d, weight))
+    for turn in range(3):
+        for g, x, i, r, d, weight in graphs:
+            y, j = make(len(i), 30011, "bf16", 100 + turn)
+            x.copy_(y)
+            i.copy_(j)
+            for f in (*r, d):
+                f.fill_(5)
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            s = spmv.token_logprobs(x, i, top=7)
+            e = spmv.token_logprobs_grad(weight, x, i, s.stats, entropy=s.entropy,
+                                         grad_entropy=weight)
+            assert all(torch.equal(p, q) for p, q in zip(r, s)) and torch.equal(d, e)
+
+
+def test_long_offsets(dev):
+    """Rows whose elements lie past 2^31 and 2^32."""
+    n, V = 34000, 128001
+    x = torch.zeros(n, V, dtype=torch.bfloat16, device=dev)
+    ids = (torch.arange(n, device=dev) * 37) % V
+    x[torch.arange(n, device=dev), ids] = 20.0
+    r = spmv.token_logprobs(x, ids, top=2)
+    total = np.log1p((V - 1) * np.exp(-20.0))
+    assert (r.logprobs.double().cpu() + total).abs().max() < 1e-6
+    assert torch.equal(r.top_ids[:, 0], ids)
+    assert torch.equal(r.top_ids[:, 1], (ids == 0).long())
+    d = spmv.token_logprobs_grad(torch.ones(n, device=dev), x, ids, r.stats, x)
+    p = 1 / (1 + (V - 1) * np.exp(-20.0))
+    at = d[torch.arange(n, device=dev), ids].double().cpu()
+    assert (at - (1 - p)).abs().max() <= (1 - p) * 2.0 ** -8
+    assert (d[-1].float().sum() - at[-1]).item() < 0

@@ -1,0 +1,108 @@
+"""Operators on a step's rows, checks that need no GPU: the C entry points refuse bad arguments
+before any device call, workspace sizes, the binding's types and sizes."""
+import ctypes
+
+import pytest
+
+import spmv_storage_formats_amd as spmv
+
+INVALID, TOO_LARGE = 1, 5
+P = ctypes.c_void_p(4096)    # a pointer that no refused call follows
+FP32, FP16, BF16, INT32, INT64 = range(5)
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return spmv.load_library()
+
+
+def test_constants_match_the_header():
+    import os
+    import re
+    hdr = open(os.path.join(os.path.dirname(spmv.__file__), "..", "include", "spmv.h")).read()
+    defs = {m.group(1): int(m.group(2)) for m in re.finditer(r"#define (SPMV_\w+) (\d+)", hdr)}
+    assert defs["SPMV_TOKEN_TOP_MOST"] == spmv.TOKEN_TOP_MOST == 64
+
+
+def logprobs(lib, **change):
+    a = dict(V=100, n=3, x=P, ld=100, dtype=BF16, ids=P, id=INT64, scale=1.0, top=2, lp=P, h=P,
+             st=P, ti=P, tl=P, ws=P, size=1 << 20)
+    a.update(change)
+    return lib.spmv_token_logprobs(a["V"], a["n"], a["x"], a["ld"], a["dtype"], a["ids"],
+                                   a["id"], a["scale"], a["top"], a["lp"], a["h"], a["st"],
+                                   a["ti"], a["tl"], a["ws"], a["size"], None)
+
+
+@pytest.mark.parametrize("change,status", [
+    ({"V": -1}, INVALID), ({"n": -1}, INVALID), ({"dtype": INT32}, INVALID),
+    ({"id": FP32}, INVALID), ({"top": -1}, INVALID), ({"top": 65}, INVALID),
+    ({"scale": 0.0}, INVALID), ({"scale": -1.0}, INVALID), ({"scale": NAN}, INVALID),
+    ({"scale": INF}, INVALID), ({"x": None}, INVALID), ({"ld": 99}, INVALID),
+    ({"ids": None}, INVALID), ({"lp": None}, INVALID), ({"ti": None}, INVALID),
+    ({"tl": None}, INVALID), ({"V": 2**31 - 1, "ld": 2**31}, TOO_LARGE),
+    ({"V": 2**31 - 65536, "ld": 2**31}, TOO_LARGE), ({"n": 2**31}, TOO_LARGE),
+    ({"V": 50000, "ld": 50000, "ws": None}, INVALID),
+    ({"V": 50000, "ld": 50000, "ws": ctypes.c_void_p(4100)}, INVALID),
+    ({"V": 50000, "ld": 50000, "size": 64}, INVALID)])
+def test_logprobs_refusals(lib, change, status):
+    assert logprobs(lib, **change) == status
+
+
+def test_nothing_to_score_is_no_error(lib):
+    assert logprobs(lib, n=0, x=None, ids=None, lp=None, ti=None, tl=None, ws=None) == 0
+
+
+@pytest.mark.parametrize("change,status", [
+    ({"V": -1}, INVALID), ({"n": -1}, INVALID), ({"dtype": INT64}, INVALID),
+    ({"id": BF16}, INVALID), ({"to": FP16}, INVALID), ({"to": INT32}, INVALID),
+    ({"scale": 0.0}, INVALID), ({"scale": NAN}, INVALID), ({"x": None}, INVALID),
+    ({"ld": 99}, INVALID), ({"out_ld": 99}, INVALID), ({"ids": None}, INVALID),
+    ({"st": None}, INVALID), ({"h": None}, INVALID), ({"out": None}, INVALID),
+    ({"out": P, "to": FP32}, INVALID), ({"out": P, "out_ld": 101}, INVALID),
+    ({"V": 2**31 - 65536, "ld": 2**31, "out_ld": 2**31}, TOO_LARGE), ({"n": 2**31}, TOO_LARGE)])
+def test_logprobs_grad_refusals(lib, change, status):
+    a = dict(V=100, n=3, x=P, ld=100, dtype=BF16, ids=P, id=INT64, scale=1.0, st=P, g=P, h=P,
+             gh=P, out=ctypes.c_void_p(1 << 20), out_ld=100, to=BF16)
+    a.update(change)
+    assert lib.spmv_token_logprobs_grad(
+        a["V"], a["n"], a["x"], a["ld"], a["dtype"], a["ids"], a["id"], a["scale"], a["st"],
+        a["g"], a["h"], a["gh"], a["out"], a["out_ld"], a["to"], None) == status
+
+
+def test_no_logits_have_no_gradient(lib):
+    assert lib.spmv_token_logprobs_grad(100, 0, None, 100, FP32, None, INT32, 1.0, None, None,
+                                        None, None, None, 100, FP32, None) == 0
+    assert lib.spmv_token_logprobs_grad(0, 7, None, 0, FP32, P, INT32, 1.0, P, P,
+                                        None, None, None, 0, FP32, None) == 0
+
+
+def test_logprobs_workspace(lib):
+    size = ctypes.c_size_t()
+    for bad in ((-1, 1, 0), (1, -1, 0), (1, 1, -1), (1, 1, 65)):
+        assert lib.spmv_token_logprobs_workspace(*bad, ctypes.byref(size)) == INVALID
+    assert lib.spmv_token_logprobs_workspace(10, 1, 0, None) == INVALID
+    assert lib.spmv_token_logprobs_workspace(2**31 - 65536, 1, 0, ctypes.byref(size)) == TOO_LARGE
+    assert lib.spmv_token_logprobs_workspace(2**31 - 65537, 1, 0, ctypes.byref(size)) == 0
+    assert spmv.token_logprobs_workspace(0, 128000, 5) == 0
+    assert spmv.token_logprobs_workspace(5000, 128000, 5) == 0
+    # three numbers of each part's statistics, a key of 8 bytes per alternative
+    few, more = (spmv.token_logprobs_workspace(2, 128000, k) for k in (0, 10))
+    assert few >= 2 * 2 * 12 and (more - few) % 160 == 0 and more > few
+    for wrap in (2**32 + 5, -2**32 + 8):
+        with pytest.raises(spmv.SpmvError):
+            spmv.token_logprobs_workspace(1, wrap, 0)
+        with pytest.raises(spmv.SpmvError):
+            spmv.token_logprobs_workspace(wrap, 5, 0)
+        with pytest.raises(spmv.SpmvError):
+            spmv.token_logprobs_workspace(1, 5, wrap)
+
+
+def test_binding_rejects_host_tensors():
+    torch = pytest.importorskip("torch")
+    x, ids = torch.zeros(3, 10), torch.zeros(3, dtype=torch.int64)
+    for call in (lambda: spmv.token_logprobs(x, ids),
+                 lambda: spmv.token_logprobs_grad(torch.zeros(3), x, ids, torch.zeros(3, 2)),
+                 lambda: spmv.token_logprobs(None, ids), lambda: spmv.token_logprobs([1.0], ids)):
+        with pytest.raises(TypeError):
+            call()
