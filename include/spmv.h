@@ -622,7 +622,8 @@ spmv_status spmv_lookup_grad(int32_t num_rows, int32_t num_cols, int64_t n, cons
                              void *workspace_dev, size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
- * Rows of a step: log probabilities of given tokens, and their gradient.
+ * Rows of a step: log probabilities of given tokens and low-rank adapters, with
+ * their gradients.
  *
  * Types, row strides, alignment, streams and reproducibility as for the weight
  * tables above.  Nothing is allocated, nothing synchronises, every call can be
@@ -680,6 +681,60 @@ spmv_status spmv_token_logprobs_grad(int32_t num_cols, int64_t n, const void *lo
                                      const float *grad_logprobs_dev, const float *entropy_dev,
                                      const float *grad_entropy_dev, void *out_dev,
                                      int64_t out_ld, spmv_dtype out_dtype, void *stream);
+
+/*
+ * Low-rank adapters beside a shared projection (spmv_quant_run, or any other).
+ * Adapter a of `num_adapters` is a pair of matrices, stored contiguously with those of
+ * the other adapters: down [num_adapters, rank, C] and up [num_adapters, R, rank], both
+ * of x's type, and a factor scales_dev[a] (fp32; NULL: 1).  Row t of x [n, C] uses
+ * adapter ids[t]; rows whose id is outside [0, num_adapters) use none.  Rows of one
+ * adapter need not lie together.
+ *   1 <= rank <= 256; at most 2048 adapters, 2^24 rows, 2^23 columns (else
+ *   SPMV_ERR_TOO_LARGE).  Smaller ranks are stored with zeros.
+ *   Numbers between two products (down[a] x[t], up[a]^T grad[t]) are kept in fp32 and
+ *   enter the next one with all their bits, but with 16 of them where x's type and the
+ *   result's are bf16 (a result of 8 bits).  NaN and infinities in a row reach that
+ *   row's results, and its adapter's gradients, only.
+ *   Workspaces are 16-byte aligned and used until the work on `stream` is done; calls
+ *   that may overlap in time need workspaces of their own.
+ *
+ * spmv_adapt --  out[t] = base[t] + scales[a] * up[a] (down[a] x[t]),  a = ids[t];
+ *   rows without an adapter get base[t].
+ *   out_dev: [n, R] of dtype or SPMV_FP32; base_dev: [n, R] of out_dtype, NULL: zeros;
+ *   base_dev may be out_dev (same stride), and must not overlap it otherwise.
+ */
+spmv_status spmv_adapt_workspace(int32_t num_adapters, int32_t rank, int32_t num_cols,
+                                 int32_t num_rows, int64_t n, size_t *bytes);
+spmv_status spmv_adapt(int32_t num_adapters, int32_t rank, int32_t num_cols, int32_t num_rows,
+                       int64_t n, const void *x_dev, int64_t x_ld, spmv_dtype dtype,
+                       const void *down_dev, const void *up_dev, const float *scales_dev,
+                       const void *ids_dev, spmv_dtype id_dtype, const void *base_dev,
+                       int64_t base_ld, void *out_dev, int64_t out_ld, spmv_dtype out_dtype,
+                       void *workspace_dev, size_t workspace_bytes, void *stream);
+
+/*
+ * spmv_adapt_grad -- the gradients of spmv_adapt for grad_dev [n, R] (of dtype), the
+ * gradient of its result:
+ *     g[t] = scales[a] * up[a]^T grad[t],      dx[t]  = base[t] + down[a]^T g[t],
+ *     ddown[a] = sum of g[t] x[t]^T,           dup[a] = scales[a] * sum of grad[t] (down[a] x[t])^T
+ *   over the rows t of a (added to ddown, dup if accumulate is nonzero).
+ *   dx_dev: [n, C] of dtype, NULL: not wanted; base_dev: [n, C] of dtype (the gradient
+ *   that reaches x through the shared projection), NULL: zeros; it may be dx_dev.
+ *   ddown_dev, dup_dev: as down and up, of weight_dtype (dtype or SPMV_FP32); either may
+ *   be NULL.  Without `accumulate` adapters without rows get zeros; with it they are left
+ *   untouched.  The order in which an adapter's rows are summed follows from the ids and
+ *   sizes alone.
+ */
+spmv_status spmv_adapt_grad_workspace(int32_t num_adapters, int32_t rank, int32_t num_cols,
+                                      int32_t num_rows, int64_t n, size_t *bytes);
+spmv_status spmv_adapt_grad(int32_t num_adapters, int32_t rank, int32_t num_cols,
+                            int32_t num_rows, int64_t n, const void *grad_dev, int64_t grad_ld,
+                            const void *x_dev, int64_t x_ld, spmv_dtype dtype,
+                            const void *down_dev, const void *up_dev, const float *scales_dev,
+                            const void *ids_dev, spmv_dtype id_dtype, const void *base_dev,
+                            int64_t base_ld, void *dx_dev, int64_t dx_ld, void *ddown_dev,
+                            void *dup_dev, spmv_dtype weight_dtype, int32_t accumulate,
+                            void *workspace_dev, size_t workspace_bytes, void *stream);
 
 const char *spmv_status_string(spmv_status status);
 const char *spmv_format_name(spmv_format format);

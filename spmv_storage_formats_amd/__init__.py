@@ -22,6 +22,8 @@ Rows of a step (one request's or sequence's each):
 
     r = spmv.token_logprobs(logits, ids, top=5)      # log probabilities, entropies, alternatives
     dlogits = spmv.token_logprobs_grad(dlogprobs, logits, ids, r.stats)
+    spmv.adapt(x, down, up, adapter_ids, y, y)       # y += up[a] (down[a] x), low-rank adapters
+    dx, ddown, dup = spmv.adapt_grad(dy, x, down, up, adapter_ids)
 """
 from __future__ import annotations
 
@@ -39,7 +41,8 @@ __all__ = ["SpmvError", "Handle", "FORMATS", "ARRAYS", "load_library", "analyze"
            "build", "build_coo", "build_tuned", "coo_to_csr", "library_path",
            "declared_functions", "QuantHandle", "build_quant", "build_quant_packed", "lookup",
            "lookup_grad", "lookup_grad_workspace", "TokenLogprobs", "token_logprobs",
-           "token_logprobs_grad", "token_logprobs_workspace"]
+           "token_logprobs_grad", "token_logprobs_workspace", "adapt", "adapt_workspace",
+           "adapt_grad", "adapt_grad_workspace"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_PKG)
@@ -210,6 +213,17 @@ def load_library():
                                                         _vp, ctypes.c_int, ctypes.c_float, _vp,
                                                         _vp, _vp, _vp, _vp, _i64, ctypes.c_int,
                                                         _vp]),
+            "spmv_adapt_workspace": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i64,
+                                                    P(ctypes.c_size_t)]),
+            "spmv_adapt": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i64, _vp, _i64, ctypes.c_int,
+                                          _vp, _vp, _vp, _vp, ctypes.c_int, _vp, _i64, _vp, _i64,
+                                          ctypes.c_int, _vp, ctypes.c_size_t, _vp]),
+            "spmv_adapt_grad_workspace": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i64,
+                                                         P(ctypes.c_size_t)]),
+            "spmv_adapt_grad": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i64, _vp, _i64, _vp,
+                                               _i64, ctypes.c_int, _vp, _vp, _vp, _vp,
+                                               ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _vp,
+                                               ctypes.c_int, _i32, _vp, ctypes.c_size_t, _vp]),
             "spmv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "spmv_format_name": (ctypes.c_char_p, [ctypes.c_int]),
         }
@@ -1107,3 +1121,193 @@ def token_logprobs_grad(grad, logits, ids, stats, out=None, *, entropy=None, gra
         V, n, xp, x_ld, xk, ip, ik, scale, sp, gp, ep, hp, op, o_ld, ok,
         _stream_of(index, stream, *made)), "spmv_token_logprobs_grad")
     return out
+
+
+def adapt_workspace(num_rows: int, num_adapters: int, rank: int, in_features: int,
+                    out_features: int) -> int:
+    """Bytes of workspace that adapt needs for these sizes."""
+    return _adapt_bytes("spmv_adapt_workspace", int(num_adapters), int(rank), int(in_features),
+                        int(out_features), int(num_rows))
+
+
+def adapt_grad_workspace(num_rows: int, num_adapters: int, rank: int, in_features: int,
+                         out_features: int) -> int:
+    """Bytes of workspace that adapt_grad needs for these sizes."""
+    return _adapt_bytes("spmv_adapt_grad_workspace", int(num_adapters), int(rank),
+                        int(in_features), int(out_features), int(num_rows))
+
+
+@functools.lru_cache(maxsize=128)
+def _adapt_bytes(name, *sizes):
+    _fits(name, *sizes)
+    size = ctypes.c_size_t()
+    _check(getattr(load_library(), name)(*sizes, ctypes.byref(size)), name)
+    return size.value
+
+
+def _adapters(down, up, scales, like, index):
+    """(adapters, rank, C, R, pointers of down, up and scales) of a table of adapters."""
+    import torch
+    if not (isinstance(down, torch.Tensor) and isinstance(up, torch.Tensor)):
+        raise TypeError("down and up must be cuda tensors")
+    if down.dim() != 3 or up.dim() != 3 or up.shape[0] != down.shape[0] \
+            or up.shape[2] != down.shape[1]:
+        raise ValueError(f"down and up must be [L, rank, C] and [L, R, rank], got "
+                         f"{tuple(down.shape)} and {tuple(up.shape)}")
+    for t, name in ((down, "down"), (up, "up")):
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    L, rank, C = down.shape
+    sp = None if scales is None else _like(scales, (L,), torch.float32, index, "scales")
+    return (L, rank, C, up.shape[1], _dev(down, like.dtype, "down"), _dev(up, like.dtype, "up"),
+            sp)
+
+
+def _unless(t, flat, base, what):
+    """Refuse a result that overlaps an operand, unless it is `base` itself."""
+    if base is not None and base.data_ptr() == flat.data_ptr() and \
+            base.stride() == flat.stride() and base.dtype == flat.dtype:
+        base = None
+    for other in (*t, base):
+        if other is not None:
+            _apart(other, flat, what)
+
+
+def adapt(x, down, up, ids, base=None, out=None, *, scales=None, dtype=None, workspace=None,
+          stream=None):
+    """Low-rank adapters beside a shared projection: out[t, :] = base[t, :] + scales[a] * up[a]
+    @ (down[a] @ x[t, :]) with a = ids[t], for rows of many requests at once; rows whose id is
+    outside [0, L) (no adapter) get base[t, :].  x: ids.shape + [C], down [L, rank, C] and up
+    [L, R, rank] of x's type (fp32, fp16 or bf16), contiguous; scales: fp32 [L] (default: 1);
+    base: ids.shape + [R] (default: zeros).  Returns `out`, ids.shape + [R] (default: a new
+    tensor of `dtype`, x's unless given; fp32 otherwise), of base's type; it may be `base`
+    itself.  `workspace`: a contiguous uint8 cuda tensor of at least adapt_workspace() bytes,
+    for this call alone until its work is done (default: allocated for the call).  Records no
+    autograd graph: adapt_grad is its backward pass."""
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() < 1:
+        raise TypeError("x must be a cuda tensor")
+    index = x.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return adapt(x, down, up, ids, base, out, scales=scales, dtype=dtype,
+                         workspace=workspace, stream=stream)
+    ip, n, ik, ie = _token_ids(ids, index)
+    L, rank, C, R, dp, up_p, sp = _adapters(down, up, scales, x, index)
+    need = _adapt_bytes("spmv_adapt_workspace", L, rank, C, R, n)
+    xp, x_ld, xk, xe = _rows(_by_token(x, ids, C, "x"), "x", index, n, C)
+    made = []
+    if out is None:
+        out = torch.empty((*ids.shape, R), device=x.device,
+                          dtype=dtype or (x.dtype if base is None else base.dtype))
+        made.append(out)
+    flat = _by_token(out, ids, R, "out", dtype)
+    op, o_ld, ok, oe = _rows(flat, "out", index, n, R)
+    if ok != xk and ok != 0:
+        raise TypeError(f"out must be {x.dtype} or torch.float32, got {out.dtype}")
+    bp, b_ld, rows = None, 0, None
+    if base is not None:
+        rows = _by_token(base, ids, R, "base", out.dtype)
+        bp, b_ld, _, _ = _rows(rows, "base", index, n, R)
+    if not made:
+        _unless((_by_token(x, ids, C, "x"), down, up, ids, scales), flat, rows,
+                "out and other tensors")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        made.append(workspace)
+        wp, size = workspace.data_ptr(), need
+    else:
+        wp, size = _workspace(workspace, need, index)
+        for t in (x, down, up, ids, scales, base, out):
+            if t is not None:
+                _apart(workspace, t, "workspace and other tensors")
+    _check(load_library().spmv_adapt(
+        L, rank, C, R, n, xp, x_ld, xk, dp, up_p, sp, ip, ik, bp, b_ld, op, o_ld, ok, wp, size,
+        _stream_of(index, stream, *made)), "spmv_adapt")
+    return out
+
+
+def adapt_grad(grad, x, down, up, ids, base=None, dx=None, ddown=None, dup=None, *, scales=None,
+               accumulate: bool = False, dtype=None, workspace=None, stream=None):
+    """Gradients of adapt for `grad` (ids.shape + [R], of x's type), the gradient of its result:
+    returns (dx, ddown, dup), with g[t] = scales[a] * up[a].T @ grad[t],
+    dx[t] = base[t] + down[a].T @ g[t] (x's type; base: the gradient that reaches x through the
+    shared projection, default zeros), ddown[a] the sum of g[t] x[t].T and dup[a] that of
+    scales[a] * grad[t] (down[a] @ x[t]).T over the rows of a, added to ddown and dup with
+    `accumulate` (adapters without rows then stay as they are).  The three are new tensors unless
+    given, ddown and dup of `dtype` (x's, or fp32; default: x's); False: not wanted (None is
+    returned).  dx may be `base` itself.  `workspace`: a contiguous uint8 cuda tensor of at least
+    adapt_grad_workspace() bytes, for this call alone until its work is done (default:
+    allocated for the call)."""
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() < 1:
+        raise TypeError("x must be a cuda tensor")
+    index = x.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return adapt_grad(grad, x, down, up, ids, base, dx, ddown, dup, scales=scales,
+                              accumulate=accumulate, dtype=dtype, workspace=workspace,
+                              stream=stream)
+    ip, n, ik, ie = _token_ids(ids, index)
+    L, rank, C, R, dp, up_p, sp = _adapters(down, up, scales, x, index)
+    need = _adapt_bytes("spmv_adapt_grad_workspace", L, rank, C, R, n)
+    x2 = _by_token(x, ids, C, "x")
+    xp, x_ld, xk, xe = _rows(x2, "x", index, n, C)
+    g2 = _by_token(grad, ids, R, "grad", x.dtype)
+    gp, g_ld, gk, ge = _rows(g2, "grad", index, n, R)
+    if accumulate and (ddown is None or dup is None):
+        raise ValueError("accumulate needs ddown and dup (or False)")
+    made = []
+    inputs = (x2, g2, down, up, ids, scales)
+    xo, xo_ld, bp, b_ld, rows = None, 0, None, 0, None
+    if dx is not False:
+        if base is not None:
+            rows = _by_token(base, ids, C, "base", x.dtype)
+            bp, b_ld, _, _ = _rows(rows, "base", index, n, C)
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            made.append(dx)
+            flat = _by_token(dx, ids, C, "dx")
+        else:
+            flat = _by_token(dx, ids, C, "dx", x.dtype)
+            _unless(inputs, flat, rows, "dx and other tensors")
+        xo, xo_ld, _, _ = _rows(flat, "dx", index, n, C)
+    given, pointers, kind = [], [], None
+    for t, like, name in ((ddown, down, "ddown"), (dup, up, "dup")):
+        if t is None:
+            t = torch.empty(like.shape, dtype=dtype or x.dtype, device=x.device)
+            made.append(t)
+        elif t is not False:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a cuda tensor")
+            _like(t, like.shape, dtype or t.dtype, index, name)
+            for other in (*inputs, rows, *(g for g in given if g is not False)):
+                if other is not None:
+                    _apart(other, t, f"{name} and other tensors")
+            if dx is not False:
+                _apart(dx, t, f"{name} and dx")
+        if t is not False:
+            k = _kind(t.dtype, _FLOATS, name)
+            if k != xk and k != 0:
+                raise TypeError(f"{name} must be {x.dtype} or torch.float32, got {t.dtype}")
+            if kind is not None and k != kind:
+                raise TypeError("ddown and dup must be of one type")
+            kind = k
+        given.append(t)
+        pointers.append(None if t is False or t.numel() == 0 else t.data_ptr())
+    ddown, dup = given
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        made.append(workspace)
+        wp, size = workspace.data_ptr(), need
+    else:
+        wp, size = _workspace(workspace, need, index)
+        for t in (*inputs, rows, dx, ddown, dup):
+            if t is not None and t is not False:
+                _apart(workspace, t, "workspace and other tensors")
+    if need:
+        _check(load_library().spmv_adapt_grad(
+            L, rank, C, R, n, gp, g_ld, xp, x_ld, xk, dp, up_p, sp, ip, ik, bp, b_ld, xo, xo_ld,
+            pointers[0], pointers[1], 0 if kind is None else kind, 1 if accumulate else 0, wp,
+            size, _stream_of(index, stream, *made)), "spmv_adapt_grad")
+    return tuple(None if t is False else t for t in (dx, ddown, dup))

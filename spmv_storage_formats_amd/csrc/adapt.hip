@@ -1,0 +1,380 @@
+// Low-rank adapters of many requests (formulas and kernels of the products:
+// adapt.h): rows sorted by adapter, plans and launches, and the join of the
+// matrices' gradients.
+#include "adapt.h"
+
+namespace spmv {
+namespace {
+
+constexpr int kGroupThreads = 1024;
+constexpr int kGroupBlocks = 64;       // workgroups that sort the rows, at most
+constexpr int kKeys = kMostAdapters + 1;
+
+struct GroupArgs {
+    const void *ids;
+    int32_t n, adapters;
+    int32_t block;          // rows of a workgroup, a multiple of kGroupThreads
+    int32_t chunk;          // rows of a chunk, at most
+    int32_t *order;
+    AdaptTile *tiles, *chunks;      // chunks null: not wanted
+    int32_t most_tiles, most_chunks;
+    int32_t *chunk_start;   // [adapters + 1]
+};
+
+// A row's key: its adapter, or `adapters` where it names none.
+template <typename I>
+__device__ inline int32_t adapter_key(const void *ids, int32_t t, int32_t adapters) {
+    const int64_t id = static_cast<const I *>(ids)[t];
+    return id >= 0 && id < adapters ? static_cast<int32_t>(id) : adapters;
+}
+
+// Exclusive prefix sums in place of v[0 .. m), their total to v[m].  m <= kKeys.
+__device__ inline void prefix(int32_t *v, int32_t m, int32_t *wsum) {
+    constexpr int E = (kKeys + kGroupThreads - 1) / kGroupThreads;
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    int32_t own[E], sum = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const int at = threadIdx.x * E + i;
+        own[i] = at < m ? v[at] : 0;
+        sum += own[i];
+    }
+    int32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const int32_t t = __shfl_up(incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == kWave - 1) wsum[wave] = incl;
+    __syncthreads();
+    int32_t at = incl - sum;
+    for (int w = 0; w < wave; ++w) at += wsum[w];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const int k = threadIdx.x * E + i;
+        if (k < m) v[k] = at;
+        at += own[i];
+        if (k == m - 1) v[m] = at;
+    }
+    __syncthreads();
+}
+
+// Rows sorted by adapter, stably, and the lists of tiles and chunks, in one
+// launch: every workgroup counts the keys of all rows and of those before its
+// block, and places its block's rows.
+template <typename I>
+__global__ __launch_bounds__(kGroupThreads) void k_adapt_group(GroupArgs a) {
+    __shared__ int32_t s_count[kKeys + 1], s_start[kKeys + 1], s_place[kKeys + 1],
+        s_first[kKeys + 1];
+    __shared__ int32_t s_wsum[kGroupThreads / kWave];
+    const int lane = threadIdx.x % kWave, tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int32_t keys = a.adapters + 1;
+    const int32_t own = static_cast<int32_t>(blockIdx.x) * a.block;
+    for (int k = tid; k < keys; k += kGroupThreads) s_count[k] = s_place[k] = 0;
+    __syncthreads();
+    for (int32_t at = wave * kWave; at < a.n; at += kGroupThreads) {
+        const int32_t t = at + lane;
+        const int32_t key = t < a.n ? adapter_key<I>(a.ids, t, a.adapters) : -1;
+        const bool early = at < own;  // whole waves lie before the block or not
+        const int32_t first = __builtin_amdgcn_readfirstlane(key);
+        if (__all(key == first)) {    // a request's rows lie together
+            if (lane == 0) {
+                atomicAdd(&s_count[first], kWave);
+                if (early) atomicAdd(&s_place[first], kWave);
+            }
+        } else if (key >= 0) {
+            atomicAdd(&s_count[key], 1);
+            if (early) atomicAdd(&s_place[key], 1);
+        }
+    }
+    __syncthreads();
+    for (int k = tid; k < keys; k += kGroupThreads) s_start[k] = s_count[k];
+    prefix(s_start, keys, s_wsum);
+    for (int k = tid; k < keys; k += kGroupThreads) s_place[k] += s_start[k];
+    __syncthreads();
+    // the block's rows: 1024 at a time, wave after wave
+    const int32_t end = a.n - own < a.block ? a.n : own + a.block;
+    const unsigned long long below = (1ull << lane) - 1ull;
+    for (int32_t at = own; at < end; at += kGroupThreads) {
+        const int32_t t = at + tid;
+        const bool there = t < end;
+        const int32_t key = there ? adapter_key<I>(a.ids, t, a.adapters) : 0;
+        unsigned long long peers = __ballot(there);
+        for (int b = 0; (keys - 1) >> b; ++b) {
+            const bool bit = (key >> b) & 1;
+            const unsigned long long m = __ballot(bit);
+            peers &= bit ? m : ~m;
+        }
+        const int rank = __popcll(peers & below);
+        int32_t to = 0;
+        for (int w = 0; w < kGroupThreads / kWave; ++w) {
+            if (w == wave && there) {
+                to = s_place[key] + rank;
+                // every lane of a key reads before its first one writes
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                if (rank == 0) s_place[key] += __popcll(peers);
+            }
+            __syncthreads();
+        }
+        if (there) a.order[to] = t;
+    }
+    // the lists, shared out over the workgroups
+    auto list = [&](AdaptTile *out, int32_t most, int32_t length) {
+        for (int32_t j = static_cast<int32_t>(blockIdx.x) * kGroupThreads + tid; j < most;
+             j += static_cast<int32_t>(gridDim.x) * kGroupThreads) {
+            AdaptTile tile{-1, 0, 0, 0};
+            if (j < s_first[keys]) {
+                int32_t lo = 0, hi = keys - 1;  // last key whose first tile is not behind j
+                while (lo < hi) {
+                    const int32_t mid = (lo + hi + 1) >> 1;
+                    if (s_first[mid] <= j) lo = mid; else hi = mid - 1;
+                }
+                const int32_t k = (j - s_first[lo]) * length;
+                const int32_t left = s_count[lo] - k;
+                tile = {lo, s_start[lo] + k, left < length ? left : length, 0};
+            }
+            out[j] = tile;
+        }
+    };
+    for (int k = tid; k < keys; k += kGroupThreads)
+        s_first[k] = (s_count[k] + kAdaptTile - 1) / kAdaptTile;
+    prefix(s_first, keys, s_wsum);
+    list(a.tiles, a.most_tiles, kAdaptTile);
+    if (!a.chunks) return;
+    __syncthreads();
+    // rows without an adapter have no share in the matrices
+    for (int k = tid; k < keys; k += kGroupThreads)
+        s_first[k] = k < a.adapters ? (s_count[k] + a.chunk - 1) / a.chunk : 0;
+    prefix(s_first, keys, s_wsum);
+    list(a.chunks, a.most_chunks, a.chunk);
+    if (blockIdx.x == 0)
+        for (int k = tid; k < keys; k += kGroupThreads) a.chunk_start[k] = s_first[k];
+}
+
+// Sums of the splits, scaled, rank by rank: what the matrices' gradients read.
+__global__ __launch_bounds__(kAdaptThreads) void k_adapt_finish(FinishArgs a, FinishArgs b) {
+    const FinishArgs &f = blockIdx.y == 0 ? a : b;
+    const AdaptTile tile = f.tiles[blockIdx.x];
+    if (tile.adapter < 0 || tile.adapter >= f.adapters) return;
+    const float scale = f.scales ? f.scales[tile.adapter] : 1.f;
+    for (int i = threadIdx.x; i < tile.count * f.width; i += kAdaptThreads) {
+        const int32_t k = i % f.width, at = tile.first + i / f.width;
+        float v = 0.f;
+        if (k < f.rank) {
+            for (int32_t j = 0; j < f.splits; ++j)
+                v += f.sums[(static_cast<int64_t>(j) * f.n + at) * f.width + k];
+            v *= scale;
+        }
+        f.out[static_cast<int64_t>(k) * f.stride + at] = v;
+    }
+}
+
+// The chunks' sums of a matrix's gradient, joined in their order.
+struct JoinArgs {
+    const float *down, *up;   // chunks x [rank, C], [R, rank]
+    const int32_t *chunk_start;
+    int64_t down_size, up_size;
+    void *ddown, *dup;
+    int32_t accumulate;
+};
+
+template <typename B>
+__global__ __launch_bounds__(kAdaptThreads) void k_adapt_join(JoinArgs a) {
+    constexpr int E = 4;
+    const int32_t adapter = static_cast<int32_t>(blockIdx.y);
+    const int32_t first = a.chunk_start[adapter], last = a.chunk_start[adapter + 1];
+    if (first == last && a.accumulate) return;
+    const bool up = blockIdx.z == 1;
+    const int64_t size = up ? a.up_size : a.down_size;
+    const float *from = up ? a.up : a.down;
+    B *out = static_cast<B *>(up ? a.dup : a.ddown) + adapter * size;
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kAdaptThreads + threadIdx.x) * E;
+         i < size; i += static_cast<int64_t>(gridDim.x) * kAdaptThreads * E) {
+        const bool whole = i + E <= size;
+        const int left = static_cast<int>(size - i < E ? size - i : E);
+        float sum[E] = {0.f, 0.f, 0.f, 0.f}, v[E];
+        for (int32_t c = first; c < last; ++c) {
+            if (whole)
+                load_piece<E>(from + c * size + i, v);
+            else
+                load_piece_tail<E>(from + c * size + i, left, v);
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum[e] += v[e];
+        }
+        if (a.accumulate) {
+            if (whole)
+                load_piece<E>(out + i, v);
+            else
+                load_piece_tail<E>(out + i, left, v);
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum[e] += v[e];
+        }
+        if (whole)
+            store_piece<E>(out + i, sum);
+        else
+            store_piece_tail<E>(out + i, left, sum);
+    }
+}
+
+size_t round16(size_t b) { return (b + 15) / 16 * 16; }
+
+// Sizes that follow from the arguments, and the workspace's parts.
+struct Plan {
+    int32_t width, tiles, chunk, chunks, stride;
+    int32_t splits_c, part_c, splits_r, part_r;
+    size_t order, tile_list, chunk_list, chunk_start, sums_c, sums_r, v_c, v_r, down, up, end;
+};
+
+// Parts of D columns: workgroups for the whole card, no part of less than 256.
+void split(int32_t D, int32_t tiles, int32_t *splits, int32_t *part) {
+    constexpr int32_t kGroups = 768, kUnit = kAdaptWaves * 32;
+    const int32_t units = std::max(1, (D + kUnit - 1) / kUnit);
+    const int32_t want = std::min(std::max(1, kGroups / std::max(1, tiles)), std::max(1, units / 2));
+    const int32_t per = (units + want - 1) / want;
+    *splits = (units + per - 1) / per;
+    *part = per * kUnit;
+}
+
+Plan plan(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R, bool grad) {
+    Plan p{};
+    p.width = adapt_width(rank);
+    // a last tile of each adapter that has rows, and of the rows without one
+    p.tiles = (n + kAdaptTile - 1) / kAdaptTile + std::min(adapters + 1, n);
+    p.chunk = std::max(kAdaptChunk, (n / 64 + 31) / 32 * 32);
+    p.chunks = (n + p.chunk - 1) / p.chunk + std::min(adapters, n);
+    p.stride = (n + 63) / 16 * 16;  // chunks are read past their last row, by 47 at most
+    split(C, p.tiles, &p.splits_c, &p.part_c);
+    split(R, p.tiles, &p.splits_r, &p.part_r);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += round16(bytes);
+        return here;
+    };
+    const size_t rows = static_cast<size_t>(n) * p.width * sizeof(float);
+    p.order = take(static_cast<size_t>(n) * sizeof(int32_t));
+    p.tile_list = take(static_cast<size_t>(p.tiles) * sizeof(AdaptTile));
+    p.sums_c = take(rows * p.splits_c);
+    if (grad) {
+        const size_t cut = static_cast<size_t>(p.chunks) * rank * sizeof(float);
+        p.chunk_list = take(static_cast<size_t>(p.chunks) * sizeof(AdaptTile));
+        p.chunk_start = take((static_cast<size_t>(adapters) + 1) * sizeof(int32_t));
+        p.sums_r = take(rows * p.splits_r);
+        p.v_c = take(static_cast<size_t>(p.stride) * p.width * sizeof(float));
+        p.v_r = take(static_cast<size_t>(p.stride) * p.width * sizeof(float));
+        p.down = take(cut * C);
+        p.up = take(cut * R);
+    }
+    p.end = at;
+    return p;
+}
+
+void group(const Plan &p, int32_t n, int32_t adapters, const void *ids, int32_t id_dtype,
+           char *ws, bool grad, hipStream_t s) {
+    const int32_t steps = std::max(1, (n + kGroupThreads - 1) / kGroupThreads);
+    const int32_t per = (steps + kGroupBlocks - 1) / kGroupBlocks;
+    GroupArgs g{ids, n, adapters, per * kGroupThreads, p.chunk,
+                reinterpret_cast<int32_t *>(ws + p.order),
+                reinterpret_cast<AdaptTile *>(ws + p.tile_list),
+                grad ? reinterpret_cast<AdaptTile *>(ws + p.chunk_list) : nullptr, p.tiles,
+                p.chunks, reinterpret_cast<int32_t *>(ws + p.chunk_start)};
+    const unsigned grid = static_cast<unsigned>((steps + per - 1) / per);
+    if (id_dtype == SPMV_INT32)
+        k_adapt_group<int32_t><<<grid, kGroupThreads, 0, s>>>(g);
+    else
+        k_adapt_group<int64_t><<<grid, kGroupThreads, 0, s>>>(g);
+}
+
+}  // namespace
+
+size_t adapt_bytes(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R) {
+    return n == 0 ? 0 : plan(n, adapters, rank, C, R, false).end;
+}
+
+spmv_status adapt(const AdaptArgs &a, hipStream_t s) {
+    const Plan p = plan(a.n, a.adapters, a.rank, a.C, a.R, false);
+    char *ws = static_cast<char *>(a.workspace);
+    group(p, a.n, a.adapters, a.ids, a.id_dtype, ws, false, s);
+    const int32_t *order = reinterpret_cast<int32_t *>(ws + p.order);
+    const AdaptTile *tiles = reinterpret_cast<AdaptTile *>(ws + p.tile_list);
+    float *sums = reinterpret_cast<float *>(ws + p.sums_c);
+    const int32_t columns = expand_columns(a.rank);
+    with_float(a.dtype, [&](auto x) {
+        using A = Adapt<decltype(x)>;
+        if (a.adapters > 0)
+            A::shrink({a.x, a.x_ld, a.down, a.C, a.rank, a.adapters, p.width, p.splits_c, p.part_c,
+                       order, tiles, a.n, sums},
+                      false, p.tiles, s);
+        A::expand({sums, p.splits_c, p.width, a.n, a.scales, a.up, a.R, a.rank, a.adapters, order,
+                   tiles, a.base, a.base_ld, a.out, a.out_ld, (a.R - 1) / columns + 1},
+                  false, a.out_dtype == SPMV_FP32, p.tiles, s);
+    });
+    SPMV_HIP(hipGetLastError());
+    return SPMV_OK;
+}
+
+size_t adapt_grad_bytes(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R) {
+    return plan(n, adapters, rank, C, R, true).end;
+}
+
+spmv_status adapt_grad(const AdaptGradArgs &a, hipStream_t s) {
+    const Plan p = plan(a.n, a.adapters, a.rank, a.C, a.R, true);
+    char *ws = static_cast<char *>(a.workspace);
+    auto floats = [&](size_t at) { return reinterpret_cast<float *>(ws + at); };
+    const int32_t *order = reinterpret_cast<int32_t *>(ws + p.order);
+    const AdaptTile *tiles = reinterpret_cast<AdaptTile *>(ws + p.tile_list);
+    const AdaptTile *chunks = reinterpret_cast<AdaptTile *>(ws + p.chunk_list);
+    int32_t *chunk_start = reinterpret_cast<int32_t *>(ws + p.chunk_start);
+    const bool weights = (a.ddown || a.dup) && a.adapters > 0;
+    group(p, a.n, a.adapters, a.ids, a.id_dtype, ws, true, s);
+    with_float(a.dtype, [&](auto x) {
+        using A = Adapt<decltype(x)>;
+        const bool any = a.adapters > 0 && a.n > 0;
+        if (any && weights)
+            A::shrink({a.x, a.x_ld, a.down, a.C, a.rank, a.adapters, p.width, p.splits_c, p.part_c,
+                       order, tiles, a.n, floats(p.sums_c)},
+                      false, p.tiles, s);
+        if (any)
+            A::shrink({a.grad, a.grad_ld, a.up, a.R, a.rank, a.adapters, p.width, p.splits_r,
+                       p.part_r, order, tiles, a.n, floats(p.sums_r)},
+                      true, p.tiles, s);
+        if (a.dx && a.n > 0 && a.C > 0)
+            A::expand({floats(p.sums_r), p.splits_r, p.width, a.n, a.scales, a.down, a.C, a.rank,
+                       a.adapters, order, tiles, a.base, a.base_ld, a.dx, a.dx_ld,
+                       (a.C - 1) / expand_columns(a.rank) + 1},
+                      true, false, p.tiles, s);
+        if (!any || !weights) return;
+        const FinishArgs h{floats(p.sums_c), p.splits_c, p.width, a.n, a.rank, a.adapters,
+                           a.scales, tiles, floats(p.v_c), p.stride};
+        const FinishArgs g{floats(p.sums_r), p.splits_r, p.width, a.n, a.rank, a.adapters,
+                           a.scales, tiles, floats(p.v_r), p.stride};
+        k_adapt_finish<<<dim3(static_cast<unsigned>(p.tiles), 2), kAdaptThreads, 0, s>>>(h, g);
+        if (a.ddown && a.C > 0)
+            A::weights({a.x, a.x_ld, floats(p.v_r), p.stride, a.C, a.rank, a.adapters, p.width,
+                        order, chunks, floats(p.down), (a.C - 1) / kWeightColumns + 1},
+                       false, p.chunks, s);
+        if (a.dup && a.R > 0)
+            A::weights({a.grad, a.grad_ld, floats(p.v_c), p.stride, a.R, a.rank, a.adapters,
+                        p.width, order, chunks, floats(p.up), (a.R - 1) / kWeightColumns + 1},
+                       true, p.chunks, s);
+    });
+    if (weights) {
+        const JoinArgs j{floats(p.down), floats(p.up), chunk_start,
+                         a.ddown ? static_cast<int64_t>(a.rank) * a.C : 0,
+                         a.dup ? static_cast<int64_t>(a.rank) * a.R : 0, a.ddown, a.dup,
+                         a.accumulate};
+        const int64_t size = std::max(j.down_size, j.up_size);
+        const dim3 grid(groups_for(std::min<int64_t>(size, 1 << 24), kAdaptThreads * 4),
+                        static_cast<unsigned>(a.adapters), 2);
+        with_float(a.w_dtype, [&](auto w) {
+            k_adapt_join<decltype(w)><<<grid, kAdaptThreads, 0, s>>>(j);
+        });
+    }
+    SPMV_HIP(hipGetLastError());
+    return SPMV_OK;
+}
+
+}  // namespace spmv

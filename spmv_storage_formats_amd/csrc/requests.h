@@ -52,4 +52,53 @@ struct LogprobsGradArgs {
 };
 spmv_status logprobs_grad(const LogprobsGradArgs &a, hipStream_t s);
 
+// adapt.hip
+// Ranks, adapters (keys of the sort, counted in LDS), columns and rows, at most
+// (blocks and tiles that one launch counts).
+constexpr int32_t kMostRank = 256;
+constexpr int32_t kMostAdapters = 2048;
+constexpr int32_t kMostColumns = 1 << 23;
+constexpr int32_t kMostAdaptRows = 1 << 24;
+
+struct AdaptArgs {
+    int32_t n, adapters, rank, C, R;  // rows, adapters, their rank, columns of x and of out
+    const void *x;                    // [n, C]
+    int64_t x_ld;
+    int32_t dtype;                    // of x, down, up, grad
+    const void *down, *up;            // [adapters, rank, C], [adapters, R, rank]
+    const float *scales;              // [adapters], null: ones
+    const void *ids;
+    int32_t id_dtype;
+    const void *base;                 // [n, R] of out_dtype, null: zeros
+    int64_t base_ld;
+    void *out;
+    int64_t out_ld;
+    int32_t out_dtype;
+    void *workspace;
+};
+size_t adapt_bytes(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R);
+spmv_status adapt(const AdaptArgs &a, hipStream_t s);
+
+struct AdaptGradArgs {
+    int32_t n, adapters, rank, C, R;
+    const void *grad;                 // [n, R]
+    int64_t grad_ld;
+    const void *x;                    // [n, C]
+    int64_t x_ld;
+    int32_t dtype;
+    const void *down, *up;
+    const float *scales;
+    const void *ids;
+    int32_t id_dtype;
+    const void *base;                 // [n, C] of dtype, null: zeros
+    int64_t base_ld;
+    void *dx;                         // [n, C] of dtype, null: not wanted
+    int64_t dx_ld;
+    void *ddown, *dup;                // as down and up, of w_dtype, null: not wanted
+    int32_t w_dtype, accumulate;
+    void *workspace;
+};
+size_t adapt_grad_bytes(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R);
+spmv_status adapt_grad(const AdaptGradArgs &a, hipStream_t s);
+
 }  // namespace spmv

@@ -9,6 +9,15 @@ namespace {
 
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+// Sizes of an adapter call: invalid, too large, or fine.
+spmv_status adapt_sizes(int32_t adapters, int32_t rank, int32_t C, int32_t R, int64_t n) {
+    if (adapters < 0 || rank < 1 || C < 0 || R < 0 || n < 0) return SPMV_ERR_INVALID_ARG;
+    if (adapters > kMostAdapters || rank > kMostRank || C > kMostColumns || R > kMostColumns ||
+        n > kMostAdaptRows)
+        return SPMV_ERR_TOO_LARGE;
+    return SPMV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -58,6 +67,74 @@ spmv_status spmv_token_logprobs_grad(int32_t V, int64_t n, const void *logits, i
     return logprobs_grad({V, n, logits, ld, dtype, ids, id_dtype, scale, stats, grad_logprobs,
                           entropy, grad_entropy, out, out_ld, out_dtype},
                          static_cast<hipStream_t>(stream));
+}
+
+spmv_status spmv_adapt_workspace(int32_t adapters, int32_t rank, int32_t C, int32_t R, int64_t n,
+                                 size_t *bytes) {
+    if (!bytes) return SPMV_ERR_INVALID_ARG;
+    SPMV_TRY(adapt_sizes(adapters, rank, C, R, n));
+    *bytes = R == 0 ? 0 : adapt_bytes(static_cast<int32_t>(n), adapters, rank, C, R);
+    return SPMV_OK;
+}
+
+spmv_status spmv_adapt(int32_t adapters, int32_t rank, int32_t C, int32_t R, int64_t n,
+                       const void *x, int64_t x_ld, spmv_dtype dtype, const void *down,
+                       const void *up, const float *scales, const void *ids, spmv_dtype id_dtype,
+                       const void *base, int64_t base_ld, void *out, int64_t out_ld,
+                       spmv_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                       void *stream) {
+    if (!float_dtype(dtype) || !id_dtype_ok(id_dtype) ||
+        (out_dtype != dtype && out_dtype != SPMV_FP32))
+        return SPMV_ERR_INVALID_ARG;
+    SPMV_TRY(adapt_sizes(adapters, rank, C, R, n));
+    if (n == 0 || R == 0) return SPMV_OK;
+    if ((C > 0 && !x) || (adapters > 0 && ((C > 0 && !down) || !up)) || !ids || !out ||
+        (n > 1 && (x_ld < C || out_ld < R || (base && base_ld < R))) ||
+        (base == out && n > 1 && base_ld != out_ld))
+        return SPMV_ERR_INVALID_ARG;
+    const int32_t rows = static_cast<int32_t>(n);
+    if (!workspace || workspace_bytes < adapt_bytes(rows, adapters, rank, C, R) ||
+        !aligned(workspace, 16))
+        return SPMV_ERR_INVALID_ARG;
+    return adapt({rows, adapters, rank, C, R, x, x_ld, dtype, down, up, scales, ids, id_dtype,
+                  base, base_ld, out, out_ld, out_dtype, workspace},
+                 static_cast<hipStream_t>(stream));
+}
+
+spmv_status spmv_adapt_grad_workspace(int32_t adapters, int32_t rank, int32_t C, int32_t R,
+                                      int64_t n, size_t *bytes) {
+    if (!bytes) return SPMV_ERR_INVALID_ARG;
+    SPMV_TRY(adapt_sizes(adapters, rank, C, R, n));
+    *bytes = adapt_grad_bytes(static_cast<int32_t>(n), adapters, rank, C, R);
+    return SPMV_OK;
+}
+
+spmv_status spmv_adapt_grad(int32_t adapters, int32_t rank, int32_t C, int32_t R, int64_t n,
+                            const void *grad, int64_t grad_ld, const void *x, int64_t x_ld,
+                            spmv_dtype dtype, const void *down, const void *up,
+                            const float *scales, const void *ids, spmv_dtype id_dtype,
+                            const void *base, int64_t base_ld, void *dx, int64_t dx_ld,
+                            void *ddown, void *dup, spmv_dtype w_dtype, int32_t accumulate,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+    if (!float_dtype(dtype) || !id_dtype_ok(id_dtype) ||
+        (w_dtype != dtype && w_dtype != SPMV_FP32))
+        return SPMV_ERR_INVALID_ARG;
+    SPMV_TRY(adapt_sizes(adapters, rank, C, R, n));
+    if ((!dx && !ddown && !dup) || (n == 0 && adapters == 0)) return SPMV_OK;
+    if (n > 0 && ((R > 0 && !grad) || (C > 0 && !x) || !ids ||
+                  (adapters > 0 && ((C > 0 && !down) || (R > 0 && !up)))))
+        return SPMV_ERR_INVALID_ARG;
+    if (n > 1 && (grad_ld < R || x_ld < C || (dx && dx_ld < C) || (dx && base && base_ld < C) ||
+                  (dx && base == dx && base_ld != dx_ld)))
+        return SPMV_ERR_INVALID_ARG;
+    const int32_t rows = static_cast<int32_t>(n);
+    if (!workspace || workspace_bytes < adapt_grad_bytes(rows, adapters, rank, C, R) ||
+        !aligned(workspace, 16))
+        return SPMV_ERR_INVALID_ARG;
+    return adapt_grad({rows, adapters, rank, C, R, grad, grad_ld, x, x_ld, dtype, down, up,
+                       scales, ids, id_dtype, base, base_ld, dx, dx_ld, ddown, dup, w_dtype,
+                       accumulate != 0, workspace},
+                      static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

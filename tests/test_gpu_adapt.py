@@ -1,0 +1,489 @@
+"""Low-rank adapters of many requests and their gradients on the GPU, against plain
+implementations in 64 bits.
+
+- exact: small whole numbers and factors of powers of two.  Every product and partial sum is a
+  whole number (times one power of two) below 2^24, and below 2^16 between two products, so
+  the fp32 sums are exact in any order and the result is the exact one, rounded once.
+- random values: within the bounds of `Want`."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import spmv_storage_formats_amd as spmv  # noqa: E402
+
+F = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
+U = 2.0 ** -24
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    spmv.load_library()
+    return torch.device("cuda:0")
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+class Case:
+    """Random operands: `exact` ones are small whole numbers."""
+
+    def __init__(self, n, L, rank, C, R, dtype, seed, order="shuffled", exact=False, pad=0.15,
+                 ids="int64", scales=True):
+        rng = np.random.default_rng(seed)
+        of = rng.integers(0, max(L, 1), n)
+        if order == "runs":
+            of = np.sort(of)[::-1].copy()
+        elif order == "one":
+            of[:] = L - 1
+        of[rng.random(n) < pad] = rng.choice([-1, L, 2**31 - 1, -2**31])
+        if L == 0:
+            of[:] = -1
+        if exact:
+            draw = lambda *s: rng.integers(-2, 3, s).astype(np.float64)
+            self.scales = torch.from_numpy(2.0 ** rng.integers(-1, 2, L)).float()
+        else:
+            draw = lambda *s: rng.normal(0, 1, s)
+            self.scales = torch.from_numpy(rng.uniform(-1.5, 1.5, L)).float()
+        to = F[dtype]
+        by = 1.0 if exact else max(C, 1) ** -0.5
+        self.x = torch.from_numpy(draw(n, C)).to(to)
+        self.down = torch.from_numpy(draw(L, rank, C) * by).to(to)
+        self.up = torch.from_numpy(draw(L, R, rank)).to(to)
+        if exact:   # between two products numbers stay below 2^16
+            self.x[torch.from_numpy(rng.random((n, C)) < 0.5)] = 0
+        self.grad = torch.from_numpy(draw(n, R)).to(to)
+        self.base = torch.from_numpy(draw(n, R))
+        self.back = torch.from_numpy(draw(n, C)).to(to)
+        self.ids = torch.from_numpy(of).to(torch.int64 if ids == "int64" else torch.int32)
+        self.of, self.L, self.dtype = of, L, to
+        if not scales:
+            self.scales = None
+
+    def to(self, dev):
+        for k, v in list(vars(self).items()):
+            if isinstance(v, torch.Tensor):
+                setattr(self, k, v.to(dev))
+        return self
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+class Want:
+    """The definition in 64 bits, adapter by adapter, and the bounds of fp32 results: a sum of m
+    exact products is off by at most 2 (m + 64) U of the sum of their magnitudes (each of its
+    additions, and those that join splits, waves and chunks, rounds or truncates by at most 2 U
+    of a partial sum; fp32 products round once more, within the factor 2); a number between two
+    products carries its own bound into the next and, where 16 of its bits enter a bf16 result,
+    2^-16 of itself; factors and the base round once; the result rounds to its type."""
+
+    def __init__(self, c, out, w_out):
+        x, down, up, grad = (f64(t) for t in (c.x, c.down, c.up, c.grad))
+        n, C = x.shape
+        L, R, rank = up.shape
+        s = np.ones(L) if c.scales is None else f64(c.scales)
+        lost = 2.0 ** -16 if c.dtype == torch.bfloat16 else 0.0
+        lost_out = lost if out == torch.bfloat16 else 0.0
+        self.y, self.y_tol = np.zeros((n, R)), np.zeros((n, R))
+        self.dx, self.dx_tol = np.zeros((n, C)), np.zeros((n, C))
+        self.ddown, self.dup = np.zeros(down.shape), np.zeros(up.shape)
+        self.ddown_tol, self.dup_tol = np.zeros(down.shape), np.zeros(up.shape)
+        e = lambda m: 2 * (m + 64) * U
+        for a in range(L):
+            t = np.flatnonzero(c.of == a)
+            if not len(t):
+                continue
+            xa, ga, D, B = x[t], grad[t], down[a], up[a]
+            h, hm = xa @ D.T * s[a], np.abs(xa) @ np.abs(D).T * abs(s[a])
+            g, gm = ga @ B * s[a], np.abs(ga) @ np.abs(B) * abs(s[a])
+            he, ge = (e(C) + U) * hm, (e(R) + U) * gm
+            self.y[t] = h @ B.T
+            self.y_tol[t] = (he + (lost_out + e(3 * rank)) * np.abs(h) + he * e(rank)) @ np.abs(B).T
+            self.dx[t] = g @ D
+            self.dx_tol[t] = (ge + (lost + e(3 * rank)) * np.abs(g) + ge * e(rank)) @ np.abs(D)
+            m = 3 * len(t)
+            self.ddown[a] = g.T @ xa
+            self.ddown_tol[a] = (ge + e(m) * np.abs(g)).T @ np.abs(xa)
+            self.dup[a] = ga.T @ h
+            self.dup_tol[a] = np.abs(ga).T @ (he + e(m) * np.abs(h))
+        for k, t in (("y", out), ("dx", c.dtype), ("ddown", w_out), ("dup", w_out)):
+            v = getattr(self, k)
+            tol = getattr(self, k + "_tol")
+            tol += half_step(t) * (np.abs(v) + tol) + torch.finfo(t).eps * torch.finfo(t).tiny
+
+    def with_base(self, base, which, dtype):
+        v, tol = getattr(self, which) + f64(base), getattr(self, which + "_tol")
+        return v, tol + (2 * U + half_step(dtype)) * (np.abs(v) + np.abs(f64(base)))
+
+
+def close(got, want, tol, what):
+    off = np.abs(f64(got) - want)
+    ratio = off / np.maximum(tol, 1e-300)
+    ratio[off == 0] = 0
+    assert np.all(ratio <= 1), (what, ratio.max(), np.unravel_index(ratio.argmax(), ratio.shape))
+
+
+def rounded(v, dtype):
+    return torch.from_numpy(v).to(dtype).double().numpy()
+
+
+SHAPES = [  # n, L, rank, C, R, order
+    (1, 1, 1, 1, 1, "one"), (1, 3, 4, 33, 7, "one"), (2, 1, 16, 130, 129, "one"),
+    (15, 4, 8, 257, 100, "shuffled"), (17, 2, 17, 96, 513, "shuffled"),
+    (64, 64, 16, 512, 520, "shuffled"), (65, 1, 20, 1000, 65, "one"),
+    (130, 5, 33, 300, 700, "runs"), (200, 3, 64, 129, 1030, "runs"),
+    (77, 2, 100, 200, 300, "shuffled"), (40, 3, 256, 64, 90, "runs"),
+    (700, 7, 12, 40, 50, "shuffled"), (2100, 9, 3, 24, 31, "shuffled"),
+    (1500, 300, 2, 16, 9, "shuffled")]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+def test_exact(dev, shape, dtype):
+    c = Case(*shape[:5], dtype, sum(shape[:5]), shape[5], exact=True,
+             ids="int32" if shape[0] % 2 else "int64").to(dev)
+    w = Want(c, torch.float32, torch.float32)
+    got = spmv.adapt(c.x, c.down, c.up, c.ids, scales=c.scales, dtype=torch.float32)
+    assert np.array_equal(f64(got), w.y)
+    for to in (F[dtype], torch.float32):
+        base = c.base.to(to)
+        got = spmv.adapt(c.x, c.down, c.up, c.ids, base, scales=c.scales)
+        assert got.dtype == to and np.array_equal(f64(got), rounded(w.y + f64(base), to))
+    dx, dd, du = spmv.adapt_grad(c.grad, c.x, c.down, c.up, c.ids, scales=c.scales,
+                                 dtype=torch.float32)
+    assert np.array_equal(f64(dx), rounded(w.dx, F[dtype]))
+    assert np.array_equal(f64(dd), w.ddown) and np.array_equal(f64(du), w.dup)
+    # added to what is there; types of their own; a base for dx, in place
+    more = [torch.ones_like(c.down), torch.ones_like(c.up)]
+    b = c.back.clone()
+    dx, *_ = spmv.adapt_grad(c.grad, c.x, c.down, c.up, c.ids, b, b, *more, scales=c.scales,
+                             accumulate=True)
+    assert dx is b and np.array_equal(f64(b), rounded(w.dx + f64(c.back), F[dtype]))
+    assert np.array_equal(f64(more[0]), rounded(w.ddown + 1, F[dtype]))
+    assert np.array_equal(f64(more[1]), rounded(w.dup + 1, F[dtype]))
+
+
+@pytest.mark.parametrize("shape", SHAPES + [(32, 64, 16, 4096, 4096, "shuffled"),
+                                            (1030, 3, 16, 2750, 1100, "runs"),
+                                            (300, 2, 64, 1024, 2050, "one")])
+@pytest.mark.parametrize("dtype,out", [("fp32", "fp32"), ("fp16", "fp16"), ("bf16", "bf16"),
+                                       ("fp16", "fp32"), ("bf16", "fp32")])
+def test_random(dev, shape, dtype, out):
+    c = Case(*shape[:5], dtype, sum(shape[:5]) + 1, shape[5]).to(dev)
+    w = Want(c, F[out], F[out])
+    close(spmv.adapt(c.x, c.down, c.up, c.ids, scales=c.scales, dtype=F[out]), w.y, w.y_tol, "y")
+    base = c.base.to(F[out])
+    close(spmv.adapt(c.x, c.down, c.up, c.ids, base, scales=c.scales),
+          *w.with_base(base, "y", F[out]), "y with base")
+    dx, dd, du = spmv.adapt_grad(c.grad, c.x, c.down, c.up, c.ids, scales=c.scales, dtype=F[out])
+    close(dx, w.dx, w.dx_tol, "dx")
+    close(dd, w.ddown, w.ddown_tol, "ddown")
+    close(du, w.dup, w.dup_tol, "dup")
+    dx, dd, du = spmv.adapt_grad(c.grad, c.x, c.down, c.up, c.ids, c.back, False, None, False,
+                                 scales=c.scales)
+    assert dx is None and du is None
+    # rounded to the operands' type; below its smallest normal number by half a step of that,
+    # eps * tiny / 2 (fp16: 2^-25), as in `Want`
+    own = torch.finfo(F[dtype])
+    close(dd, w.ddown, w.ddown_tol + own.eps / 2 * (np.abs(w.ddown) + w.ddown_tol)
+          + own.eps * own.tiny, "ddown alone")
+    dx, dd, du = spmv.adapt_grad(c.grad, c.x, c.down, c.up, c.ids, c.back, None, False, False,
+                                 scales=c.scales)
+    assert dd is None and du is None
+    close(dx, *w.with_base(c.back, "dx", F[dtype]), "dx alone")
+
+
+def test_without_scales_and_results_repeat(dev):
+    c = Case(900, 4, 16, 600, 800, "bf16", 5, scales=False).to(dev)
+    w = Want(c, torch.bfloat16, torch.bfloat16)
+    y = spmv.adapt(c.x, c.down, c.up, c.ids)
+    g = spmv.adapt_grad(c.grad, c.x, c.down, c.up, c.ids)
+    close(y, w.y, w.y_tol, "y")
+    close(g[1], w.ddown, w.ddown_tol, "ddown")
+    for _ in range(3):
+        assert torch.equal(spmv.adapt(c.x, c.down, c.up, c.ids), y)
+        again = spmv.adapt_grad(c.grad, c.x, c.down, c.up, c.ids)
+        assert all(torch.equal(p, q) for p, q in zip(again, g))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+def test_strides_and_rows_beside(dev, dtype):
+    """Rows at any stride and offset; what lies beside and behind them stays."""
+    c = Case(70, 3, 9, 37, 61, dtype, 8, exact=True).to(dev)
+    w = Want(c, torch.float32, torch.float32)
+
+    def inside(t, left, right):
+        buf = torch.full((t.shape[0] + 3, t.shape[1] + left + right), 9.0, dtype=t.dtype,
+                         device=dev)
+        view = buf[:t.shape[0], left:left + t.shape[1]]
+        view.copy_(t)
+        return buf, view
+
+    def untouched(buf, view, left):
+        n, D = view.shape
+        rest = buf.clone()
+        rest[:n, left:left + D] = 9
+        return (rest == 9).all()
+
+    x, grad = inside(c.x, 3, 2)[1], inside(c.grad, 1, 6)[1]
+    ob, out = inside(c.base.to(F[dtype]), 5, 1)
+    want = rounded(w.y + f64(out), F[dtype])
+    got = spmv.adapt(x, c.down, c.up, c.ids, out, out, scales=c.scales)
+    assert got is out and np.array_equal(f64(out), want) and untouched(ob, out, 5)
+    db, dx = inside(c.back, 1, 1)
+    got = spmv.adapt_grad(grad, x, c.down, c.up, c.ids, c.back, dx, scales=c.scales,
+                          dtype=torch.float32)
+    assert got[0] is dx and np.array_equal(f64(dx), rounded(w.dx + f64(c.back), F[dtype]))
+    assert untouched(db, dx, 1)
+    assert np.array_equal(f64(got[1]), w.ddown) and np.array_equal(f64(got[2]), w.dup)
+    # as a batch has them
+    y = spmv.adapt(c.x.view(7, 10, 37), c.down, c.up, c.ids.view(7, 10), scales=c.scales,
+                   dtype=torch.float32)
+    assert y.shape == (7, 10, 61) and np.array_equal(f64(y).reshape(70, 61), w.y)
+    got = spmv.adapt_grad(c.grad.view(7, 10, 61), c.x.view(7, 10, 37), c.down, c.up,
+                          c.ids.view(7, 10), scales=c.scales)
+    assert got[0].shape == (7, 10, 37)
+    assert np.array_equal(f64(got[0]).reshape(70, 37), rounded(w.dx, F[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_not_finite_rows_stay_alone(dev, dtype, bad):
+    """NaN and infinities in a row reach its own results only; rows without an adapter hand
+    their base on, whatever x holds there, and adapters that no row names may hold anything."""
+    c = Case(90, 4, 10, 50, 45, dtype, 3, exact=True, pad=0.0).to(dev)
+    c.of[:] = np.arange(90) % 3
+    c.of[5], c.of[6] = -1, 4
+    c.ids.copy_(torch.from_numpy(c.of))
+    c.down[3], c.up[3] = bad, bad
+    w = Want(c, torch.float32, torch.float32)
+    c.x[7, 11] = c.x[5, 0] = bad
+    c.grad[8, 44] = c.grad[6, 3] = bad
+    base = c.base.to(F[dtype])
+    base[5, 2] = bad
+    y = spmv.adapt(c.x, c.down, c.up, c.ids, base, scales=c.scales)
+    rest = np.arange(90) != 7
+    assert not y[7].isfinite().any()
+    want = rounded(w.y + np.nan_to_num(f64(base), nan=0, posinf=0), F[dtype])
+    want[5, 2] = bad
+    assert np.array_equal(f64(y)[rest], want[rest], equal_nan=True)
+    dx, dd, du = spmv.adapt_grad(c.grad, c.x, c.down, c.up, c.ids, scales=c.scales,
+                                 dtype=torch.float32)
+    assert not dx[8].isfinite().any()
+    rest = np.arange(90) != 8
+    assert np.array_equal(f64(dx)[rest], rounded(w.dx, F[dtype])[rest])
+    sound = [0, 3]          # of rows 7 and 8 the adapters are 1 and 2
+    assert np.array_equal(f64(dd)[sound], w.ddown[sound])
+    assert np.array_equal(f64(du)[sound], w.dup[sound])
+    assert not dd[1].isfinite().all() and not du[2].isfinite().all()
+
+
+def test_large_and_small_numbers(dev):
+    """Numbers between two products beyond fp16's range, and small ones, keep their bits."""
+    for dtype, big in (("fp16", 3e4), ("bf16", 1e30), ("fp32", 1e30)):
+        x = torch.full((3, 64), big, dtype=F[dtype], device=dev)
+        down = torch.ones(1, 2, 64, dtype=F[dtype], device=dev)
+        down[0, 1] = 2.0 ** -10
+        up = torch.full((1, 5, 2), 2.0 ** -12, dtype=F[dtype], device=dev)
+        ids = torch.zeros(3, dtype=torch.int64, device=dev)
+        y = spmv.adapt(x, down, up, ids, dtype=torch.float32)
+        v = float(x[0, 0]) * 64 * (1 + 2.0 ** -10) * 2.0 ** -12
+        assert (y.double().cpu() / v - 1).abs().max() <= 1e-6
+        y = spmv.adapt(x * 0 + 2.0 ** -14, down, up, ids, dtype=torch.float32)
+        v = 2.0 ** -14 * 64 * (1 + 2.0 ** -10) * 2.0 ** -12
+        assert (y.double().cpu() / v - 1).abs().max() <= 1e-6
+
+
+def test_empty_and_none(dev):
+    for dtype in F.values():
+        x = torch.ones(5, 12, dtype=dtype, device=dev)
+        ids = torch.zeros(5, dtype=torch.int32, device=dev)
+        down, up = (torch.ones(2, *s, dtype=dtype, device=dev) for s in ((3, 12), (7, 3)))
+        # no adapters at all; no rows; no columns
+        y = spmv.adapt(x, down[:0], up[:0], ids)
+        assert (y == 0).all() and y.shape == (5, 7)
+        y = spmv.adapt(x[:0], down, up, ids[:0])
+        assert y.shape == (0, 7)
+        y = spmv.adapt(x[:, :0], down[..., :0].contiguous(), up, ids, torch.ones(
+            5, 7, dtype=dtype, device=dev))
+        assert (y == 1).all()
+        g = torch.ones(5, 7, dtype=dtype, device=dev)
+        dx, dd, du = spmv.adapt_grad(g, x, down[:0], up[:0], ids)
+        assert (dx == 0).all() and dd.shape == (0, 3, 12)
+        keep = [torch.ones_like(down), torch.ones_like(up)]
+        dx, dd, du = spmv.adapt_grad(g[:0], x[:0], down, up, ids[:0], None, None, *keep,
+                                     accumulate=True)
+        assert (keep[0] == 1).all() and (keep[1] == 1).all()
+        dx, dd, du = spmv.adapt_grad(g[:0], x[:0], down, up, ids[:0])
+        assert (dd == 0).all() and (du == 0).all()
+        # adapters without rows: zeros, or what was there (NaN among it)
+        keep = [torch.full_like(down, NAN), torch.full_like(up, NAN)]
+        keep[0][0], keep[1][0] = 0, 0
+        spmv.adapt_grad(g, x, down, up, ids, None, None, *keep, accumulate=True)
+        assert keep[0][1].isnan().all() and keep[1][1].isnan().all()
+        assert (keep[0][0] == 35).all() and (keep[1][0] == 60).all()
+        dx, dd, du = spmv.adapt_grad(g, x, down, up, ids)
+        assert (dd[1] == 0).all() and (du[1] == 0).all() and (dx == 21).all()
+
+
+def test_gradients_are_differences(dev):
+    """L = sum(r * adapt(x, down, up)) is linear in each operand: with whole numbers a step of 1
+    in one element changes L by exactly its gradient."""
+    c = Case(9, 2, 3, 5, 4, "fp32", 6, exact=True).to(dev)
+
+    def loss(x, down, up):
+        y = spmv.adapt(x, down, up, c.ids, scales=c.scales)
+        return (y.double() * c.grad.double()).sum().item()
+
+    args = [c.x, c.down, c.up]
+    grads = spmv.adapt_grad(c.grad, *args, c.ids, scales=c.scales)
+    at = loss(*args)
+    for k, (t, d) in enumerate(zip(args, grads)):
+        for i in range(t.numel()):
+            moved = list(args)
+            moved[k] = t.clone()
+            moved[k].view(-1)[i] += 1
+            assert loss(*moved) - at == d.view(-1)[i].item()
+
+
+def test_refusals(dev):
+    c = Case(6, 2, 4, 10, 12, "fp16", 1).to(dev)
+    ok = (c.x, c.down, c.up, c.ids)
+    y = spmv.adapt(*ok)
+    bad = [
+        (TypeError, lambda: spmv.adapt(c.x.float(), c.down, c.up, c.ids)),
+        (TypeError, lambda: spmv.adapt(c.x, c.down, c.up, c.ids.float())),
+        (TypeError, lambda: spmv.adapt(*ok, dtype=torch.bfloat16)),
+        (TypeError, lambda: spmv.adapt(*ok, scales=c.scales.half())),
+        (TypeError, lambda: spmv.adapt(*ok, y, dtype=torch.float32)),
+        (ValueError, lambda: spmv.adapt(c.x, c.down, c.up[:1], c.ids)),
+        (ValueError, lambda: spmv.adapt(c.x, c.down[:, :3].contiguous(), c.up, c.ids)),
+        (ValueError, lambda: spmv.adapt(c.x, c.down[:, ::2], c.up[..., ::2], c.ids)),
+        (ValueError, lambda: spmv.adapt(c.x[:, :9], c.down, c.up, c.ids)),
+        (ValueError, lambda: spmv.adapt(c.x, c.down, c.up, c.ids[:5])),
+        (ValueError, lambda: spmv.adapt(*ok, scales=c.scales[:1])),
+        (ValueError, lambda: spmv.adapt(*ok, y[:5])),
+        (ValueError, lambda: spmv.adapt(*ok, None, y.t().contiguous().t())),
+        (ValueError, lambda: spmv.adapt(*ok, workspace=torch.empty(
+            16, dtype=torch.uint8, device=dev))),
+        (TypeError, lambda: spmv.adapt_grad(c.grad.float(), *ok)),
+        (TypeError, lambda: spmv.adapt_grad(c.grad, *ok, dtype=torch.bfloat16)),
+        (ValueError, lambda: spmv.adapt_grad(c.grad[:5], *ok)),
+        (ValueError, lambda: spmv.adapt_grad(c.grad, *ok, accumulate=True)),
+        (ValueError, lambda: spmv.adapt_grad(c.grad, *ok, None, c.x)),
+        (ValueError, lambda: spmv.adapt_grad(c.grad, *ok, None, None, c.down)),
+        (TypeError, lambda: spmv.adapt_grad(c.grad, *ok, None, None, torch.zeros_like(c.down),
+                                            torch.zeros(c.up.shape, device=dev))),
+    ]
+    wide = torch.empty(7, 12, dtype=torch.float16, device=dev)
+    bad.append((ValueError, lambda: spmv.adapt(*ok, wide[1:], wide[:6])))
+    for error, call in bad:
+        with pytest.raises(error):
+            call()
+
+
+def test_streams_and_graphs(dev):
+    """Steps at once on streams of their own; captured ones replayed in turn on other inputs."""
+    cases = [Case(700, 5, 16, 300, 400, "bf16", 1).to(dev), Case(9, 7, 8, 900, 100, "bf16", 2
+                                                                ).to(dev)]
+
+    def step(c, **kw):
+        y = spmv.adapt(c.x, c.down, c.up, c.ids, scales=c.scales, **kw)
+        return [y, *spmv.adapt_grad(c.grad, c.x, c.down, c.up, c.ids, c.back, scales=c.scales,
+                                    **kw)]
+
+    want = [step(c) for c in cases]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        got = [step(cases[0], stream=a), step(cases[1], stream=b.cuda_stream)]
+        junk = torch.full((1 << 20,), 7.0, device=dev)
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(g, w))
+        del junk
+    graphs = []
+    for c in cases:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step(c)
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r = step(c)
+        graphs.append((g, c, r))
+    for turn in range(3):
+        for g, c, r in graphs:
+            o = Case(c.x.shape[0], c.L, c.down.shape[1], c.x.shape[1], c.up.shape[1], "bf16",
+                     50 + turn, order="runs" if turn == 1 else "shuffled").to(dev)
+            for k in ("x", "ids", "grad", "back", "up"):
+                getattr(c, k).copy_(getattr(o, k))
+            for t in r:
+                t.fill_(5)
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(r, step(c)))
+
+
+@pytest.mark.parametrize("n", [1025, 70_000, 200_000])
+def test_many_rows_sort(dev, n):
+    """The rows' sort over several workgroups, by counts that tell rows apart."""
+    rng = np.random.default_rng(n)
+    for L, kind in ((3, "runs"), (700, "mixed"), (2048, "mixed")):
+        of = rng.integers(-1, L, n)
+        if kind == "runs":
+            of = np.sort(of)
+        ids = torch.from_numpy(of).to(dev)
+        x = torch.from_numpy(rng.integers(-3, 4, (n, 8)).astype(np.float32)).to(dev)
+        down = torch.from_numpy(rng.integers(-3, 4, (L, 1, 8)).astype(np.float32)).to(dev)
+        up = torch.from_numpy(rng.integers(-3, 4, (L, 2, 1)).astype(np.float32)).to(dev)
+        y = spmv.adapt(x, down, up, ids)
+        at = ids.clamp(min=0)
+        h = torch.where(ids >= 0, (x * down[at, 0]).sum(1), 0.0)
+        assert torch.equal(y, h[:, None] * up[at, :, 0])
+        g = x[:, :2].contiguous()
+        dx, dd, du = spmv.adapt_grad(g, x, down, up, ids)
+        b = torch.where(ids >= 0, (g * up[at, :, 0]).sum(1), 0.0)
+        assert torch.equal(dx, b[:, None] * down[at, 0])
+        want = torch.zeros(L + 1, 8, dtype=torch.float64, device=dev)
+        slot = torch.where(ids >= 0, ids, L)
+        want.index_add_(0, slot, (b[:, None] * x).double())
+        assert torch.equal(dd[:, 0].double(), want[:L])
+        want = torch.zeros(L + 1, 2, dtype=torch.float64, device=dev)
+        want.index_add_(0, slot, (h[:, None] * g).double())
+        assert torch.equal(du[..., 0].double(), want[:L])
+
+
+def test_long_offsets(dev):
+    """Rows, tables of adapters and results past 2^31 and 2^32 elements."""
+    n, C, R = 560_000, 16, 8192
+    ids = torch.arange(n, device=dev) % 3 - 1
+    x = torch.ones(n, C, dtype=torch.bfloat16, device=dev)
+    down = torch.ones(2, 1, C, dtype=torch.bfloat16, device=dev)
+    up = torch.ones(2, R, 1, dtype=torch.bfloat16, device=dev)
+    up[1] = 2
+    y = spmv.adapt(x, down, up, ids)
+    want = torch.tensor([0.0, 16.0, 32.0], device=dev)
+    assert torch.equal(y[:, 0].float(), want[ids + 1]) and torch.equal(y[:, -1], y[:, 0])
+    assert torch.equal(y[-2000:].float(), want[ids[-2000:] + 1][:, None].expand(2000, R))
+    dx, dd, du = spmv.adapt_grad(y, x, down, up, ids, dtype=torch.float32)
+    t = int((ids == 1).sum())
+    assert (dx[ids == 0] == 16.0 * R).all() and (dx[ids == 1] == 64.0 * R).all()
+    assert (du[1] == 32.0 * 16 * t).all() and (dd[1] == 64.0 * R * t).all()
+    del y, dx
+    L, rank, C = 2048, 64, 36_000          # 4.7e9 elements
+    down = torch.zeros(L, rank, C, dtype=torch.bfloat16, device=dev)
+    down[L - 1] = 1
+    up = torch.ones(L, 3, rank, dtype=torch.bfloat16, device=dev)
+    x = torch.ones(2, C, dtype=torch.bfloat16, device=dev)
+    y = spmv.adapt(x, down, up, torch.tensor([L - 1, 0], device=dev), dtype=torch.float32)
+    assert (y[0] == 64.0 * C).all() and (y[1] == 0).all()

@@ -106,3 +106,90 @@ def test_binding_rejects_host_tensors():
                  lambda: spmv.token_logprobs(None, ids), lambda: spmv.token_logprobs([1.0], ids)):
         with pytest.raises(TypeError):
             call()
+
+
+# ------------------------------------------------------------------ adapters
+
+def adapt(lib, **change):
+    a = dict(L=3, rank=4, C=10, R=20, n=5, x=P, x_ld=10, dtype=BF16, down=P, up=P, sc=P, ids=P,
+             id=INT32, base=P, b_ld=20, out=ctypes.c_void_p(1 << 20), o_ld=20, to=BF16, ws=P,
+             size=1 << 24)
+    a.update(change)
+    return lib.spmv_adapt(a["L"], a["rank"], a["C"], a["R"], a["n"], a["x"], a["x_ld"],
+                          a["dtype"], a["down"], a["up"], a["sc"], a["ids"], a["id"], a["base"],
+                          a["b_ld"], a["out"], a["o_ld"], a["to"], a["ws"], a["size"], None)
+
+
+def adapt_grad(lib, **change):
+    a = dict(L=3, rank=4, C=10, R=20, n=5, g=P, g_ld=20, x=P, x_ld=10, dtype=BF16, down=P, up=P,
+             sc=P, ids=P, id=INT32, base=P, b_ld=10, dx=ctypes.c_void_p(1 << 20), d_ld=10,
+             dd=P, du=P, w=FP32, ws=P, size=1 << 24)
+    a.update(change)
+    return lib.spmv_adapt_grad(a["L"], a["rank"], a["C"], a["R"], a["n"], a["g"], a["g_ld"],
+                               a["x"], a["x_ld"], a["dtype"], a["down"], a["up"], a["sc"],
+                               a["ids"], a["id"], a["base"], a["b_ld"], a["dx"], a["d_ld"],
+                               a["dd"], a["du"], a["w"], 0, a["ws"], a["size"], None)
+
+
+SIZES = [({"L": -1}, INVALID), ({"rank": 0}, INVALID), ({"rank": -1}, INVALID),
+         ({"C": -1}, INVALID), ({"R": -1}, INVALID), ({"n": -1}, INVALID),
+         ({"L": 2049}, TOO_LARGE), ({"rank": 257}, TOO_LARGE), ({"C": 2**23 + 1}, TOO_LARGE),
+         ({"R": 2**23 + 1}, TOO_LARGE), ({"n": 2**24 + 1}, TOO_LARGE)]
+
+
+@pytest.mark.parametrize("change,status", SIZES + [
+    ({"dtype": INT32}, INVALID), ({"id": FP16}, INVALID), ({"to": FP16}, INVALID),
+    ({"x": None}, INVALID), ({"down": None}, INVALID), ({"up": None}, INVALID),
+    ({"ids": None}, INVALID), ({"out": None}, INVALID), ({"x_ld": 9}, INVALID),
+    ({"o_ld": 19}, INVALID), ({"b_ld": 19}, INVALID), ({"out": P, "o_ld": 21}, INVALID),
+    ({"ws": None}, INVALID), ({"ws": ctypes.c_void_p(4104)}, INVALID), ({"size": 100}, INVALID)])
+def test_adapt_refusals(lib, change, status):
+    assert adapt(lib, **change) == status
+
+
+@pytest.mark.parametrize("change,status", SIZES + [
+    ({"dtype": INT32}, INVALID), ({"id": FP16}, INVALID), ({"w": FP16}, INVALID),
+    ({"g": None}, INVALID), ({"x": None}, INVALID), ({"down": None}, INVALID),
+    ({"up": None}, INVALID), ({"ids": None}, INVALID), ({"g_ld": 19}, INVALID),
+    ({"x_ld": 9}, INVALID), ({"d_ld": 9}, INVALID), ({"b_ld": 9}, INVALID),
+    ({"dx": P, "d_ld": 11}, INVALID), ({"ws": None}, INVALID),
+    ({"ws": ctypes.c_void_p(4104)}, INVALID), ({"size": 100}, INVALID)])
+def test_adapt_grad_refusals(lib, change, status):
+    assert adapt_grad(lib, **change) == status
+
+
+def test_no_rows_to_adapt_is_no_error(lib):
+    assert adapt(lib, n=0, x=None, ids=None, out=None, ws=None) == 0
+    assert adapt(lib, R=0, out=None, up=None, ws=None, o_ld=0, b_ld=0) == 0
+    assert adapt_grad(lib, dx=None, dd=None, du=None, ws=None) == 0
+
+
+def test_adapt_workspaces(lib):
+    size = ctypes.c_size_t()
+    names = ("L", "rank", "C", "R", "n")
+    good = dict(L=3, rank=4, C=10, R=20, n=5)
+    for f in (lib.spmv_adapt_workspace, lib.spmv_adapt_grad_workspace):
+        assert f(3, 4, 10, 20, 5, None) == INVALID
+        for change, status in SIZES:
+            a = {**good, **change}
+            assert f(*(a[k] for k in names), ctypes.byref(size)) == status
+    for f in (spmv.adapt_workspace, spmv.adapt_grad_workspace):
+        sizes = [f(n, 8, 16, 4096, 4096) for n in (1, 100, 10_000, 1_000_000)]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+        for empty in ((0, 8, 16, 64, 64), (5, 0, 16, 64, 64), (5, 8, 16, 0, 64),
+                      (5, 8, 16, 64, 0), (0, 0, 1, 0, 0)):
+            assert f(*empty) >= 0
+        for k in range(5):
+            for wrap in (2**32 + 5, -2**32 + 8):
+                with pytest.raises(spmv.SpmvError):
+                    f(*(wrap if i == k else 8 for i in range(5)))
+
+
+def test_adapt_rejects_host_tensors():
+    torch = pytest.importorskip("torch")
+    x, ids = torch.zeros(3, 10), torch.zeros(3, dtype=torch.int64)
+    down, up = torch.zeros(2, 4, 10), torch.zeros(2, 6, 4)
+    for call in (lambda: spmv.adapt(x, down, up, ids), lambda: spmv.adapt(None, down, up, ids),
+                 lambda: spmv.adapt_grad(torch.zeros(3, 6), x, down, up, ids)):
+        with pytest.raises(TypeError):
+            call()
