@@ -15,6 +15,7 @@ struct GroupArgs {
     int32_t n, adapters;
     int32_t block;          // rows of a workgroup, a multiple of kGroupThreads
     int32_t chunk;          // rows of a chunk, at most
+    int32_t single;         // one chunk of every adapter, rows or not
     int32_t *order;
     AdaptTile *tiles, *chunks;      // chunks null: not wanted
     int32_t most_tiles, most_chunks;
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(kGroupThreads) void k_adapt_group(GroupArgs a) {
     __syncthreads();
     // rows without an adapter have no share in the matrices
     for (int k = tid; k < keys; k += kGroupThreads)
-        s_first[k] = k < a.adapters ? (s_count[k] + a.chunk - 1) / a.chunk : 0;
+        s_first[k] = k == a.adapters ? 0 : a.single ? 1 : (s_count[k] + a.chunk - 1) / a.chunk;
     prefix(s_first, keys, s_wsum);
     list(a.chunks, a.most_chunks, a.chunk);
     if (blockIdx.x == 0)
@@ -155,20 +156,41 @@ __global__ __launch_bounds__(kGroupThreads) void k_adapt_group(GroupArgs a) {
 }
 
 // Sums of the splits, scaled, rank by rank: what the matrices' gradients read.
+// A workgroup takes a tile and 16 ranks, a thread four of a row.
+template <bool kParts>
 __global__ __launch_bounds__(kAdaptThreads) void k_adapt_finish(FinishArgs a, FinishArgs b) {
     const FinishArgs &f = blockIdx.y == 0 ? a : b;
     const AdaptTile tile = f.tiles[blockIdx.x];
-    if (tile.adapter < 0 || tile.adapter >= f.adapters) return;
+    const int32_t row = static_cast<int32_t>(threadIdx.x) / 4;
+    if (tile.adapter < 0 || tile.adapter >= f.adapters || row >= tile.count) return;
+    const int32_t at = tile.first + row;
+    const int32_t k = static_cast<int32_t>(blockIdx.z) * 16 + static_cast<int32_t>(threadIdx.x) % 4 * 4;
     const float scale = f.scales ? f.scales[tile.adapter] : 1.f;
-    for (int i = threadIdx.x; i < tile.count * f.width; i += kAdaptThreads) {
-        const int32_t k = i % f.width, at = tile.first + i / f.width;
-        float v = 0.f;
-        if (k < f.rank) {
-            for (int32_t j = 0; j < f.splits; ++j)
-                v += f.sums[(static_cast<int64_t>(j) * f.n + at) * f.width + k];
-            v *= scale;
+    const float *p = f.sums + static_cast<int64_t>(f.order[at]) * f.width + k;
+    float v[4];
+    load_piece<4>(p, v);
+#pragma unroll 4
+    for (int32_t j = 1; j < f.splits; ++j) {
+        float more[4];
+        load_piece<4>(p + static_cast<int64_t>(j) * f.n * f.width, more);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += more[i];
+    }
+    const int64_t part = static_cast<int64_t>(f.stride) * f.width;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t to = static_cast<int64_t>(k + i) * f.stride + at;
+        float s = k + i < f.rank ? v[i] * scale : 0.f;
+        if constexpr (kParts) {
+            bf16 *out = static_cast<bf16 *>(f.out) + to;
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                out[q * part] = upper(s);
+                s = below(s);
+            }
+        } else {
+            static_cast<float *>(f.out)[to] = s;
         }
-        f.out[static_cast<int64_t>(k) * f.stride + at] = v;
     }
 }
 
@@ -223,6 +245,7 @@ size_t round16(size_t b) { return (b + 15) / 16 * 16; }
 
 // Sizes that follow from the arguments, and the workspace's parts.
 struct Plan {
+    bool single;  // no adapter has more than a chunk: no join
     int32_t width, tiles, chunk, chunks, stride;
     int32_t splits_c, part_c, splits_r, part_r;
     size_t order, tile_list, chunk_list, chunk_start, sums_c, sums_r, v_c, v_r, down, up, end;
@@ -244,8 +267,9 @@ Plan plan(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R, bool 
     // a last tile of each adapter that has rows, and of the rows without one
     p.tiles = (n + kAdaptTile - 1) / kAdaptTile + std::min(adapters + 1, n);
     p.chunk = std::max(kAdaptChunk, (n / 64 + 31) / 32 * 32);
-    p.chunks = (n + p.chunk - 1) / p.chunk + std::min(adapters, n);
-    p.stride = (n + 63) / 16 * 16;  // chunks are read past their last row, by 47 at most
+    p.single = n > 0 && n <= p.chunk;
+    p.chunks = p.single ? adapters : (n + p.chunk - 1) / p.chunk + std::min(adapters, n);
+    p.stride = (n + 7) / 8 * 8;
     split(C, p.tiles, &p.splits_c, &p.part_c);
     split(R, p.tiles, &p.splits_r, &p.part_r);
     size_t at = 0;
@@ -259,12 +283,14 @@ Plan plan(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R, bool 
     p.tile_list = take(static_cast<size_t>(p.tiles) * sizeof(AdaptTile));
     p.sums_c = take(rows * p.splits_c);
     if (grad) {
-        const size_t cut = static_cast<size_t>(p.chunks) * rank * sizeof(float);
+        const size_t cut = p.single ? 0 : static_cast<size_t>(p.chunks) * rank * sizeof(float);
+        // fp32, or three bf16 parts
+        const size_t v = static_cast<size_t>(p.stride) * p.width * 6;
         p.chunk_list = take(static_cast<size_t>(p.chunks) * sizeof(AdaptTile));
         p.chunk_start = take((static_cast<size_t>(adapters) + 1) * sizeof(int32_t));
         p.sums_r = take(rows * p.splits_r);
-        p.v_c = take(static_cast<size_t>(p.stride) * p.width * sizeof(float));
-        p.v_r = take(static_cast<size_t>(p.stride) * p.width * sizeof(float));
+        p.v_c = take(v);
+        p.v_r = take(v);
         p.down = take(cut * C);
         p.up = take(cut * R);
     }
@@ -276,7 +302,7 @@ void group(const Plan &p, int32_t n, int32_t adapters, const void *ids, int32_t 
            char *ws, bool grad, hipStream_t s) {
     const int32_t steps = std::max(1, (n + kGroupThreads - 1) / kGroupThreads);
     const int32_t per = (steps + kGroupBlocks - 1) / kGroupBlocks;
-    GroupArgs g{ids, n, adapters, per * kGroupThreads, p.chunk,
+    GroupArgs g{ids, n, adapters, per * kGroupThreads, p.chunk, p.single,
                 reinterpret_cast<int32_t *>(ws + p.order),
                 reinterpret_cast<AdaptTile *>(ws + p.tile_list),
                 grad ? reinterpret_cast<AdaptTile *>(ws + p.chunk_list) : nullptr, p.tiles,
@@ -294,23 +320,32 @@ size_t adapt_bytes(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t
     return n == 0 ? 0 : plan(n, adapters, rank, C, R, false).end;
 }
 
+// Columns of a workgroup of expand: all workgroups together about kGroups.
+int32_t expand_columns(int32_t D, int32_t tiles) {
+    constexpr int32_t kGroups = 2048, kUnit = kAdaptWaves * kExpandColumns;
+    const int32_t units = (D - 1) / kUnit + 1;
+    const int32_t want = std::min(units, std::max(1, kGroups / tiles));
+    return (units + want - 1) / want * kUnit;
+}
+
 spmv_status adapt(const AdaptArgs &a, hipStream_t s) {
     const Plan p = plan(a.n, a.adapters, a.rank, a.C, a.R, false);
     char *ws = static_cast<char *>(a.workspace);
-    group(p, a.n, a.adapters, a.ids, a.id_dtype, ws, false, s);
-    const int32_t *order = reinterpret_cast<int32_t *>(ws + p.order);
-    const AdaptTile *tiles = reinterpret_cast<AdaptTile *>(ws + p.tile_list);
+    const bool direct = a.n <= kAdaptDirect;
+    if (!direct) group(p, a.n, a.adapters, a.ids, a.id_dtype, ws, false, s);
+    const RowsArgs rows{a.ids, a.id_dtype, a.n, a.adapters,
+                        reinterpret_cast<int32_t *>(ws + p.order),
+                        direct ? nullptr : reinterpret_cast<AdaptTile *>(ws + p.tile_list)};
+    const int32_t tiles = direct ? a.n : p.tiles;
     float *sums = reinterpret_cast<float *>(ws + p.sums_c);
-    const int32_t columns = expand_columns(a.rank);
     with_float(a.dtype, [&](auto x) {
         using A = Adapt<decltype(x)>;
         if (a.adapters > 0)
-            A::shrink({a.x, a.x_ld, a.down, a.C, a.rank, a.adapters, p.width, p.splits_c, p.part_c,
-                       order, tiles, a.n, sums},
-                      false, p.tiles, s);
-        A::expand({sums, p.splits_c, p.width, a.n, a.scales, a.up, a.R, a.rank, a.adapters, order,
-                   tiles, a.base, a.base_ld, a.out, a.out_ld, (a.R - 1) / columns + 1},
-                  false, a.out_dtype == SPMV_FP32, p.tiles, s);
+            A::shrink({rows, a.x, a.x_ld, a.down, a.C, a.rank, p.width, p.splits_c, p.part_c, sums},
+                      tiles, s);
+        A::expand({rows, sums, p.splits_c, p.width, a.scales, a.up, a.R, a.rank, a.base, a.base_ld,
+                   a.out, a.out_ld, expand_columns(a.R, tiles)},
+                  false, a.out_dtype == SPMV_FP32, tiles, s);
     });
     SPMV_HIP(hipGetLastError());
     return SPMV_OK;
@@ -333,35 +368,39 @@ spmv_status adapt_grad(const AdaptGradArgs &a, hipStream_t s) {
     with_float(a.dtype, [&](auto x) {
         using A = Adapt<decltype(x)>;
         const bool any = a.adapters > 0 && a.n > 0;
-        if (any && weights)
-            A::shrink({a.x, a.x_ld, a.down, a.C, a.rank, a.adapters, p.width, p.splits_c, p.part_c,
-                       order, tiles, a.n, floats(p.sums_c)},
-                      false, p.tiles, s);
-        if (any)
-            A::shrink({a.grad, a.grad_ld, a.up, a.R, a.rank, a.adapters, p.width, p.splits_r,
-                       p.part_r, order, tiles, a.n, floats(p.sums_r)},
-                      true, p.tiles, s);
+        const RowsArgs rows{a.ids, a.id_dtype, a.n, a.adapters, order, tiles};
+        const ShrinkArgs h{rows, a.x, a.x_ld, a.down, a.C, a.rank, p.width, p.splits_c, p.part_c,
+                           floats(p.sums_c)};
+        const ShrinkArgs g{rows, a.grad, a.grad_ld, a.up, a.R, a.rank, p.width, p.splits_r,
+                           p.part_r, floats(p.sums_r)};
+        if (any) A::shrink_both(h, g, p.tiles, s);
         if (a.dx && a.n > 0 && a.C > 0)
-            A::expand({floats(p.sums_r), p.splits_r, p.width, a.n, a.scales, a.down, a.C, a.rank,
-                       a.adapters, order, tiles, a.base, a.base_ld, a.dx, a.dx_ld,
-                       (a.C - 1) / expand_columns(a.rank) + 1},
+            A::expand({rows, g.sums, g.splits, p.width, a.scales, a.down, a.C, a.rank, a.base,
+                       a.base_ld, a.dx, a.dx_ld, expand_columns(a.C, p.tiles)},
                       true, false, p.tiles, s);
         if (!any || !weights) return;
-        const FinishArgs h{floats(p.sums_c), p.splits_c, p.width, a.n, a.rank, a.adapters,
-                           a.scales, tiles, floats(p.v_c), p.stride};
-        const FinishArgs g{floats(p.sums_r), p.splits_r, p.width, a.n, a.rank, a.adapters,
-                           a.scales, tiles, floats(p.v_r), p.stride};
-        k_adapt_finish<<<dim3(static_cast<unsigned>(p.tiles), 2), kAdaptThreads, 0, s>>>(h, g);
-        if (a.ddown && a.C > 0)
-            A::weights({a.x, a.x_ld, floats(p.v_r), p.stride, a.C, a.rank, a.adapters, p.width,
-                        order, chunks, floats(p.down), (a.C - 1) / kWeightColumns + 1},
-                       false, p.chunks, s);
-        if (a.dup && a.R > 0)
-            A::weights({a.grad, a.grad_ld, floats(p.v_c), p.stride, a.R, a.rank, a.adapters,
-                        p.width, order, chunks, floats(p.up), (a.R - 1) / kWeightColumns + 1},
-                       true, p.chunks, s);
+        const FinishArgs fh{h.sums, h.splits, p.width, a.n, a.rank, a.adapters, a.scales, order,
+                            tiles, ws + p.v_c, p.stride};
+        const FinishArgs fg{g.sums, g.splits, p.width, a.n, a.rank, a.adapters, a.scales, order,
+                            tiles, ws + p.v_r, p.stride};
+        const dim3 grid(static_cast<unsigned>(p.tiles), 2, static_cast<unsigned>(p.width / 16));
+        if (a.dtype == SPMV_FP32)
+            k_adapt_finish<false><<<grid, kAdaptThreads, 0, s>>>(fh, fg);
+        else
+            k_adapt_finish<true><<<grid, kAdaptThreads, 0, s>>>(fh, fg);
+        auto sums = [&](const void *x, int64_t ld, const FinishArgs &f, int32_t D, size_t partial,
+                        void *out) {
+            return WeightArgs{x, ld, f.out, p.stride, D, a.rank, p.width, order, chunks,
+                              floats(partial), p.single ? out : nullptr, a.accumulate,
+                              a.w_dtype == SPMV_FP32,
+                              out && D > 0 ? (D - 1) / kWeightColumns + 1 : 0};
+        };
+        const WeightArgs down = sums(a.x, a.x_ld, fg, a.C, p.down, a.ddown);
+        const WeightArgs up = sums(a.grad, a.grad_ld, fh, a.R, p.up, a.dup);
+        if (down.blocks + up.blocks > 0) A::weights(down, up, a.adapters, p.chunks, s);
     });
-    if (weights) {
+    // no rows: nothing above wrote the gradients
+    if (weights && (!p.single || a.n == 0)) {
         const JoinArgs j{floats(p.down), floats(p.up), chunk_start,
                          a.ddown ? static_cast<int64_t>(a.rank) * a.C : 0,
                          a.dup ? static_cast<int64_t>(a.rank) * a.R : 0, a.ddown, a.dup,

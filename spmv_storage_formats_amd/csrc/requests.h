@@ -57,7 +57,7 @@ spmv_status logprobs_grad(const LogprobsGradArgs &a, hipStream_t s);
 // (blocks and tiles that one launch counts).
 constexpr int32_t kMostRank = 256;
 constexpr int32_t kMostAdapters = 2048;
-constexpr int32_t kMostColumns = 1 << 23;
+constexpr int32_t kMostColumns = 1 << 21;
 constexpr int32_t kMostAdaptRows = 1 << 24;
 
 struct AdaptArgs {
