@@ -232,30 +232,67 @@ __device__ inline void shrink_rows(const ShrinkArgs &a, int32_t adapter, int32_t
     for (int m = 0; m < M; ++m)
 #pragma unroll
         for (int b = 0; b < RB; ++b) sum[m][b] = f32x4{0, 0, 0, 0};
-    const int64_t from = static_cast<int64_t>(split) * a.part;
-    const int64_t to = from + a.part < a.D ? from + a.part : a.D;
-    for (int64_t c = from + wave * 32; c < to; c += kAdaptWaves * 32) {
-        const int64_t at = c + q * 8;
-        const int64_t there = to - at;
-        Piece<T, 8> x[M], m[RB];
+    const T *wp[RB];  // ranks past the last repeat it: not used
 #pragma unroll
-        for (int u = 0; u < M; ++u) x[u] = load_some<T, 8>(xp[u] + at, there);
+    for (int b = 0; b < RB; ++b) {
+        const int32_t k = rank0 + b * 16 + i16;
+        const int32_t row = k < a.rank ? k : a.rank - 1;
+        wp[b] = w + (kAcross ? row : static_cast<int64_t>(row) * a.D);
+    }
+    struct Step {
+        Piece<T, 8> x[M], m[RB];
+    };
+    auto load = [&](int64_t c, Step &s) {
+        const int64_t at = c + q * 8;
+#pragma unroll
+        for (int u = 0; u < M; ++u) s.x[u] = load_some<T, 8>(xp[u] + at, 8);
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-            const int32_t k = rank0 + b * 16 + i16;
-            const int32_t row = k < a.rank ? k : a.rank - 1;  // ranks past the last: not used
             if constexpr (kAcross) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    m[b].v[e] = e < there ? w[(at + e) * a.rank + row] : static_cast<T>(0.f);
+                for (int e = 0; e < 8; ++e) s.m[b].v[e] = wp[b][(at + e) * a.rank];
             } else {
-                m[b] = load_some<T, 8>(w + static_cast<int64_t>(row) * a.D + at, there);
+                s.m[b] = load_some<T, 8>(wp[b] + at, 8);
             }
         }
+    };
+    auto add = [&](const Step &s) {
 #pragma unroll
         for (int u = 0; u < M; ++u)
 #pragma unroll
-            for (int b = 0; b < RB; ++b) sum[u][b] = multiply(x[u], m[b], sum[u][b]);
+            for (int b = 0; b < RB; ++b) sum[u][b] = multiply(s.x[u], s.m[b], sum[u][b]);
+    };
+    constexpr int kStep = kAdaptWaves * 32;
+    const int64_t from = static_cast<int64_t>(split) * a.part;
+    const int64_t to = from + a.part < a.D ? from + a.part : a.D;
+    int64_t c = from + wave * 32;
+    if (c + 32 <= to) {
+        // The next columns are loaded before these are multiplied; no branch
+        // around a load: the last ones are loaded again.
+        Step cur, nxt;
+        load(c, cur);
+        for (; c + 32 <= to; c += kStep) {
+            load(c + kStep + 32 <= to ? c + kStep : c, nxt);
+            add(cur);
+            cur = nxt;
+        }
+    }
+    if (c < to) {
+        const int64_t at = c + q * 8, there = to - at;
+        Step s;
+#pragma unroll
+        for (int u = 0; u < M; ++u) s.x[u] = load_some<T, 8>(xp[u] + at, there);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+            if constexpr (kAcross) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    s.m[b].v[e] = e < there ? wp[b][(at + e) * a.rank] : static_cast<T>(0.f);
+            } else {
+                s.m[b] = load_some<T, 8>(wp[b] + at, there);
+            }
+        }
+        add(s);
     }
     // the waves' sums, two and two
     f32x4 *const part = reinterpret_cast<f32x4 *>(lds);
@@ -502,17 +539,31 @@ __global__ __launch_bounds__(kAdaptThreads) void k_adapt_expand(ExpandArgs a) {
         base[e] = static_cast<const B *>(a.base) + t * a.base_ld;
         out[e] = static_cast<B *>(a.out) + t * a.out_ld;
     }
-    const int64_t from = static_cast<int64_t>(blockIdx.y) * a.columns;
-    const int64_t to = from + a.columns < a.D ? from + a.columns : a.D;
-    for (int64_t c0 = from + wave % turns * kExpandColumns; c0 < to;
-         c0 += turns * kExpandColumns) {
+    // Ranks past the last: their lanes load others, which count as 0.
+    using Bits = Piece<uint32_t, K * sizeof(T) / 4>;
+    Bits keep[NG];
+    int32_t k0[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const int32_t first = H::first(g, q);
+        k0[g] = first < a.rank ? first : 0;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const uint32_t m = first + i < a.rank ? ~0u : 0u;
+            if constexpr (sizeof(T) == 4)
+                keep[g].v[i] = m;
+            else
+                keep[g].v[i / 2] = i % 2 ? keep[g].v[i / 2] | (m << 16) : m & 0xffffu;
+        }
+    }
+    auto block = [&](int64_t c0, auto fast) {
+        constexpr bool kFast = decltype(fast)::value;  // every load in bounds
         const int64_t col = c0 + i16 * 8;
-        const bool whole = col + 8 <= a.D;
+        const int64_t left = kFast ? 8 : a.D - col;
         Piece<B, 8> o[4];
         if (a.base) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (there[e]) o[e] = load_some<B, 8>(base[e] + col, a.D - col);
+            for (int e = 0; e < 4; ++e) o[e] = load_some<B, 8>(base[e] + col, left);
         }
         f32x4 sum[8];
 #pragma unroll
@@ -520,15 +571,13 @@ __global__ __launch_bounds__(kAdaptThreads) void k_adapt_expand(ExpandArgs a) {
         if (adapted) {
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const int32_t k0 = H::first(g, q);
                 Piece<T, K> m[8];
                 if constexpr (kAcross) {
                     Piece<T, 8> r[K];
 #pragma unroll
                     for (int k = 0; k < K; ++k) {
-                        const bool in = k0 + k < a.rank;
-                        r[k] = load_some<T, 8>(w + static_cast<int64_t>(in ? k0 + k : 0) * a.D + col,
-                                               in ? a.D - col : 0);
+                        const int32_t row = k0[g] + k < a.rank ? k0[g] + k : a.rank - 1;
+                        r[k] = load_some<T, 8>(w + static_cast<int64_t>(row) * a.D + col, left);
                     }
                     if constexpr (sizeof(T) == 2) {
                         turn(r, m);
@@ -541,16 +590,20 @@ __global__ __launch_bounds__(kAdaptThreads) void k_adapt_expand(ExpandArgs a) {
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        m[j] = load_some<T, K>(w + (col + j) * a.rank + k0,
-                                               col + j < a.D ? a.rank - k0 : 0);
+                        m[j] = load_some<T, K>(w + (col + j) * a.rank + k0[g],
+                                               kFast ? K : j < left ? a.rank - k0[g] : 0);
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[j] = h.by(g, m[j], sum[j]);
+                for (int j = 0; j < 8; ++j) {
+                    Bits bits = __builtin_bit_cast(Bits, m[j]);
+#pragma unroll
+                    for (unsigned i = 0; i < K * sizeof(T) / 4; ++i) bits.v[i] &= keep[g].v[i];
+                    sum[j] = h.by(g, __builtin_bit_cast(std::decay_t<decltype(m[0])>, bits), sum[j]);
+                }
             }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            if (!there[e]) continue;
             float v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -560,11 +613,23 @@ __global__ __launch_bounds__(kAdaptThreads) void k_adapt_expand(ExpandArgs a) {
                     v[j] = adapted ? v[j] + b : b;
                 }
             }
-            if (whole)
+            if (!there[e]) continue;
+            if (left >= 8)
                 store_piece<8>(out[e] + col, v);
-            else if (col < a.D)
-                store_piece_tail<8>(out[e] + col, static_cast<int>(a.D - col), v);
+            else if (left > 0)
+                store_piece_tail<8>(out[e] + col, static_cast<int>(left), v);
         }
+    };
+    const int64_t from = static_cast<int64_t>(blockIdx.y) * a.columns;
+    const int64_t to = from + a.columns < a.D ? from + a.columns : a.D;
+    const int32_t reach = (a.rank - 1) / K * K + K;  // numbers of a matrix row that are loaded
+    for (int64_t c0 = from + wave % turns * kExpandColumns; c0 < to;
+         c0 += turns * kExpandColumns) {
+        const int64_t behind = a.D - c0 - kExpandColumns;  // columns
+        if (behind >= 0 && (kAcross || (behind + 1) * a.rank >= reach))
+            block(c0, std::true_type{});
+        else
+            block(c0, std::false_type{});
     }
 }
 
@@ -646,31 +711,68 @@ __device__ inline void weight_sums(const WeightArgs &a, const AdaptTile &chunk, 
 #pragma unroll
         for (int b = 0; b < RB; ++b) sum[j][b] = f32x4{0, 0, 0, 0};
     const int64_t part = static_cast<int64_t>(a.stride) * a.width;
-    for (int32_t t0 = wave * 32; t0 < chunk.count; t0 += kAdaptWaves * 32) {
-        const int32_t k0 = t0 + q * 8;  // this lane's eight rows of the chunk
+    const V *vp[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+        vp[b] = static_cast<const V *>(a.v) +
+                static_cast<int64_t>(rank0 + b * 16 + i16) * a.stride + chunk.first;
+    const int32_t *order = a.order + chunk.first;
+    const bool whole = col0 + kWeightColumns <= a.D;
+    struct Step {
         Piece<T, 8> x[8];
+        Piece<V, 8> v[RB][P];
+    };
+    // Rows past the last: their numbers count as 0, beside a row that is there.
+    auto load = [&](int32_t t0, Step &s, auto fast) {
+        constexpr bool kFast = decltype(fast)::value;
+        const int32_t k0 = t0 + q * 8;  // this lane's eight rows of the chunk
+        Piece<int32_t, 8> t;
+        __builtin_memcpy(&t, order + k0, sizeof(t));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const bool there = k0 + i < chunk.count;
-            const int32_t t = there ? a.order[chunk.first + k0 + i] : 0;
-            x[i] = load_some<T, 8>(static_cast<const T *>(a.x) + t * a.x_ld + col,
-                                   there ? a.D - col : 0);
+            const int32_t row = k0 + i < chunk.count ? t.v[i] : order[0];
+            s.x[i] = load_some<T, 8>(static_cast<const T *>(a.x) + row * a.x_ld + col,
+                                     kFast ? 8 : a.D - col);
         }
-        Piece<V, 8> v[RB][P];
 #pragma unroll
         for (int b = 0; b < RB; ++b)
 #pragma unroll
-            for (int p = 0; p < P; ++p)
-                v[b][p] = load_some<V, 8>(static_cast<const V *>(a.v) + p * part +
-                                              static_cast<int64_t>(rank0 + b * 16 + i16) * a.stride +
-                                              chunk.first + k0,
-                                          chunk.count - k0);
+            for (int p = 0; p < P; ++p) {
+                s.v[b][p] = load_some<V, 8>(vp[b] + p * part + k0, 8);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    s.v[b][p].v[i] =
+                        k0 + i < chunk.count ? s.v[b][p].v[i] : static_cast<V>(0.f);
+            }
+    };
+    auto add = [&](const Step &s) {
         Columns<T> c;
-        c.set(x);
+        c.set(s.x);
 #pragma unroll
         for (int b = 0; b < RB; ++b)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j][b] = c.template by<kAcross>(j, v[b], sum[j][b]);
+            for (int j = 0; j < 8; ++j) sum[j][b] = c.template by<kAcross>(j, s.v[b], sum[j][b]);
+    };
+    constexpr int kStep = kAdaptWaves * 32;
+    int32_t t0 = wave * 32;
+    if (whole) {
+        if (t0 < chunk.count) {
+            Step cur, nxt;
+            load(t0, cur, std::true_type{});
+#pragma unroll 1
+            for (; t0 < chunk.count; t0 += kStep) {
+                load(t0 + kStep < chunk.count ? t0 + kStep : t0, nxt, std::true_type{});
+                add(cur);
+                cur = nxt;
+            }
+        }
+    } else {
+#pragma unroll 1
+        for (; t0 < chunk.count; t0 += kStep) {
+            Step s;
+            load(t0, s, std::false_type{});
+            add(s);
+        }
     }
     float *const to = a.partial + static_cast<int64_t>(blockIdx.x) * a.rank * a.D;
     auto put = [&](int64_t at, float s) {

@@ -261,6 +261,8 @@ void split(int32_t D, int32_t tiles, int32_t *splits, int32_t *part) {
     *part = per * kUnit;
 }
 
+constexpr int32_t kPast = 32;  // rows that the last step of a chunk loads past its end
+
 Plan plan(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R, bool grad) {
     Plan p{};
     p.width = adapt_width(rank);
@@ -269,7 +271,7 @@ Plan plan(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R, bool 
     p.chunk = std::max(kAdaptChunk, (n / 64 + 31) / 32 * 32);
     p.single = n > 0 && n <= p.chunk;
     p.chunks = p.single ? adapters : (n + p.chunk - 1) / p.chunk + std::min(adapters, n);
-    p.stride = (n + 7) / 8 * 8;
+    p.stride = (n + kPast + 15) / 16 * 16;
     split(C, p.tiles, &p.splits_c, &p.part_c);
     split(R, p.tiles, &p.splits_r, &p.part_r);
     size_t at = 0;
@@ -279,7 +281,7 @@ Plan plan(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R, bool 
         return here;
     };
     const size_t rows = static_cast<size_t>(n) * p.width * sizeof(float);
-    p.order = take(static_cast<size_t>(n) * sizeof(int32_t));
+    p.order = take((static_cast<size_t>(n) + kPast) * sizeof(int32_t));
     p.tile_list = take(static_cast<size_t>(p.tiles) * sizeof(AdaptTile));
     p.sums_c = take(rows * p.splits_c);
     if (grad) {
