@@ -33,7 +33,8 @@ constexpr int kAdaptWaves = kAdaptThreads / kWave;
 
 // `count` rows from place `first` of the sorted list; adapter -1: no tile.
 struct AdaptTile {
-    int32_t adapter, first, count, pad;
+    int32_t adapter, first, count;
+    int32_t tile;               // of a chunk: its first tile
 };
 
 // The rows of a workgroup's tile.  Up to kAdaptDirect rows there are no lists:
@@ -55,6 +56,7 @@ struct ShrinkArgs {
     const void *w;          // adapters x [rank, D], or across [D, rank]
     int32_t D, rank, width;     // width: adapt_width(rank)
     int32_t splits, part;   // parts of D, columns of each
+    int32_t subs;           // workgroups that share a tile's rows
     float *sums;            // [splits][n][width]
 };
 
@@ -69,7 +71,6 @@ struct ExpandArgs {
     int64_t base_ld;
     void *out;
     int64_t out_ld;
-    int32_t columns;        // of a workgroup, whole kExpandColumns
 };
 
 struct FinishArgs {         // sums of splits, scaled, rank by rank
@@ -78,14 +79,19 @@ struct FinishArgs {         // sums of splits, scaled, rank by rank
     const float *scales;
     const int32_t *order;
     const AdaptTile *tiles;
-    void *out;              // [width][stride], rows in sorted order: fp32, or three
-    int32_t stride;         // such arrays of bf16 parts
+    // [width][stride], rows in sorted order: fp32; three such arrays of bf16
+    // parts; or two of fp16 parts, of the numbers times a power of two by tile
+    // and rank whose inverse is in factors [tiles][width]
+    void *out;
+    float *factors;
+    int32_t stride;
 };
 
 struct WeightArgs {
     const void *x;          // [n, D]
     int64_t x_ld;
     const void *v;          // FinishArgs::out
+    const float *factors;
     int32_t stride, D, rank, width;
     const int32_t *order;
     const AdaptTile *chunks;
@@ -115,7 +121,6 @@ inline int32_t adapt_width(int32_t rank) {
 }
 // Ranks of a workgroup of shrink and weights; more are further workgroups.
 inline int32_t adapt_slabs(int32_t rank) { return (rank + 63) / 64; }
-constexpr int32_t kExpandColumns = 128;                  // of a wave, at a time
 constexpr int32_t kWeightColumns = 128;                  // of a workgroup
 
 // bf16 parts of a number: its upper 16 bits, the next ones of the rest, the rest.
@@ -127,42 +132,69 @@ __device__ inline float below(float v) {  // 0 where nothing is left, infinities
     return v == u ? 0.f : v - u;
 }
 
+// The exponent bits that bring a number up to `most` between 2^14 and 2^15 as
+// fp16 parts, and back: powers of two, 1 where `most` is no number.
+struct Power {
+    float up, back;
+};
+__device__ inline Power power(float most) {
+    int e = static_cast<int>(__builtin_bit_cast(uint32_t, most) >> 23);
+    e = e < 15 ? 15 : e == 255 ? 141 : e;
+    return {__builtin_bit_cast(float, static_cast<uint32_t>(268 - e) << 23),
+            __builtin_bit_cast(float, static_cast<uint32_t>(e - 14) << 23)};
+}
+// fp16 parts of such a number: its first 11 bits, and the next.
+__device__ inline f16 rest_of(float v, f16 lead) {
+    return static_cast<f16>(v == static_cast<float>(lead) ? 0.f : v - static_cast<float>(lead));
+}
+
 #ifdef SPMV_ADAPT_KERNELS
 namespace {
 
 using f32x4 = float __attribute__((ext_vector_type(4)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
-using bf16x8 = bf16 __attribute__((ext_vector_type(8)));
-using f16x8 = f16 __attribute__((ext_vector_type(8)));
+
+// Vectors in registers, and in memory at the alignment of their elements: the
+// compiler takes such an access apart if it is one of a struct or an array.
+template <typename T, int E>
+struct VecOf {
+    typedef T type __attribute__((ext_vector_type(E)));
+    typedef T loose __attribute__((ext_vector_type(E), aligned(sizeof(T)), may_alias));
+};
+template <typename T, int E>
+using Vec = typename VecOf<T, E>::type;
+template <typename T, int E>
+using Loose = typename VecOf<T, E>::loose;
 
 // Operands: the lane's row (or column) is lane % 16, its summed indexes eight
 // neighbours from 8 * (lane / 16).  Results: column lane % 16, rows
 // 4 * (lane / 16) + 0..3.
-__device__ inline f32x4 multiply(Piece<bf16, 8> a, Piece<bf16, 8> b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+__device__ inline f32x4 multiply(Vec<bf16, 8> a, Vec<bf16, 8> b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-__device__ inline f32x4 multiply(Piece<f16, 8> a, Piece<f16, 8> b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
-                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+__device__ inline f32x4 multiply(Vec<f16, 8> a, Vec<f16, 8> b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
-__device__ inline f32x4 multiply(const Piece<float, 8> &a, const Piece<float, 8> &b, f32x4 c) {
+__device__ inline f32x4 multiply(const Vec<float, 8> &a, const Vec<float, 8> &b, f32x4 c) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
     return c;
 }
 
+// E neighbours, the first `there` of them; the others are 0.
 template <typename T, int E>
-__device__ inline Piece<T, E> load_some(const T *p, int64_t there) {
-    Piece<T, E> o;
-    if (there >= E) {
-        __builtin_memcpy(&o, p, sizeof(o));
-    } else {
+__device__ inline Vec<T, E> load_some(const T *p, int64_t there) {
+    if (there >= E) return *reinterpret_cast<const Loose<T, E> *>(p);
+    Vec<T, E> o = {};
 #pragma unroll
-        for (int i = 0; i < E; ++i) o.v[i] = i < there ? p[i] : static_cast<T>(0.f);
-    }
+    for (int i = 0; i < E; ++i)
+        if (i < there) o[i] = p[i];
     return o;
+}
+template <typename T, int E>
+__device__ inline Vec<T, E> load_all(const T *p) {
+    return *reinterpret_cast<const Loose<T, E> *>(p);
 }
 
 // --------------------------------------------------------------------- rows
@@ -174,10 +206,11 @@ struct RowsShared {
 
 // The tile's rows to LDS; returns its adapter (`adapters`: none, -1: no tile)
 // and their number.
-__device__ inline int32_t find_rows(const RowsArgs &a, RowsShared &s, int32_t *count) {
+__device__ inline int32_t find_rows(const RowsArgs &a, int32_t number, RowsShared &s,
+                                    int32_t *count) {
     const int tid = threadIdx.x, lane = tid % kWave;
     if (a.tiles) {
-        const AdaptTile tile = a.tiles[blockIdx.x];
+        const AdaptTile tile = a.tiles[number];
         if (tile.adapter >= 0 && tid < tile.count) s.row[tid] = a.order[tile.first + tid];
         __syncthreads();
         *count = tile.count;
@@ -188,7 +221,7 @@ __device__ inline int32_t find_rows(const RowsArgs &a, RowsShared &s, int32_t *c
                                                     : static_cast<const int64_t *>(a.ids)[t];
         return id >= 0 && id < a.adapters ? static_cast<int32_t>(id) : a.adapters;
     };
-    const int32_t t = static_cast<int32_t>(blockIdx.x), own = key(t);
+    const int32_t t = number, own = key(t);
     const bool same = tid < a.n && key(tid) == own;
     const unsigned long long mask = __ballot(same);
     if (lane == 0) s.same[tid / kWave] = mask;
@@ -240,19 +273,19 @@ __device__ inline void shrink_rows(const ShrinkArgs &a, int32_t adapter, int32_t
         wp[b] = w + (kAcross ? row : static_cast<int64_t>(row) * a.D);
     }
     struct Step {
-        Piece<T, 8> x[M], m[RB];
+        Vec<T, 8> x[M], m[RB];
     };
     auto load = [&](int64_t c, Step &s) {
         const int64_t at = c + q * 8;
 #pragma unroll
-        for (int u = 0; u < M; ++u) s.x[u] = load_some<T, 8>(xp[u] + at, 8);
+        for (int u = 0; u < M; ++u) s.x[u] = load_all<T, 8>(xp[u] + at);
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
             if constexpr (kAcross) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s.m[b].v[e] = wp[b][(at + e) * a.rank];
+                for (int e = 0; e < 8; ++e) s.m[b][e] = wp[b][(at + e) * a.rank];
             } else {
-                s.m[b] = load_some<T, 8>(wp[b] + at, 8);
+                s.m[b] = load_all<T, 8>(wp[b] + at);
             }
         }
     };
@@ -287,7 +320,7 @@ __device__ inline void shrink_rows(const ShrinkArgs &a, int32_t adapter, int32_t
             if constexpr (kAcross) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    s.m[b].v[e] = e < there ? wp[b][(at + e) * a.rank] : static_cast<T>(0.f);
+                    s.m[b][e] = e < there ? wp[b][(at + e) * a.rank] : static_cast<T>(0.f);
             } else {
                 s.m[b] = load_some<T, 8>(wp[b] + at, there);
             }
@@ -325,52 +358,68 @@ __device__ inline void shrink_rows(const ShrinkArgs &a, int32_t adapter, int32_t
         }
 }
 
-template <typename T, int RB>
+template <typename T, int RB, int M>
 __global__ __launch_bounds__(kAdaptThreads) void k_adapt_shrink(ShrinkArgs a) {
-    __shared__ __attribute__((aligned(16))) float lds[2 * 4 * RB * kWave * 4];
+    __shared__ __attribute__((aligned(16))) float lds[2 * M * RB * kWave * 4];
     __shared__ RowsShared s_rows;
     int32_t count;
-    const int32_t adapter = find_rows(a.rows, s_rows, &count);
-    if (adapter < 0 || adapter >= a.rows.adapters) return;
+    const int32_t tile = static_cast<int32_t>(blockIdx.x) / a.subs;
+    const int32_t row0 = static_cast<int32_t>(blockIdx.x) % a.subs * (16 * M);
+    const int32_t adapter = find_rows(a.rows, tile, s_rows, &count);
+    if (adapter < 0 || adapter >= a.rows.adapters || row0 >= count) return;
     const int32_t rank0 = static_cast<int32_t>(blockIdx.z) * 64;
-    if (count <= 16)
-        shrink_rows<T, RB, false, 1>(a, adapter, count, s_rows.row, blockIdx.y, rank0, lds);
-    else
-        shrink_rows<T, RB, false, 4>(a, adapter, count, s_rows.row, blockIdx.y, rank0, lds);
+    shrink_rows<T, RB, false, M>(a, adapter, count - row0, s_rows.row + row0, blockIdx.y, rank0,
+                                 lds);
 }
 
 // x by down and grad by up, in one launch.
-template <typename T, int RB>
+template <typename T, int RB, int M>
 __global__ __launch_bounds__(kAdaptThreads) void k_adapt_shrink_both(ShrinkArgs a, ShrinkArgs c) {
-    __shared__ __attribute__((aligned(16))) float lds[2 * 4 * RB * kWave * 4];
+    __shared__ __attribute__((aligned(16))) float lds[2 * M * RB * kWave * 4];
     __shared__ RowsShared s_rows;
     int32_t count;
-    const int32_t adapter = find_rows(a.rows, s_rows, &count);
-    if (adapter < 0 || adapter >= a.rows.adapters) return;
+    const int32_t tile = static_cast<int32_t>(blockIdx.x) / a.subs;
+    const int32_t row0 = static_cast<int32_t>(blockIdx.x) % a.subs * (16 * M);
+    const int32_t adapter = find_rows(a.rows, tile, s_rows, &count);
+    if (adapter < 0 || adapter >= a.rows.adapters || row0 >= count) return;
     const int32_t rank0 = static_cast<int32_t>(blockIdx.z) * 64;
     const int32_t y = static_cast<int32_t>(blockIdx.y);
     if (y < a.splits)
-        shrink_rows<T, RB, false, 4>(a, adapter, count, s_rows.row, y, rank0, lds);
+        shrink_rows<T, RB, false, M>(a, adapter, count - row0, s_rows.row + row0, y, rank0, lds);
     else
-        shrink_rows<T, RB, true, 4>(c, adapter, count, s_rows.row, y - a.splits, rank0, lds);
+        shrink_rows<T, RB, true, M>(c, adapter, count - row0, s_rows.row + row0, y - a.splits,
+                                    rank0, lds);
 }
 
 // ------------------------------------------------------------------- expand
 
-// Eight rows of eight 16-bit numbers, turned into columns.
-template <typename T>
-__device__ inline void turn(const Piece<T, 8> (&row)[8], Piece<T, 8> (&col)[8]) {
-    u32x4 in[8], out[8];
+// K rows of N numbers (of 16 bits: eight rows), turned into columns.
+template <typename T, int N, int K>
+__device__ inline void turn(const Vec<T, N> (&row)[K], Vec<T, K> (&col)[N]) {
+    if constexpr (sizeof(T) == 2) {
+        static_assert(K == 8);
+        using W = uint32_t __attribute__((ext_vector_type(N / 2)));
+        W in[8];
+        u32x4 out[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) in[i] = __builtin_bit_cast(u32x4, row[i]);
+        for (int i = 0; i < 8; ++i) in[i] = __builtin_bit_cast(W, row[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < N; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            out[j][i] = __builtin_amdgcn_perm(in[2 * i + 1][j / 2], in[2 * i][j / 2],
-                                              j % 2 ? 0x07060302u : 0x05040100u);
+            for (int i = 0; i < 4; ++i)
+                out[j][i] = __builtin_amdgcn_perm(in[2 * i + 1][j / 2], in[2 * i][j / 2],
+                                                  j % 2 ? 0x07060302u : 0x05040100u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) col[j] = __builtin_bit_cast(Piece<T, 8>, out[j]);
+        for (int j = 0; j < N; ++j) {
+            using Col = Vec<T, K>;
+            col[j] = __builtin_bit_cast(Col, out[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int k = 0; k < K; ++k) col[j][k] = row[k][j];
+    }
 }
 
 // The numbers of a row, as operands beside a matrix of type T.  The ranks are
@@ -389,7 +438,7 @@ struct Numbers<bf16, G, kAll> {
     static constexpr int kPer = 8;
     static constexpr int kGroups = G == 0 ? 1 : G;
     static constexpr int kParts = G == 0 ? (kAll ? 2 : 1) : (kAll ? 3 : 2);
-    Piece<bf16, 8> p[kGroups][kParts];
+    Vec<bf16, 8> p[kGroups][kParts];
     static __device__ inline int first(int g, int q) { return G == 0 ? q % 2 * 8 : g * 32 + q * 8; }
     __device__ inline float set(const float (&h)[kGroups][8], int q) {
 #pragma unroll
@@ -399,18 +448,18 @@ struct Numbers<bf16, G, kAll> {
                 const float v = h[g][i], next = below(v);
                 const bf16 mid = kAll ? upper(next) : static_cast<bf16>(next);
                 if constexpr (G == 0) {
-                    p[g][0].v[i] = q < 2 ? upper(v) : mid;
+                    p[g][0][i] = q < 2 ? upper(v) : mid;
                     if constexpr (kAll)
-                        p[g][1].v[i] = q < 2 ? upper(below(next)) : static_cast<bf16>(0.f);
+                        p[g][1][i] = q < 2 ? upper(below(next)) : static_cast<bf16>(0.f);
                 } else {
-                    p[g][0].v[i] = upper(v);
-                    p[g][1].v[i] = mid;
-                    if constexpr (kAll) p[g][2].v[i] = upper(below(next));
+                    p[g][0][i] = upper(v);
+                    p[g][1][i] = mid;
+                    if constexpr (kAll) p[g][2][i] = upper(below(next));
                 }
             }
         return 1.f;
     }
-    __device__ inline f32x4 by(int g, const Piece<bf16, 8> &w, f32x4 c) const {
+    __device__ inline f32x4 by(int g, const Vec<bf16, 8> &w, f32x4 c) const {
 #pragma unroll
         for (int k = kParts - 1; k >= 0; --k) c = multiply(p[g][k], w, c);
         return c;
@@ -422,7 +471,7 @@ struct Numbers<f16, G, kAll> {
     static constexpr int kPer = 8;
     static constexpr int kGroups = G == 0 ? 1 : G;
     static constexpr int kParts = G == 0 ? 1 : 2;
-    Piece<f16, 8> p[kGroups][kParts];
+    Vec<f16, 8> p[kGroups][kParts];
     static __device__ inline int first(int g, int q) { return G == 0 ? q % 2 * 8 : g * 32 + q * 8; }
     __device__ inline float set(const float (&h)[kGroups][8], int q) {
         float most = 0.f;
@@ -432,27 +481,23 @@ struct Numbers<f16, G, kAll> {
             for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(h[g][i]));
         most = fmaxf(most, __shfl_xor(most, 16));
         most = fmaxf(most, __shfl_xor(most, 32));
-        int e = static_cast<int>(__builtin_bit_cast(uint32_t, most) >> 23);
-        e = e < 15 ? 15 : e == 255 ? 141 : e;  // infinities: as they are
-        const float up = __builtin_bit_cast(float, static_cast<uint32_t>(268 - e) << 23);
+        const Power power = spmv::power(most);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float v = h[g][i] * up;
-                const f16 lead = static_cast<f16>(v);
-                const float left = v - static_cast<float>(lead);
-                const f16 rest = static_cast<f16>(v == static_cast<float>(lead) ? 0.f : left);
+                const float v = h[g][i] * power.up;
+                const f16 lead = static_cast<f16>(v), rest = rest_of(v, lead);
                 if constexpr (G == 0) {
-                    p[g][0].v[i] = q < 2 ? lead : rest;
+                    p[g][0][i] = q < 2 ? lead : rest;
                 } else {
-                    p[g][0].v[i] = lead;
-                    p[g][1].v[i] = rest;
+                    p[g][0][i] = lead;
+                    p[g][1][i] = rest;
                 }
             }
-        return __builtin_bit_cast(float, static_cast<uint32_t>(e - 14) << 23);
+        return power.back;
     }
-    __device__ inline f32x4 by(int g, const Piece<f16, 8> &w, f32x4 c) const {
+    __device__ inline f32x4 by(int g, const Vec<f16, 8> &w, f32x4 c) const {
 #pragma unroll
         for (int k = kParts - 1; k >= 0; --k) c = multiply(p[g][k], w, c);
         return c;
@@ -463,173 +508,233 @@ template <int G, bool kAll>
 struct Numbers<float, G, kAll> {
     static constexpr int kPer = G == 0 ? 4 : 8;
     static constexpr int kGroups = G == 0 ? 1 : G;
-    Piece<float, kPer> p[kGroups];
+    Vec<float, kPer> p[kGroups];
     static __device__ inline int first(int g, int q) { return g * 32 + q * kPer; }
     __device__ inline float set(const float (&h)[kGroups][kPer], int) {
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) p[g].v[i] = h[g][i];
+            for (int i = 0; i < kPer; ++i) p[g][i] = h[g][i];
         return 1.f;
     }
-    __device__ inline f32x4 by(int g, const Piece<float, kPer> &w, f32x4 c) const {
+    __device__ inline f32x4 by(int g, const Vec<float, kPer> &w, f32x4 c) const {
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            c = __builtin_amdgcn_mfma_f32_16x16x4f32(p[g].v[i], w.v[i], c, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(p[g][i], w[i], c, 0, 0, 0);
         return c;
     }
 };
 
-// A workgroup takes a tile and a range of columns.  A wave keeps the numbers of
-// 16 rows in registers and goes over its columns, 128 at a time; the waves take
-// further rows first, then further columns.  Column tile j holds columns
-// i16 * 8 + j, so that a lane's results of one row are eight neighbours and 16
-// lanes read the base and write 256 neighbouring bytes.
-template <typename T, typename B, int G, bool kAcross>
+// A workgroup takes a tile and 4 * 16 * NT columns.  The numbers of its rows
+// become operands in LDS, each wave those of 16 rows; then each wave keeps its
+// columns of the matrix in registers and goes over the rows, 16 at a time.
+// Column tile j holds columns i16 * NT + j, so that a lane's results of one row
+// are neighbours, and those of 16 lanes are 128 bytes (fp32: 256) or more.
+template <typename T, typename B, int G, int NT, bool kAcross>
 __global__ __launch_bounds__(kAdaptThreads) void k_adapt_expand(ExpandArgs a) {
     using H = Numbers<T, G, sizeof(B) == 4>;
+    using M = Vec<T, H::kPer>;
     constexpr int K = H::kPer, NG = H::kGroups;
+    constexpr int kWords = sizeof(H) / 16;       // of the numbers of a lane's row
+    constexpr int kTiles = kWords <= 8 ? 4 : 1;  // 16 rows each, in LDS at a time
+    // more of the matrix than this is loaded again for each 16 rows
+    constexpr bool kHold = NG * sizeof(M) <= 32;
+    __shared__ u32x4 s_h[kTiles][kWords][kWave];
+    __shared__ float s_back[std::is_same<T, f16>::value ? kAdaptTile : 1];
     __shared__ RowsShared s_rows;
     int32_t count;
-    const int32_t adapter = find_rows(a.rows, s_rows, &count);
+    const int32_t blocks = (a.D - 1) / (kAdaptWaves * 16 * NT) + 1;
+    const int32_t tile = static_cast<int32_t>(blockIdx.x) / blocks;
+    const int32_t adapter = find_rows(a.rows, tile, s_rows, &count);
     if (adapter < 0) return;
     const int lane = threadIdx.x % kWave, i16 = lane % 16, q = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const bool adapted = adapter < a.rows.adapters;
     if (!adapted && a.base == a.out) return;
-    const int turns = count <= 16 ? 4 : count <= 32 ? 2 : 1;  // waves on the same rows
-    const int row0 = wave / turns * 16;
-    if (row0 >= count) return;
-    const T *w = static_cast<const T *>(a.w) +
-                 static_cast<int64_t>(adapted ? adapter : 0) * a.rank * a.D;
-    H h;
-    float back[4] = {1.f, 1.f, 1.f, 1.f};
-    if (adapted) {
-        const float scale = a.scales ? a.scales[adapter] : 1.f;
-        const int32_t t = s_rows.row[row0 + i16 < count ? row0 + i16 : count - 1];
-        float v[NG][K];
+    const int64_t first =
+        (static_cast<int64_t>(static_cast<int32_t>(blockIdx.x) % blocks) * kAdaptWaves + wave) *
+        (16 * NT);
+    const int64_t col = first + i16 * NT;
+    const bool whole = first + 16 * NT <= a.D;
+    auto load_base = [&](int u, Vec<B, NT> (&o)[4]) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const float *p = a.sums + static_cast<int64_t>(t) * a.width + H::first(g, q);
-            load_piece<K>(p, v[g]);
-            for (int32_t j = 1; j < a.splits; ++j) {
-                float more[K];
-                load_piece<K>(p + static_cast<int64_t>(j) * a.rows.n * a.width, more);
+        for (int e = 0; e < 4; ++e) {
+            const int32_t k = u * 16 + q * 4 + e;
+            const B *p = static_cast<const B *>(a.base) +
+                         s_rows.row[k < count ? k : 0] * a.base_ld + col;
+            o[e] = whole ? load_all<B, NT>(p) : load_some<B, NT>(p, a.D - col);
+        }
+    };
+    auto store = [&](int u, int e, Vec<B, NT> v) {
+        const int32_t k = u * 16 + q * 4 + e;
+        if (k >= count) return;
+        B *p = static_cast<B *>(a.out) + s_rows.row[k] * a.out_ld + col;
+        if (whole) {
+            *reinterpret_cast<Loose<B, NT> *>(p) = v;
+        } else {
 #pragma unroll
-                for (int i = 0; i < K; ++i) v[g][i] += more[i];
+            for (int j = 0; j < NT; ++j)
+                if (col + j < a.D) p[j] = v[j];
+        }
+    };
+    if (!adapted) {  // hands the base on
+        for (int u = 0; u * 16 < count; ++u) {
+            Vec<B, NT> o[4] = {};
+            if (a.base) load_base(u, o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) store(u, e, o[e]);
+        }
+        return;
+    }
+
+    // The matrix: this wave's columns; ranks past the last count as 0 (their
+    // lanes load others).
+    const T *w = static_cast<const T *>(a.w) + static_cast<int64_t>(adapter) * a.rank * a.D;
+    const int32_t reach = (a.rank - 1) / K * K + K;  // numbers of a row that are loaded
+    const bool fast = whole && (kAcross || (a.D - first - 16 * NT + 1) * a.rank >= reach);
+    auto load_matrix = [&](int g, M (&m)[NT]) {
+        const int32_t k1 = H::first(g, q), k0 = k1 < a.rank ? k1 : 0;
+        if constexpr (kAcross) {
+            Vec<T, NT> r[K];
+            if (fast) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const int32_t row = k0 + k < a.rank ? k0 + k : a.rank - 1;
+                    r[k] = load_all<T, NT>(w + static_cast<int64_t>(row) * a.D + col);
+                }
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < K; ++k) {
+                    const int32_t row = k0 + k < a.rank ? k0 + k : a.rank - 1;
+                    const Vec<T, NT> o =
+                        load_some<T, NT>(w + static_cast<int64_t>(row) * a.D + col, a.D - col);
+#pragma unroll
+                    for (int i = 0; i < K; ++i)
+                        if (i == k) r[i] = o;
+                }
             }
+            turn<T, NT, K>(r, m);
+        } else if (fast) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) m[j] = load_all<T, K>(w + (col + j) * a.rank + k0);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < NT; ++j) {
+                const M o = load_some<T, K>(w + (col + j) * a.rank + k0,
+                                            col + j < a.D ? a.rank - k0 : 0);
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    if (i == j) m[i] = o;
+            }
+        }
+    };
+    auto mask_matrix = [&](int g, M (&m)[NT]) {
+        const int32_t k1 = H::first(g, q);
+        using Bits = Vec<uint32_t, sizeof(M) / 4>;
+        Bits mask;
+#pragma unroll
+        for (unsigned i = 0; i < sizeof(M) / 4; ++i) {
+            if constexpr (sizeof(T) == 4)
+                mask[i] = k1 + static_cast<int>(i) < a.rank ? ~0u : 0u;
+            else
+                mask[i] = (k1 + 2 * static_cast<int>(i) < a.rank ? 0xffffu : 0u) |
+                            (k1 + 2 * static_cast<int>(i) + 1 < a.rank ? 0xffff0000u : 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            Bits bits = __builtin_bit_cast(Bits, m[j]);
+#pragma unroll
+            for (unsigned i = 0; i < sizeof(M) / 4; ++i) bits[i] &= mask[i];
+            m[j] = __builtin_bit_cast(M, bits);
+        }
+    };
+    M m[kHold ? NG : 1][NT];
+    if constexpr (kHold) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) load_matrix(g, m[g]);
+    }
+    const float scale = a.scales ? a.scales[adapter] : 1.f;
+    auto stage = [&](int u, int slot) {
+        const int32_t t = s_rows.row[u * 16 + i16 < count ? u * 16 + i16 : count - 1];
+        float v[NG][K] = {};
+        constexpr int kAhead = NG >= 4 ? 1 : 4 / NG;  // splits whose loads are in flight
+#pragma unroll 1
+        for (int32_t j0 = 0; j0 < a.splits; j0 += kAhead) {
+            Vec<float, K> more[kAhead][NG];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int32_t at = j0 + j < a.splits ? j0 + j : 0;
+                const float *p = a.sums + (static_cast<int64_t>(at) * a.rows.n + t) * a.width;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) more[j][g] = load_all<float, K>(p + H::first(g, q));
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (j0 + j >= a.splits) continue;
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int i = 0; i < K; ++i) v[g][i] += more[j][g][i];
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int i = 0; i < K; ++i)
                 v[g][i] = H::first(g, q) + i < a.rank ? v[g][i] * scale : 0.f;
-        }
-        const float factor = h.set(v, q);
+        H h;
+        const float back = h.set(v, q);
         if constexpr (std::is_same<T, f16>::value) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) back[e] = __shfl(factor, q * 4 + e);
+            if (q == 0) s_back[u * 16 + i16] = back;
         }
-    }
-    const B *base[4];
-    B *out[4];
-    bool there[4];
+        u32x4 words[kWords];
+        __builtin_memcpy(words, &h, sizeof(words));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {  // the rows of this lane's results
-        const int32_t k = row0 + q * 4 + e;
-        there[e] = k < count;
-        const int64_t t = s_rows.row[there[e] ? k : 0];
-        base[e] = static_cast<const B *>(a.base) + t * a.base_ld;
-        out[e] = static_cast<B *>(a.out) + t * a.out_ld;
-    }
-    // Ranks past the last: their lanes load others, which count as 0.
-    using Bits = Piece<uint32_t, K * sizeof(T) / 4>;
-    Bits keep[NG];
-    int32_t k0[NG];
+        for (int i = 0; i < kWords; ++i) s_h[slot][i][lane] = words[i];
+    };
+#pragma unroll 1
+    for (int u0 = 0; u0 * 16 < count; u0 += kTiles) {
+        if (u0 > 0) __syncthreads();
+        if (wave < kTiles && (u0 + wave) * 16 < count) stage(u0 + wave, wave);
+        __syncthreads();
+        if constexpr (kHold) {
+            if (u0 == 0) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        const int32_t first = H::first(g, q);
-        k0[g] = first < a.rank ? first : 0;
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const uint32_t m = first + i < a.rank ? ~0u : 0u;
-            if constexpr (sizeof(T) == 4)
-                keep[g].v[i] = m;
-            else
-                keep[g].v[i / 2] = i % 2 ? keep[g].v[i / 2] | (m << 16) : m & 0xffffu;
+                for (int g = 0; g < NG; ++g) mask_matrix(g, m[g]);
+            }
         }
-    }
-    auto block = [&](int64_t c0, auto fast) {
-        constexpr bool kFast = decltype(fast)::value;  // every load in bounds
-        const int64_t col = c0 + i16 * 8;
-        const int64_t left = kFast ? 8 : a.D - col;
-        Piece<B, 8> o[4];
-        if (a.base) {
+#pragma unroll 1
+        for (int u = u0; u < u0 + kTiles && u * 16 < count; ++u) {
+            Vec<B, NT> o[4];
+            if (a.base) load_base(u, o);
+            H h;
+            u32x4 words[kWords];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = load_some<B, 8>(base[e] + col, left);
-        }
-        f32x4 sum[8];
+            for (int i = 0; i < kWords; ++i) words[i] = s_h[u - u0][i][lane];
+            __builtin_memcpy(&h, words, sizeof(words));
+            f32x4 sum[NT];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = f32x4{0, 0, 0, 0};
-        if (adapted) {
+            for (int j = 0; j < NT; ++j) sum[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                Piece<T, K> m[8];
-                if constexpr (kAcross) {
-                    Piece<T, 8> r[K];
-#pragma unroll
-                    for (int k = 0; k < K; ++k) {
-                        const int32_t row = k0[g] + k < a.rank ? k0[g] + k : a.rank - 1;
-                        r[k] = load_some<T, 8>(w + static_cast<int64_t>(row) * a.D + col, left);
-                    }
-                    if constexpr (sizeof(T) == 2) {
-                        turn(r, m);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-#pragma unroll
-                            for (int k = 0; k < K; ++k) m[j].v[k] = r[k].v[j];
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        m[j] = load_some<T, K>(w + (col + j) * a.rank + k0[g],
-                                               kFast ? K : j < left ? a.rank - k0[g] : 0);
+                if constexpr (!kHold) {
+                    load_matrix(g, m[0]);
+                    mask_matrix(g, m[0]);
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    Bits bits = __builtin_bit_cast(Bits, m[j]);
+                for (int j = 0; j < NT; ++j) sum[j] = h.by(g, m[kHold ? g : 0][j], sum[j]);
+            }
 #pragma unroll
-                    for (unsigned i = 0; i < K * sizeof(T) / 4; ++i) bits.v[i] &= keep[g].v[i];
-                    sum[j] = h.by(g, __builtin_bit_cast(std::decay_t<decltype(m[0])>, bits), sum[j]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                float back = 1.f;
+                if constexpr (std::is_same<T, f16>::value) back = s_back[u * 16 + q * 4 + e];
+                Vec<float, NT> v;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) v[j] = sum[j][e] * back;
+                if (a.base) v += __builtin_convertvector(o[e], Vec<float, NT>);
+                store(u, e, __builtin_convertvector(v, Vec<B, NT>));
             }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] = sum[j][e] * back[e];
-                if (a.base) {
-                    const float b = static_cast<float>(o[e].v[j]);
-                    v[j] = adapted ? v[j] + b : b;
-                }
-            }
-            if (!there[e]) continue;
-            if (left >= 8)
-                store_piece<8>(out[e] + col, v);
-            else if (left > 0)
-                store_piece_tail<8>(out[e] + col, static_cast<int>(left), v);
-        }
-    };
-    const int64_t from = static_cast<int64_t>(blockIdx.y) * a.columns;
-    const int64_t to = from + a.columns < a.D ? from + a.columns : a.D;
-    const int32_t reach = (a.rank - 1) / K * K + K;  // numbers of a matrix row that are loaded
-    for (int64_t c0 = from + wave % turns * kExpandColumns; c0 < to;
-         c0 += turns * kExpandColumns) {
-        const int64_t behind = a.D - c0 - kExpandColumns;  // columns
-        if (behind >= 0 && (kAcross || (behind + 1) * a.rank >= reach))
-            block(c0, std::true_type{});
-        else
-            block(c0, std::false_type{});
     }
 }
 
@@ -640,58 +745,30 @@ __global__ __launch_bounds__(kAdaptThreads) void k_adapt_expand(ExpandArgs a) {
 // lane's rows and columns, 8 x 8, are turned into operands of eight rows for
 // eight column tiles (tile j: columns i16 * 8 + j).
 template <typename T>
-struct Columns;  // x's operands and their product with the parts of v
-template <>
-struct Columns<bf16> {
-    Piece<bf16, 8> c[8];
-    __device__ inline void set(const Piece<bf16, 8> (&x)[8]) { turn(x, c); }
-    template <bool kAcross>
-    __device__ inline f32x4 by(int j, const Piece<bf16, 8> (&v)[3], f32x4 s) const {
+struct Columns {  // x's operands and their product with the P parts of v
+    Vec<T, 8> c[8];
+    __device__ inline void set(const Vec<T, 8> (&x)[8]) { turn<T, 8, 8>(x, c); }
+    template <bool kAcross, int P>
+    __device__ inline f32x4 by(int j, const Vec<T, 8> (&v)[P], f32x4 s) const {
 #pragma unroll
-        for (int p = 2; p >= 0; --p) s = kAcross ? multiply(v[p], c[j], s) : multiply(c[j], v[p], s);
-        return s;
-    }
-};
-template <>
-struct Columns<f16> {  // two bf16 parts hold the 11 bits of an fp16 number
-    Piece<bf16, 8> c[8], d[8];
-    __device__ inline void set(const Piece<f16, 8> (&x)[8]) {
-        Piece<bf16, 8> lead[8], rest[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float f = static_cast<float>(x[i].v[j]);
-                lead[i].v[j] = upper(f);
-                rest[i].v[j] = upper(below(f));
-            }
-        turn(lead, c);
-        turn(rest, d);
-    }
-    // the rest's product with the third part lies below fp32's last bit
-    template <bool kAcross>
-    __device__ inline f32x4 by(int j, const Piece<bf16, 8> (&v)[3], f32x4 s) const {
-#pragma unroll
-        for (int p = 2; p >= 0; --p) {
-            if (p < 2) s = kAcross ? multiply(v[p], d[j], s) : multiply(d[j], v[p], s);
+        for (int p = P - 1; p >= 0; --p)
             s = kAcross ? multiply(v[p], c[j], s) : multiply(c[j], v[p], s);
-        }
         return s;
     }
 };
 template <>
 struct Columns<float> {
-    Piece<float, 8> x[8];
-    __device__ inline void set(const Piece<float, 8> (&r)[8]) {
+    Vec<float, 8> x[8];
+    __device__ inline void set(const Vec<float, 8> (&r)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = r[i];
     }
-    template <bool kAcross>
-    __device__ inline f32x4 by(int j, const Piece<float, 8> (&v)[1], f32x4 s) const {
+    template <bool kAcross, int P>
+    __device__ inline f32x4 by(int j, const Vec<float, 8> (&v)[P], f32x4 s) const {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            s = kAcross ? __builtin_amdgcn_mfma_f32_16x16x4f32(v[0].v[i], x[i].v[j], s, 0, 0, 0)
-                        : __builtin_amdgcn_mfma_f32_16x16x4f32(x[i].v[j], v[0].v[i], s, 0, 0, 0);
+            s = kAcross ? __builtin_amdgcn_mfma_f32_16x16x4f32(v[0][i], x[i][j], s, 0, 0, 0)
+                        : __builtin_amdgcn_mfma_f32_16x16x4f32(x[i][j], v[0][i], s, 0, 0, 0);
         return s;
     }
 };
@@ -699,8 +776,9 @@ struct Columns<float> {
 template <typename T, int RB, bool kAcross>
 __device__ inline void weight_sums(const WeightArgs &a, const AdaptTile &chunk, int32_t block,
                                    int32_t rank0, f32x4 (*lds)[8][kWave]) {
-    using V = std::conditional_t<sizeof(T) == 4, float, bf16>;
-    constexpr int P = sizeof(T) == 4 ? 1 : 3;
+    using V = T;
+    constexpr bool kScaled = std::is_same<T, f16>::value;
+    constexpr int P = sizeof(T) == 4 ? 1 : kScaled ? 2 : 3;
     const int lane = threadIdx.x % kWave, i16 = lane % 16, q = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t col0 = static_cast<int64_t>(block) * kWeightColumns;
@@ -719,31 +797,42 @@ __device__ inline void weight_sums(const WeightArgs &a, const AdaptTile &chunk, 
     const int32_t *order = a.order + chunk.first;
     const bool whole = col0 + kWeightColumns <= a.D;
     struct Step {
-        Piece<T, 8> x[8];
-        Piece<V, 8> v[RB][P];
+        Vec<T, 8> x[8];
+        Vec<V, 8> v[RB][P];
+        f32x4 factor[kScaled ? RB : 1];  // of results e (all of one rank: [0])
     };
     // Rows past the last: their numbers count as 0, beside a row that is there.
     auto load = [&](int32_t t0, Step &s, auto fast) {
         constexpr bool kFast = decltype(fast)::value;
         const int32_t k0 = t0 + q * 8;  // this lane's eight rows of the chunk
-        Piece<int32_t, 8> t;
-        __builtin_memcpy(&t, order + k0, sizeof(t));
+        const Vec<int32_t, 8> t = load_all<int32_t, 8>(order + k0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int32_t row = k0 + i < chunk.count ? t.v[i] : order[0];
-            s.x[i] = load_some<T, 8>(static_cast<const T *>(a.x) + row * a.x_ld + col,
-                                     kFast ? 8 : a.D - col);
+            const int32_t row = k0 + i < chunk.count ? t[i] : order[0];
+            const T *p = static_cast<const T *>(a.x) + row * a.x_ld + col;
+            s.x[i] = kFast ? load_all<T, 8>(p) : load_some<T, 8>(p, a.D - col);
         }
 #pragma unroll
         for (int b = 0; b < RB; ++b)
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                s.v[b][p] = load_some<V, 8>(vp[b] + p * part + k0, 8);
+                s.v[b][p] = load_all<V, 8>(vp[b] + p * part + k0);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    s.v[b][p].v[i] =
-                        k0 + i < chunk.count ? s.v[b][p].v[i] : static_cast<V>(0.f);
+                    s.v[b][p][i] =
+                        k0 + i < chunk.count ? s.v[b][p][i] : static_cast<V>(0.f);
             }
+        if constexpr (kScaled) {
+            const float *f = a.factors +
+                             static_cast<int64_t>(chunk.tile + t0 / kAdaptTile) * a.width + rank0;
+#pragma unroll
+            for (int b = 0; b < RB; ++b) {
+                if constexpr (kAcross)
+                    s.factor[b] = load_all<float, 4>(f + b * 16 + q * 4);
+                else
+                    s.factor[b] = f32x4{f[b * 16 + i16], 0, 0, 0};
+            }
+        }
     };
     auto add = [&](const Step &s) {
         Columns<T> c;
@@ -751,7 +840,16 @@ __device__ inline void weight_sums(const WeightArgs &a, const AdaptTile &chunk, 
 #pragma unroll
         for (int b = 0; b < RB; ++b)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j][b] = c.template by<kAcross>(j, s.v[b], sum[j][b]);
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (kScaled) {
+                    const f32x4 r = c.template by<kAcross, P>(j, s.v[b], f32x4{0, 0, 0, 0});
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sum[j][b][e] = fmaf(r[e], s.factor[b][kAcross ? e : 0], sum[j][b][e]);
+                } else {
+                    sum[j][b] = c.template by<kAcross, P>(j, s.v[b], sum[j][b]);
+                }
+            }
     };
     constexpr int kStep = kAdaptWaves * 32;
     int32_t t0 = wave * 32;
@@ -869,38 +967,59 @@ void with_groups(int32_t rank, F f) {
         f(std::integral_constant<int, 8>{});
 }
 
+// f(integral_constant<rank blocks>, integral_constant<16 rows of a workgroup>)
+template <typename F>
+void with_rows(int32_t rank, int32_t subs, F f) {
+    with_ranks(rank, [&](auto rb) {
+        if (subs == 1)
+            f(rb, std::integral_constant<int, 4>{});
+        else if (subs == 2)
+            f(rb, std::integral_constant<int, 2>{});
+        else
+            f(rb, std::integral_constant<int, 1>{});
+    });
+}
+
 template <typename T>
 void Adapt<T>::shrink(const ShrinkArgs &a, int64_t tiles, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(a.splits),
-                    static_cast<unsigned>(adapt_slabs(a.rank)));
-    with_ranks(a.rank, [&](auto rb) {
-        k_adapt_shrink<T, decltype(rb)::value><<<grid, kAdaptThreads, 0, s>>>(a);
+    // tiles that find their rows have 16 at most
+    const bool direct = !a.rows.tiles;
+    const dim3 grid(static_cast<unsigned>(tiles * (direct ? 1 : a.subs)),
+                    static_cast<unsigned>(a.splits), static_cast<unsigned>(adapt_slabs(a.rank)));
+    with_rows(a.rank, direct ? 4 : a.subs, [&](auto rb, auto m) {
+        ShrinkArgs b = a;
+        if (direct) b.subs = 1;
+        k_adapt_shrink<T, decltype(rb)::value, decltype(m)::value>
+            <<<grid, kAdaptThreads, 0, s>>>(b);
     });
 }
 
 template <typename T>
 void Adapt<T>::shrink_both(const ShrinkArgs &a, const ShrinkArgs &across, int64_t tiles,
                            hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(a.splits + across.splits),
+    const dim3 grid(static_cast<unsigned>(tiles * a.subs),
+                    static_cast<unsigned>(a.splits + across.splits),
                     static_cast<unsigned>(adapt_slabs(a.rank)));
-    with_ranks(a.rank, [&](auto rb) {
-        k_adapt_shrink_both<T, decltype(rb)::value><<<grid, kAdaptThreads, 0, s>>>(a, across);
+    with_rows(a.rank, a.subs, [&](auto rb, auto m) {
+        k_adapt_shrink_both<T, decltype(rb)::value, decltype(m)::value>
+            <<<grid, kAdaptThreads, 0, s>>>(a, across);
     });
 }
 
 template <typename T>
 void Adapt<T>::expand(const ExpandArgs &a, bool across, bool out_fp32, int64_t tiles,
                       hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(tiles),
-                    static_cast<unsigned>((a.D - 1) / a.columns + 1));
+    constexpr int NT = 4;
+    const unsigned grid =
+        static_cast<unsigned>(tiles * ((a.D - 1) / (kAdaptWaves * 16 * NT) + 1));
     with_groups(a.rank, [&](auto groups) {
         constexpr int G = decltype(groups)::value;
         if (across)  // dx, of the inputs' type
-            k_adapt_expand<T, T, G, true><<<grid, kAdaptThreads, 0, s>>>(a);
+            k_adapt_expand<T, T, G, NT, true><<<grid, kAdaptThreads, 0, s>>>(a);
         else if (out_fp32)
-            k_adapt_expand<T, float, G, false><<<grid, kAdaptThreads, 0, s>>>(a);
+            k_adapt_expand<T, float, G, NT, false><<<grid, kAdaptThreads, 0, s>>>(a);
         else
-            k_adapt_expand<T, T, G, false><<<grid, kAdaptThreads, 0, s>>>(a);
+            k_adapt_expand<T, T, G, NT, false><<<grid, kAdaptThreads, 0, s>>>(a);
     });
 }
 

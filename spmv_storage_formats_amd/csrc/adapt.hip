@@ -33,6 +33,22 @@ __device__ inline int32_t adapter_key(const void *ids, int32_t t, int32_t adapte
 __device__ inline void prefix(int32_t *v, int32_t m, int32_t *wsum) {
     constexpr int E = (kKeys + kGroupThreads - 1) / kGroupThreads;
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    if (m <= kWave) {  // one wave's work
+        __syncthreads();
+        if (wave == 0) {
+            const int32_t own = lane < m ? v[lane] : 0;
+            int32_t incl = own;
+#pragma unroll
+            for (int o = 1; o < kWave; o <<= 1) {
+                const int32_t t = __shfl_up(incl, o);
+                if (lane >= o) incl += t;
+            }
+            if (lane < m) v[lane] = incl - own;
+            if (lane == m - 1) v[m] = incl;
+        }
+        __syncthreads();
+        return;
+    }
     int32_t own[E], sum = 0;
     __syncthreads();
 #pragma unroll
@@ -68,26 +84,36 @@ template <typename I>
 __global__ __launch_bounds__(kGroupThreads) void k_adapt_group(GroupArgs a) {
     __shared__ int32_t s_count[kKeys + 1], s_start[kKeys + 1], s_place[kKeys + 1],
         s_first[kKeys + 1];
-    __shared__ int32_t s_wsum[kGroupThreads / kWave];
+    __shared__ int32_t s_wsum[kGroupThreads / kWave], s_waves[kGroupThreads / kWave][kWave];
     const int lane = threadIdx.x % kWave, tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int32_t keys = a.adapters + 1;
     const int32_t own = static_cast<int32_t>(blockIdx.x) * a.block;
     for (int k = tid; k < keys; k += kGroupThreads) s_count[k] = s_place[k] = 0;
     __syncthreads();
-    for (int32_t at = wave * kWave; at < a.n; at += kGroupThreads) {
-        const int32_t t = at + lane;
-        const int32_t key = t < a.n ? adapter_key<I>(a.ids, t, a.adapters) : -1;
-        const bool early = at < own;  // whole waves lie before the block or not
-        const int32_t first = __builtin_amdgcn_readfirstlane(key);
-        if (__all(key == first)) {    // a request's rows lie together
-            if (lane == 0) {
-                atomicAdd(&s_count[first], kWave);
-                if (early) atomicAdd(&s_place[first], kWave);
+    constexpr int kAhead = 8;  // loads in flight
+    for (int32_t at0 = wave * kWave; at0 < a.n; at0 += kAhead * kGroupThreads) {
+        int32_t keys_at[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int32_t t = at0 + u * kGroupThreads + lane;
+            keys_at[u] = t < a.n ? adapter_key<I>(a.ids, t, a.adapters) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int32_t at = at0 + u * kGroupThreads, key = keys_at[u];
+            if (at >= a.n) continue;
+            const bool early = at < own;  // whole waves lie before the block or not
+            const int32_t first = __builtin_amdgcn_readfirstlane(key);
+            if (__all(key == first)) {    // a request's rows lie together
+                if (lane == 0) {
+                    atomicAdd(&s_count[first], kWave);
+                    if (early) atomicAdd(&s_place[first], kWave);
+                }
+            } else if (key >= 0) {
+                atomicAdd(&s_count[key], 1);
+                if (early) atomicAdd(&s_place[key], 1);
             }
-        } else if (key >= 0) {
-            atomicAdd(&s_count[key], 1);
-            if (early) atomicAdd(&s_place[key], 1);
         }
     }
     __syncthreads();
@@ -110,20 +136,40 @@ __global__ __launch_bounds__(kGroupThreads) void k_adapt_group(GroupArgs a) {
         }
         const int rank = __popcll(peers & below);
         int32_t to = 0;
-        for (int w = 0; w < kGroupThreads / kWave; ++w) {
-            if (w == wave && there) {
-                to = s_place[key] + rank;
-                // every lane of a key reads before its first one writes
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                __builtin_amdgcn_wave_barrier();
-                if (rank == 0) s_place[key] += __popcll(peers);
-            }
+        if (keys <= kWave) {  // every wave's counts by key, added up
             __syncthreads();
+            s_waves[tid / kWave][lane] = 0;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (there && rank == 0) s_waves[wave][key] = __popcll(peers);
+            __syncthreads();
+            to = s_place[key] + rank;
+#pragma unroll
+            for (int w = 0; w < kGroupThreads / kWave; ++w)
+                to += w < wave ? s_waves[w][key] : 0;
+            __syncthreads();
+            if (tid < keys) {
+                int32_t all = 0;
+#pragma unroll
+                for (int w = 0; w < kGroupThreads / kWave; ++w) all += s_waves[w][tid];
+                s_place[tid] += all;
+            }
+        } else {              // wave after wave
+            for (int w = 0; w < kGroupThreads / kWave; ++w) {
+                if (w == wave && there) {
+                    to = s_place[key] + rank;
+                    // every lane of a key reads before its first one writes
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
+                    if (rank == 0) s_place[key] += __popcll(peers);
+                }
+                __syncthreads();
+            }
         }
         if (there) a.order[to] = t;
     }
     // the lists, shared out over the workgroups
-    auto list = [&](AdaptTile *out, int32_t most, int32_t length) {
+    auto list = [&](AdaptTile *out, int32_t most, int32_t length, const int32_t *tiles) {
         for (int32_t j = static_cast<int32_t>(blockIdx.x) * kGroupThreads + tid; j < most;
              j += static_cast<int32_t>(gridDim.x) * kGroupThreads) {
             AdaptTile tile{-1, 0, 0, 0};
@@ -135,7 +181,8 @@ __global__ __launch_bounds__(kGroupThreads) void k_adapt_group(GroupArgs a) {
                 }
                 const int32_t k = (j - s_first[lo]) * length;
                 const int32_t left = s_count[lo] - k;
-                tile = {lo, s_start[lo] + k, left < length ? left : length, 0};
+                tile = {lo, s_start[lo] + k, left < length ? left : length,
+                        tiles ? tiles[lo] + k / kAdaptTile : j};
             }
             out[j] = tile;
         }
@@ -143,29 +190,33 @@ __global__ __launch_bounds__(kGroupThreads) void k_adapt_group(GroupArgs a) {
     for (int k = tid; k < keys; k += kGroupThreads)
         s_first[k] = (s_count[k] + kAdaptTile - 1) / kAdaptTile;
     prefix(s_first, keys, s_wsum);
-    list(a.tiles, a.most_tiles, kAdaptTile);
+    list(a.tiles, a.most_tiles, kAdaptTile, nullptr);
     if (!a.chunks) return;
+    // the rows are placed: their places give way to the first tiles
+    for (int k = tid; k < keys; k += kGroupThreads) s_place[k] = s_first[k];
     __syncthreads();
     // rows without an adapter have no share in the matrices
     for (int k = tid; k < keys; k += kGroupThreads)
         s_first[k] = k == a.adapters ? 0 : a.single ? 1 : (s_count[k] + a.chunk - 1) / a.chunk;
     prefix(s_first, keys, s_wsum);
-    list(a.chunks, a.most_chunks, a.chunk);
+    list(a.chunks, a.most_chunks, a.chunk, s_place);
     if (blockIdx.x == 0)
         for (int k = tid; k < keys; k += kGroupThreads) a.chunk_start[k] = s_first[k];
 }
 
 // Sums of the splits, scaled, rank by rank: what the matrices' gradients read.
 // A workgroup takes a tile and 16 ranks, a thread four of a row.
-template <bool kParts>
+template <typename T>
 __global__ __launch_bounds__(kAdaptThreads) void k_adapt_finish(FinishArgs a, FinishArgs b) {
     const FinishArgs &f = blockIdx.y == 0 ? a : b;
     const AdaptTile tile = f.tiles[blockIdx.x];
+    if (tile.adapter < 0 || tile.adapter >= f.adapters) return;
     const int32_t row = static_cast<int32_t>(threadIdx.x) / 4;
-    if (tile.adapter < 0 || tile.adapter >= f.adapters || row >= tile.count) return;
-    const int32_t at = tile.first + row;
-    const int32_t k = static_cast<int32_t>(blockIdx.z) * 16 + static_cast<int32_t>(threadIdx.x) % 4 * 4;
+    const int32_t k =
+        static_cast<int32_t>(blockIdx.z) * 16 + static_cast<int32_t>(threadIdx.x) % 4 * 4;
     const float scale = f.scales ? f.scales[tile.adapter] : 1.f;
+    const bool there = row < tile.count;
+    const int32_t at = tile.first + (there ? row : 0);
     const float *p = f.sums + static_cast<int64_t>(f.order[at]) * f.width + k;
     float v[4];
     load_piece<4>(p, v);
@@ -176,12 +227,49 @@ __global__ __launch_bounds__(kAdaptThreads) void k_adapt_finish(FinishArgs a, Fi
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] += more[i];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = there && k + i < f.rank ? v[i] * scale : 0.f;
+    Power power[4] = {{1.f, 1.f}, {1.f, 1.f}, {1.f, 1.f}, {1.f, 1.f}};
+    if constexpr (std::is_same<T, f16>::value) {
+        // the largest of the tile's rows, by rank
+        __shared__ float s_most[kAdaptWaves][16];
+        const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+        float most[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            most[i] = fabsf(v[i]);
+            // a NaN must not hide what is beside it: its row is no number anyway
+#pragma unroll
+            for (int j = 4; j < kWave; j *= 2) most[i] = fmaxf(most[i], __shfl_xor(most[i], j));
+            if (lane < 4) s_most[wave][lane * 4 + i] = most[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float m = 0.f;
+#pragma unroll
+            for (int w = 0; w < kAdaptWaves; ++w)
+                m = fmaxf(m, s_most[w][threadIdx.x % 4 * 4 + i]);
+            power[i] = spmv::power(m);
+        }
+        if (row == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f.factors[static_cast<int64_t>(blockIdx.x) * f.width + k + i] = power[i].back;
+        }
+    }
+    if (!there) return;
     const int64_t part = static_cast<int64_t>(f.stride) * f.width;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t to = static_cast<int64_t>(k + i) * f.stride + at;
-        float s = k + i < f.rank ? v[i] * scale : 0.f;
-        if constexpr (kParts) {
+        float s = v[i] * power[i].up;
+        if constexpr (std::is_same<T, f16>::value) {
+            f16 *out = static_cast<f16 *>(f.out) + to;
+            const f16 lead = static_cast<f16>(s);
+            out[0] = lead;
+            out[part] = rest_of(s, lead);
+        } else if constexpr (std::is_same<T, bf16>::value) {
             bf16 *out = static_cast<bf16 *>(f.out) + to;
 #pragma unroll
             for (int q = 0; q < 3; ++q) {
@@ -246,16 +334,19 @@ size_t round16(size_t b) { return (b + 15) / 16 * 16; }
 // Sizes that follow from the arguments, and the workspace's parts.
 struct Plan {
     bool single;  // no adapter has more than a chunk: no join
-    int32_t width, tiles, chunk, chunks, stride;
+    int32_t width, subs, tiles, chunk, chunks, stride;
     int32_t splits_c, part_c, splits_r, part_r;
-    size_t order, tile_list, chunk_list, chunk_start, sums_c, sums_r, v_c, v_r, down, up, end;
+    size_t order, tile_list, chunk_list, chunk_start, sums_c, sums_r, v_c, v_r, factors_c, factors_r,
+        down, up, end;
 };
 
-// Parts of D columns: workgroups for the whole card, no part of less than 256.
-void split(int32_t D, int32_t tiles, int32_t *splits, int32_t *part) {
-    constexpr int32_t kGroups = 768, kUnit = kAdaptWaves * 32;
+// Parts of D columns: workgroups for the whole card, no part of less than 256
+// columns, at most 8 (every workgroup of expand adds them up).
+void split(int32_t D, int32_t groups, int32_t *splits, int32_t *part) {
+    constexpr int32_t kGroups = 1024, kUnit = kAdaptWaves * 32, kMost = 8;
     const int32_t units = std::max(1, (D + kUnit - 1) / kUnit);
-    const int32_t want = std::min(std::max(1, kGroups / std::max(1, tiles)), std::max(1, units / 2));
+    const int32_t most = std::min(kMost, std::max(1, units / 2));
+    const int32_t want = std::min(most, (kGroups - 1) / std::max(1, groups) + 1);
     const int32_t per = (units + want - 1) / want;
     *splits = (units + per - 1) / per;
     *part = per * kUnit;
@@ -268,12 +359,16 @@ Plan plan(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R, bool 
     p.width = adapt_width(rank);
     // a last tile of each adapter that has rows, and of the rows without one
     p.tiles = (n + kAdaptTile - 1) / kAdaptTile + std::min(adapters + 1, n);
-    p.chunk = std::max(kAdaptChunk, (n / 64 + 31) / 32 * 32);
+    p.chunk = std::max(kAdaptChunk, (n / 64 + kAdaptTile - 1) / kAdaptTile * kAdaptTile);
     p.single = n > 0 && n <= p.chunk;
     p.chunks = p.single ? adapters : (n + p.chunk - 1) / p.chunk + std::min(adapters, n);
     p.stride = (n + kPast + 15) / 16 * 16;
-    split(C, p.tiles, &p.splits_c, &p.part_c);
-    split(R, p.tiles, &p.splits_r, &p.part_r);
+    // few rows: 16 of a workgroup (32 of large ranks); many: 64
+    const int32_t full = (n + kAdaptTile - 1) / kAdaptTile;
+    p.subs = full >= 1024 ? 1 : rank > 32 ? 2 : 4;
+    const int32_t groups = !grad && n <= kAdaptDirect ? n : full * p.subs;
+    split(C, groups, &p.splits_c, &p.part_c);
+    split(R, groups, &p.splits_r, &p.part_r);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -293,6 +388,8 @@ Plan plan(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R, bool 
         p.sums_r = take(rows * p.splits_r);
         p.v_c = take(v);
         p.v_r = take(v);
+        p.factors_c = take(static_cast<size_t>(p.tiles) * p.width * sizeof(float));
+        p.factors_r = take(static_cast<size_t>(p.tiles) * p.width * sizeof(float));
         p.down = take(cut * C);
         p.up = take(cut * R);
     }
@@ -322,14 +419,6 @@ size_t adapt_bytes(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t
     return n == 0 ? 0 : plan(n, adapters, rank, C, R, false).end;
 }
 
-// Columns of a workgroup of expand: all workgroups together about kGroups.
-int32_t expand_columns(int32_t D, int32_t tiles) {
-    constexpr int32_t kGroups = 2048, kUnit = kAdaptWaves * kExpandColumns;
-    const int32_t units = (D - 1) / kUnit + 1;
-    const int32_t want = std::min(units, std::max(1, kGroups / tiles));
-    return (units + want - 1) / want * kUnit;
-}
-
 spmv_status adapt(const AdaptArgs &a, hipStream_t s) {
     const Plan p = plan(a.n, a.adapters, a.rank, a.C, a.R, false);
     char *ws = static_cast<char *>(a.workspace);
@@ -343,10 +432,11 @@ spmv_status adapt(const AdaptArgs &a, hipStream_t s) {
     with_float(a.dtype, [&](auto x) {
         using A = Adapt<decltype(x)>;
         if (a.adapters > 0)
-            A::shrink({rows, a.x, a.x_ld, a.down, a.C, a.rank, p.width, p.splits_c, p.part_c, sums},
+            A::shrink({rows, a.x, a.x_ld, a.down, a.C, a.rank, p.width, p.splits_c, p.part_c,
+                       p.subs, sums},
                       tiles, s);
         A::expand({rows, sums, p.splits_c, p.width, a.scales, a.up, a.R, a.rank, a.base, a.base_ld,
-                   a.out, a.out_ld, expand_columns(a.R, tiles)},
+                   a.out, a.out_ld},
                   false, a.out_dtype == SPMV_FP32, tiles, s);
     });
     SPMV_HIP(hipGetLastError());
@@ -372,27 +462,24 @@ spmv_status adapt_grad(const AdaptGradArgs &a, hipStream_t s) {
         const bool any = a.adapters > 0 && a.n > 0;
         const RowsArgs rows{a.ids, a.id_dtype, a.n, a.adapters, order, tiles};
         const ShrinkArgs h{rows, a.x, a.x_ld, a.down, a.C, a.rank, p.width, p.splits_c, p.part_c,
-                           floats(p.sums_c)};
+                           p.subs, floats(p.sums_c)};
         const ShrinkArgs g{rows, a.grad, a.grad_ld, a.up, a.R, a.rank, p.width, p.splits_r,
-                           p.part_r, floats(p.sums_r)};
+                           p.part_r, p.subs, floats(p.sums_r)};
         if (any) A::shrink_both(h, g, p.tiles, s);
         if (a.dx && a.n > 0 && a.C > 0)
             A::expand({rows, g.sums, g.splits, p.width, a.scales, a.down, a.C, a.rank, a.base,
-                       a.base_ld, a.dx, a.dx_ld, expand_columns(a.C, p.tiles)},
+                       a.base_ld, a.dx, a.dx_ld},
                       true, false, p.tiles, s);
         if (!any || !weights) return;
         const FinishArgs fh{h.sums, h.splits, p.width, a.n, a.rank, a.adapters, a.scales, order,
-                            tiles, ws + p.v_c, p.stride};
+                            tiles, ws + p.v_c, floats(p.factors_c), p.stride};
         const FinishArgs fg{g.sums, g.splits, p.width, a.n, a.rank, a.adapters, a.scales, order,
-                            tiles, ws + p.v_r, p.stride};
+                            tiles, ws + p.v_r, floats(p.factors_r), p.stride};
         const dim3 grid(static_cast<unsigned>(p.tiles), 2, static_cast<unsigned>(p.width / 16));
-        if (a.dtype == SPMV_FP32)
-            k_adapt_finish<false><<<grid, kAdaptThreads, 0, s>>>(fh, fg);
-        else
-            k_adapt_finish<true><<<grid, kAdaptThreads, 0, s>>>(fh, fg);
+        k_adapt_finish<decltype(x)><<<grid, kAdaptThreads, 0, s>>>(fh, fg);
         auto sums = [&](const void *x, int64_t ld, const FinishArgs &f, int32_t D, size_t partial,
                         void *out) {
-            return WeightArgs{x, ld, f.out, p.stride, D, a.rank, p.width, order, chunks,
+            return WeightArgs{x, ld, f.out, f.factors, p.stride, D, a.rank, p.width, order, chunks,
                               floats(partial), p.single ? out : nullptr, a.accumulate,
                               a.w_dtype == SPMV_FP32,
                               out && D > 0 ? (D - 1) / kWeightColumns + 1 : 0};
