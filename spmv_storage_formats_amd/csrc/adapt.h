@@ -556,13 +556,25 @@ __global__ __launch_bounds__(kAdaptThreads) void k_adapt_expand(ExpandArgs a) {
         (16 * NT);
     const int64_t col = first + i16 * NT;
     const bool whole = first + 16 * NT <= a.D;
-    auto load_base = [&](int u, Vec<B, NT> (&o)[4]) {
+    // rows past the last: another one's, not used
+    auto load_base = [&](int u, Vec<B, NT> (&o)[4], auto all) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int32_t k = u * 16 + q * 4 + e;
             const B *p = static_cast<const B *>(a.base) +
                          s_rows.row[k < count ? k : 0] * a.base_ld + col;
-            o[e] = whole ? load_all<B, NT>(p) : load_some<B, NT>(p, a.D - col);
+            o[e] = decltype(all)::value ? load_all<B, NT>(p) : load_some<B, NT>(p, a.D - col);
+        }
+    };
+    constexpr int kOpen = kTiles == 4 ? 4 : 1;  // 16 rows each, their base in registers
+    auto load_bases = [&](int u0, Vec<B, NT> (&o)[kOpen][4]) {
+        if (!a.base) return;
+        if (whole) {
+#pragma unroll
+            for (int u = 0; u < kOpen; ++u) load_base(u0 + u, o[u], std::true_type{});
+        } else {
+#pragma unroll
+            for (int u = 0; u < kOpen; ++u) load_base(u0 + u, o[u], std::false_type{});
         }
     };
     auto store = [&](int u, int e, Vec<B, NT> v) {
@@ -578,11 +590,13 @@ __global__ __launch_bounds__(kAdaptThreads) void k_adapt_expand(ExpandArgs a) {
         }
     };
     if (!adapted) {  // hands the base on
-        for (int u = 0; u * 16 < count; ++u) {
-            Vec<B, NT> o[4] = {};
-            if (a.base) load_base(u, o);
+        for (int u0 = 0; u0 * 16 < count; u0 += kOpen) {
+            Vec<B, NT> o[kOpen][4] = {};
+            load_bases(u0, o);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) store(u, e, o[e]);
+            for (int u = 0; u < kOpen; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) store(u0 + u, e, o[u][e]);
         }
         return;
     }
@@ -653,6 +667,8 @@ __global__ __launch_bounds__(kAdaptThreads) void k_adapt_expand(ExpandArgs a) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) load_matrix(g, m[g]);
     }
+    Vec<B, NT> o[kOpen][4];
+    load_bases(0, o);
     const float scale = a.scales ? a.scales[adapter] : 1.f;
     auto stage = [&](int u, int slot) {
         const int32_t t = s_rows.row[u * 16 + i16 < count ? u * 16 + i16 : count - 1];
@@ -703,14 +719,16 @@ __global__ __launch_bounds__(kAdaptThreads) void k_adapt_expand(ExpandArgs a) {
                 for (int g = 0; g < NG; ++g) mask_matrix(g, m[g]);
             }
         }
-#pragma unroll 1
-        for (int u = u0; u < u0 + kTiles && u * 16 < count; ++u) {
-            Vec<B, NT> o[4];
-            if (a.base) load_base(u, o);
+#pragma unroll
+        for (int slot = 0; slot < kTiles; ++slot) {
+            const int u = u0 + slot;
+            if (u * 16 >= count) continue;
+            if (kOpen == 1 && u > 0) load_bases(u, o);
+            auto &own = o[slot % kOpen];
             H h;
             u32x4 words[kWords];
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) words[i] = s_h[u - u0][i][lane];
+            for (int i = 0; i < kWords; ++i) words[i] = s_h[slot][i][lane];
             __builtin_memcpy(&h, words, sizeof(words));
             f32x4 sum[NT];
 #pragma unroll
@@ -731,7 +749,7 @@ __global__ __launch_bounds__(kAdaptThreads) void k_adapt_expand(ExpandArgs a) {
                 Vec<float, NT> v;
 #pragma unroll
                 for (int j = 0; j < NT; ++j) v[j] = sum[j][e] * back;
-                if (a.base) v += __builtin_convertvector(o[e], Vec<float, NT>);
+                if (a.base) v += __builtin_convertvector(own[e], Vec<float, NT>);
                 store(u, e, __builtin_convertvector(v, Vec<B, NT>));
             }
         }
