@@ -27,7 +27,6 @@
 namespace spmv {
 
 constexpr int kAdaptTile = 64;     // rows of a tile, at most
-constexpr int kAdaptChunk = 512;   // rows of a chunk, at most
 constexpr int kAdaptThreads = 256;
 constexpr int kAdaptWaves = kAdaptThreads / kWave;
 
@@ -121,6 +120,7 @@ inline int32_t adapt_width(int32_t rank) {
 }
 // Ranks of a workgroup of shrink and weights; more are further workgroups.
 inline int32_t adapt_slabs(int32_t rank) { return (rank + 63) / 64; }
+constexpr int32_t kShrinkColumns = kAdaptWaves * 64;     // of a workgroup's step
 constexpr int32_t kWeightColumns = 128;                  // of a workgroup
 
 // bf16 parts of a number: its upper 16 bits, the next ones of the rest, the rest.
@@ -245,7 +245,7 @@ __device__ inline int32_t find_rows(const RowsArgs &a, int32_t number, RowsShare
 // ------------------------------------------------------------------- shrink
 
 // A workgroup takes a tile, a part of the columns and up to 64 ranks; its waves
-// take every fourth 32 columns and add up in LDS.  M: row tiles of 16 that the
+// take every fourth 64 columns and add up in LDS.  M: row tiles of 16 that the
 // tile fills.
 template <typename T, int RB, bool kAcross, int M>
 __device__ inline void shrink_rows(const ShrinkArgs &a, int32_t adapter, int32_t count,
@@ -272,57 +272,70 @@ __device__ inline void shrink_rows(const ShrinkArgs &a, int32_t adapter, int32_t
         const int32_t row = k < a.rank ? k : a.rank - 1;
         wp[b] = w + (kAcross ? row : static_cast<int64_t>(row) * a.D);
     }
+    // 64 columns, 16 of a lane: neighbouring lanes read a row's 128 bytes
     struct Step {
-        Vec<T, 8> x[M], m[RB];
+        Vec<T, 8> x[M][2], m[RB][2];
     };
     auto load = [&](int64_t c, Step &s) {
-        const int64_t at = c + q * 8;
-#pragma unroll
-        for (int u = 0; u < M; ++u) s.x[u] = load_all<T, 8>(xp[u] + at);
-#pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            if constexpr (kAcross) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s.m[b][e] = wp[b][(at + e) * a.rank];
-            } else {
-                s.m[b] = load_all<T, 8>(wp[b] + at);
-            }
-        }
-    };
-    auto add = [&](const Step &s) {
+        const int64_t at = c + q * 16;
 #pragma unroll
         for (int u = 0; u < M; ++u)
 #pragma unroll
-            for (int b = 0; b < RB; ++b) sum[u][b] = multiply(s.x[u], s.m[b], sum[u][b]);
+            for (int h = 0; h < 2; ++h) s.x[u][h] = load_all<T, 8>(xp[u] + at + h * 8);
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (kAcross) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        s.m[b][h][e] = wp[b][(at + h * 8 + e) * a.rank];
+                } else {
+                    s.m[b][h] = load_all<T, 8>(wp[b] + at + h * 8);
+                }
+            }
     };
-    constexpr int kStep = kAdaptWaves * 32;
+    auto add = [&](const Step &s) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int u = 0; u < M; ++u)
+#pragma unroll
+                for (int b = 0; b < RB; ++b)
+                    sum[u][b] = multiply(s.x[u][h], s.m[b][h], sum[u][b]);
+    };
+    constexpr int kStep = kShrinkColumns;
     const int64_t from = static_cast<int64_t>(split) * a.part;
     const int64_t to = from + a.part < a.D ? from + a.part : a.D;
-    int64_t c = from + wave * 32;
-    if (c + 32 <= to) {
+    int64_t c = from + wave * 64;
+    if (c + 64 <= to) {
         // The next columns are loaded before these are multiplied; no branch
         // around a load: the last ones are loaded again.
         Step cur, nxt;
         load(c, cur);
-        for (; c + 32 <= to; c += kStep) {
-            load(c + kStep + 32 <= to ? c + kStep : c, nxt);
+        for (; c + 64 <= to; c += kStep) {
+            load(c + kStep + 64 <= to ? c + kStep : c, nxt);
             add(cur);
             cur = nxt;
         }
     }
     if (c < to) {
-        const int64_t at = c + q * 8, there = to - at;
         Step s;
 #pragma unroll
-        for (int u = 0; u < M; ++u) s.x[u] = load_some<T, 8>(xp[u] + at, there);
+        for (int h = 0; h < 2; ++h) {
+            const int64_t at = c + q * 16 + h * 8, there = to - at;
 #pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            if constexpr (kAcross) {
+            for (int u = 0; u < M; ++u) s.x[u][h] = load_some<T, 8>(xp[u] + at, there);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    s.m[b][e] = e < there ? wp[b][(at + e) * a.rank] : static_cast<T>(0.f);
-            } else {
-                s.m[b] = load_some<T, 8>(wp[b] + at, there);
+            for (int b = 0; b < RB; ++b) {
+                if constexpr (kAcross) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        s.m[b][h][e] =
+                            e < there ? wp[b][(at + e) * a.rank] : static_cast<T>(0.f);
+                } else {
+                    s.m[b][h] = load_some<T, 8>(wp[b] + at, there);
+                }
             }
         }
         add(s);
@@ -531,7 +544,8 @@ struct Numbers<float, G, kAll> {
 // Column tile j holds columns i16 * NT + j, so that a lane's results of one row
 // are neighbours, and those of 16 lanes are 128 bytes (fp32: 256) or more.
 template <typename T, typename B, int G, int NT, bool kAcross>
-__global__ __launch_bounds__(kAdaptThreads) void k_adapt_expand(ExpandArgs a) {
+__global__ __launch_bounds__(kAdaptThreads, G == 2 && sizeof(T) == 2 ? 3 : 1) void
+k_adapt_expand(ExpandArgs a) {
     using H = Numbers<T, G, sizeof(B) == 4>;
     using M = Vec<T, H::kPer>;
     constexpr int K = H::kPer, NG = H::kGroups;
@@ -870,25 +884,14 @@ __device__ inline void weight_sums(const WeightArgs &a, const AdaptTile &chunk, 
             }
     };
     constexpr int kStep = kAdaptWaves * 32;
-    int32_t t0 = wave * 32;
-    if (whole) {
-        if (t0 < chunk.count) {
-            Step cur, nxt;
-            load(t0, cur, std::true_type{});
 #pragma unroll 1
-            for (; t0 < chunk.count; t0 += kStep) {
-                load(t0 + kStep < chunk.count ? t0 + kStep : t0, nxt, std::true_type{});
-                add(cur);
-                cur = nxt;
-            }
-        }
-    } else {
-#pragma unroll 1
-        for (; t0 < chunk.count; t0 += kStep) {
-            Step s;
+    for (int32_t t0 = wave * 32; t0 < chunk.count; t0 += kStep) {
+        Step s;
+        if (whole)
+            load(t0, s, std::true_type{});
+        else
             load(t0, s, std::false_type{});
-            add(s);
-        }
+        add(s);
     }
     float *const to = a.partial + static_cast<int64_t>(blockIdx.x) * a.rank * a.D;
     auto put = [&](int64_t at, float s) {

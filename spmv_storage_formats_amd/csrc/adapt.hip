@@ -23,9 +23,7 @@ struct GroupArgs {
 };
 
 // A row's key: its adapter, or `adapters` where it names none.
-template <typename I>
-__device__ inline int32_t adapter_key(const void *ids, int32_t t, int32_t adapters) {
-    const int64_t id = static_cast<const I *>(ids)[t];
+__device__ inline int32_t key_of(int64_t id, int32_t adapters) {
     return id >= 0 && id < adapters ? static_cast<int32_t>(id) : adapters;
 }
 
@@ -91,29 +89,41 @@ __global__ __launch_bounds__(kGroupThreads) void k_adapt_group(GroupArgs a) {
     const int32_t own = static_cast<int32_t>(blockIdx.x) * a.block;
     for (int k = tid; k < keys; k += kGroupThreads) s_count[k] = s_place[k] = 0;
     __syncthreads();
-    constexpr int kAhead = 8;  // loads in flight
-    for (int32_t at0 = wave * kWave; at0 < a.n; at0 += kAhead * kGroupThreads) {
-        int32_t keys_at[kAhead];
+    // 512 rows of a wave at a time, eight neighbours of a lane
+    constexpr int E = 8;
+    for (int32_t at = wave * (kWave * E); at < a.n; at += kGroupThreads * E) {
+        const int32_t t = at + lane * E;
+        int32_t key[E];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int32_t t = at0 + u * kGroupThreads + lane;
-            keys_at[u] = t < a.n ? adapter_key<I>(a.ids, t, a.adapters) : -1;
+        for (int i = 0; i < E; ++i) key[i] = -1;
+        if (t + E <= a.n) {
+            Piece<I, E> ids;
+            __builtin_memcpy(&ids, static_cast<const I *>(a.ids) + t, sizeof(ids));
+#pragma unroll
+            for (int i = 0; i < E; ++i) key[i] = key_of(ids.v[i], a.adapters);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (t + i < a.n)
+                    key[i] = key_of(static_cast<const I *>(a.ids)[t + i], a.adapters);
+        }
+        const bool early = at < own;  // blocks are whole multiples of these rows
+        const int32_t first = __builtin_amdgcn_readfirstlane(key[0]);
+        bool one = true;
+#pragma unroll
+        for (int i = 1; i < E; ++i) one = one && key[i] == key[0];
+        if (__all(one && key[0] == first)) {  // a request's rows lie together
+            if (lane == 0) {
+                atomicAdd(&s_count[first], kWave * E);
+                if (early) atomicAdd(&s_place[first], kWave * E);
+            }
+            continue;
         }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int32_t at = at0 + u * kGroupThreads, key = keys_at[u];
-            if (at >= a.n) continue;
-            const bool early = at < own;  // whole waves lie before the block or not
-            const int32_t first = __builtin_amdgcn_readfirstlane(key);
-            if (__all(key == first)) {    // a request's rows lie together
-                if (lane == 0) {
-                    atomicAdd(&s_count[first], kWave);
-                    if (early) atomicAdd(&s_place[first], kWave);
-                }
-            } else if (key >= 0) {
-                atomicAdd(&s_count[key], 1);
-                if (early) atomicAdd(&s_place[key], 1);
-            }
+        for (int i = 0; i < E; ++i) {
+            if (key[i] < 0 || (one && i > 0)) continue;
+            atomicAdd(&s_count[key[i]], one ? E : 1);
+            if (early) atomicAdd(&s_place[key[i]], one ? E : 1);
         }
     }
     __syncthreads();
@@ -127,7 +137,7 @@ __global__ __launch_bounds__(kGroupThreads) void k_adapt_group(GroupArgs a) {
     for (int32_t at = own; at < end; at += kGroupThreads) {
         const int32_t t = at + tid;
         const bool there = t < end;
-        const int32_t key = there ? adapter_key<I>(a.ids, t, a.adapters) : 0;
+        const int32_t key = there ? key_of(static_cast<const I *>(a.ids)[t], a.adapters) : 0;
         unsigned long long peers = __ballot(there);
         for (int b = 0; (keys - 1) >> b; ++b) {
             const bool bit = (key >> b) & 1;
@@ -343,10 +353,9 @@ struct Plan {
 // Parts of D columns: workgroups for the whole card, no part of less than 256
 // columns, at most 8 (every workgroup of expand adds them up).
 void split(int32_t D, int32_t groups, int32_t *splits, int32_t *part) {
-    constexpr int32_t kGroups = 1024, kUnit = kAdaptWaves * 32, kMost = 8;
+    constexpr int32_t kGroups = 1024, kUnit = kShrinkColumns, kMost = 8;
     const int32_t units = std::max(1, (D + kUnit - 1) / kUnit);
-    const int32_t most = std::min(kMost, std::max(1, units / 2));
-    const int32_t want = std::min(most, (kGroups - 1) / std::max(1, groups) + 1);
+    const int32_t want = std::min(std::min(kMost, units), (kGroups - 1) / std::max(1, groups) + 1);
     const int32_t per = (units + want - 1) / want;
     *splits = (units + per - 1) / per;
     *part = per * kUnit;
@@ -359,13 +368,16 @@ Plan plan(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R, bool 
     p.width = adapt_width(rank);
     // a last tile of each adapter that has rows, and of the rows without one
     p.tiles = (n + kAdaptTile - 1) / kAdaptTile + std::min(adapters + 1, n);
-    p.chunk = std::max(kAdaptChunk, (n / 64 + kAdaptTile - 1) / kAdaptTile * kAdaptTile);
+    // workgroups of the matrices' gradients: about 1024, of no less than 128 rows
+    const int64_t blocks = (static_cast<int64_t>(C) + R) / kWeightColumns + 2;
+    p.chunk = static_cast<int32_t>(
+        std::max<int64_t>(128, (n * blocks / 1024 + kAdaptTile - 1) / kAdaptTile * kAdaptTile));
     p.single = n > 0 && n <= p.chunk;
     p.chunks = p.single ? adapters : (n + p.chunk - 1) / p.chunk + std::min(adapters, n);
     p.stride = (n + kPast + 15) / 16 * 16;
-    // few rows: 16 of a workgroup (32 of large ranks); many: 64
+    // few rows of small ranks: 32 of a workgroup; many: 64
     const int32_t full = (n + kAdaptTile - 1) / kAdaptTile;
-    p.subs = full >= 1024 ? 1 : rank > 32 ? 2 : 4;
+    p.subs = full >= 1024 || rank > 32 ? 1 : 2;
     const int32_t groups = !grad && n <= kAdaptDirect ? n : full * p.subs;
     split(C, groups, &p.splits_c, &p.part_c);
     split(R, groups, &p.splits_r, &p.part_r);
