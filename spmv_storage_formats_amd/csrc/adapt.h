@@ -154,18 +154,6 @@ namespace {
 using f32x4 = float __attribute__((ext_vector_type(4)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
-// Vectors in registers, and in memory at the alignment of their elements: the
-// compiler takes such an access apart if it is one of a struct or an array.
-template <typename T, int E>
-struct VecOf {
-    typedef T type __attribute__((ext_vector_type(E)));
-    typedef T loose __attribute__((ext_vector_type(E), aligned(sizeof(T)), may_alias));
-};
-template <typename T, int E>
-using Vec = typename VecOf<T, E>::type;
-template <typename T, int E>
-using Loose = typename VecOf<T, E>::loose;
-
 // Operands: the lane's row (or column) is lane % 16, its summed indexes eight
 // neighbours from 8 * (lane / 16).  Results: column lane % 16, rows
 // 4 * (lane / 16) + 0..3.
@@ -180,21 +168,6 @@ __device__ inline f32x4 multiply(const Vec<float, 8> &a, const Vec<float, 8> &b,
     for (int i = 0; i < 8; ++i)
         c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
     return c;
-}
-
-// E neighbours, the first `there` of them; the others are 0.
-template <typename T, int E>
-__device__ inline Vec<T, E> load_some(const T *p, int64_t there) {
-    if (there >= E) return *reinterpret_cast<const Loose<T, E> *>(p);
-    Vec<T, E> o = {};
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-        if (i < there) o[i] = p[i];
-    return o;
-}
-template <typename T, int E>
-__device__ inline Vec<T, E> load_all(const T *p) {
-    return *reinterpret_cast<const Loose<T, E> *>(p);
 }
 
 // --------------------------------------------------------------------- rows

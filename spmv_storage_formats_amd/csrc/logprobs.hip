@@ -40,9 +40,6 @@ constexpr float kFirst = -3.402823466e38f;  // below every finite logit, or equa
 template <typename T>
 constexpr int kPer = sizeof(T) == 4 ? 4 : 8;   // elements of a 16-byte piece
 
-template <int N>
-using Whole = std::integral_constant<int, N>;
-
 // A row's statistics: largest logit, sum of 2^y beside one largest logit (-1:
 // nothing but masked logits), sum of 2^y y.
 struct Stat {
@@ -81,28 +78,71 @@ __device__ inline u64 larger(u64 a, u64 b, bool larger_one) {
     return (a > b) == larger_one ? a : b;
 }
 
+// Lane ^ J's key.  Within 16 lanes without LDS: exchanges in fours and halves
+// of eight, rotations of 16.
+constexpr int kDppQuadXor3 = 0x1B;   // quad_perm [3,2,1,0]
+constexpr int kDppRowRotate8 = 0x128;
+template <int kControl>
+__device__ inline u64 dpp(u64 k) {
+    const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(k), kControl, 0xF, 0xF, false);
+    const int hi =
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(k >> 32), kControl, 0xF, 0xF, false);
+    return (static_cast<u64>(static_cast<uint32_t>(hi)) << 32) | static_cast<uint32_t>(lo);
+}
+template <int J>
+__device__ inline u64 across(u64 k) {
+    if constexpr (J == 1)
+        return dpp<kDppQuadXor1>(k);
+    else if constexpr (J == 2)
+        return dpp<kDppQuadXor2>(k);
+    else if constexpr (J == 4)
+        return dpp<kDppRowHalfMirror>(dpp<kDppQuadXor3>(k));
+    else if constexpr (J == 8)
+        return dpp<kDppRowRotate8>(k);
+    else
+        return __shfl_xor(k, J);
+}
+
+// Keys J lanes apart put in order, J, J / 2, ..., 1; `size`: lanes of a run.
+template <int J>
+__device__ inline u64 exchange(u64 k, int lane, int size) {
+    k = larger(k, across<J>(k), ((lane & J) == 0) == ((lane & size) == 0));
+    if constexpr (J > 1) k = exchange<J / 2>(k, lane, size);
+    return k;
+}
+
 // The wave's 64 keys in falling order, lane 0 the largest (bitonic).
 __device__ inline u64 sort_wave(u64 k, int lane) {
-#pragma unroll
-    for (int size = 2; size <= kWave; size *= 2)
-#pragma unroll
-        for (int j = size / 2; j >= 1; j /= 2) {
-            const u64 other = __shfl_xor(k, j);
-            k = larger(k, other, ((lane & j) == 0) == ((lane & size) == 0));
-        }
-    return k;
+    k = exchange<1>(k, lane, 2);
+    k = exchange<2>(k, lane, 4);
+    k = exchange<4>(k, lane, 8);
+    k = exchange<8>(k, lane, 16);
+    k = exchange<16>(k, lane, 32);
+    return exchange<32>(k, lane, 64);
 }
 
 // The 64 largest of two lists in falling order, in falling order.
 __device__ inline u64 merge_wave(u64 a, u64 b, int lane) {
     const u64 back = __shfl(b, kWave - 1 - lane);
-    u64 k = a > back ? a : back;
+    return exchange<32>(a > back ? a : back, lane, 64);
+}
+
+// The k-th largest of the wave's keys that are not 0; 0 if there are fewer.
+__device__ inline u64 kth_wave(u64 key, int k) {
+    const uint32_t lo = static_cast<uint32_t>(key), hi = static_cast<uint32_t>(key >> 32);
+    int before = 0;
 #pragma unroll
-    for (int j = kWave / 2; j >= 1; j /= 2) {
-        const u64 other = __shfl_xor(k, j);
-        k = larger(k, other, (lane & j) == 0);
+    for (int l = 0; l < kWave; ++l) {
+        const u64 other =
+            (static_cast<u64>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, l))) << 32) |
+            static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, l));
+        before += other > key;
     }
-    return k;
+    const u64 who = __ballot(key != 0 && before == k - 1);  // keys differ: one lane or none
+    if (!who) return 0;
+    const int at = __builtin_ctzll(who);
+    return (static_cast<u64>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, at))) << 32) |
+           static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, at));
 }
 
 // The 64 largest of the waves' lists, in wave 0.  Begins and ends with a barrier.
@@ -172,9 +212,25 @@ __device__ inline void finish(const LogprobsArgs &a, int64_t t, Stat st, u64 bes
     }
 }
 
+// E elements of a part from column `at`; those behind its end are masked.
+template <typename T, int E>
+__device__ inline void load_part(const T *row, int32_t at, int32_t count, float *v) {
+    Vec<T, E> o;
+    if (at + E <= count) {
+        o = load_all<T, E>(row + at);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            o[i] = at + i < count ? row[at + i] : static_cast<T>(-__builtin_huge_valf());
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = static_cast<float>(o[i]);
+}
+
 // A workgroup takes one part of a row; with one part per row it writes the
-// row's results, otherwise the part's, which k_join puts together.
-template <typename T, typename I, bool kTop>
+// row's results, otherwise the part's, which k_join puts together.  kShort: the
+// part is no longer than kFlight pieces of each thread and stays in registers.
+template <typename T, typename I, bool kTop, bool kShort>
 __global__ __launch_bounds__(kThreads) void k_logprobs(Place p) {
     constexpr int E = kPer<T>;
     constexpr int kStep = kThreads * E;
@@ -182,7 +238,8 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(Place p) {
     __shared__ Stat s_stat[kWaves];
     __shared__ u64 s_list[kTop ? kWaves : 1][kWave];
     __shared__ u64 s_found[kTop ? kWaves : 1][kWave * (E + 1)];
-    __shared__ u64 s_bound;
+    __shared__ int s_again[kTop && !kShort ? kWaves : 1][kWave];
+    __shared__ u64 s_bound[kWaves];
     const int lane = threadIdx.x % kWave, tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const float c = a.scale * kLog2e;
@@ -194,12 +251,11 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(Place p) {
         const T *row = static_cast<const T *>(a.logits) + t * a.ld + first;
         float m = kFirst, s = 0.f, w = 0.f;
         int32_t last = -1;  // last column of the piece that holds the first maximum
-        // `many` pieces of E, kStep apart, the first at column `at`
-        auto take = [&](const float *v, auto many, int32_t at) {
-            constexpr int M = decltype(many)::value;
-            float pm[M], cm;
+        // kFlight pieces of E, kStep apart, the first at column `at`
+        auto take = [&](const float *v, int32_t at) {
+            float pm[kFlight], cm;
 #pragma unroll
-            for (int u = 0; u < M; ++u) {
+            for (int u = 0; u < kFlight; ++u) {
                 pm[u] = v[u * E];
 #pragma unroll
                 for (int i = 1; i < E; ++i) pm[u] = fmaxf(pm[u], v[u * E + i]);
@@ -211,89 +267,105 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(Place p) {
                 w = f * (w + d * s);
                 s *= f;
                 m = cm;
-                if constexpr (kTop) {
 #pragma unroll
-                    for (int u = M - 1; u >= 0; --u)
-                        if (pm[u] == cm) last = at + u * kStep + E - 1;
-                }
+                for (int u = kFlight - 1; u >= 0; --u)
+                    if (pm[u] == cm) last = at + u * kStep + E - 1;
             }
 #pragma unroll
-            for (int i = 0; i < M * E; ++i) {
+            for (int i = 0; i < kFlight * E; ++i) {
                 const float y = (v[i] - m) * c;
                 const float e = __builtin_amdgcn_exp2f(y);
                 s += e;
                 w += e * fmaxf(y, kLowest);
             }
         };
+        float v[kFlight * E];
         int32_t at = tid * E;
-        const int32_t full = count - count % (kFlight * kStep);
-        for (; at < full; at += kFlight * kStep) {
-            float v[kFlight * E];
+        if constexpr (!kShort) {
+            const int32_t full = count - count % (kFlight * kStep);
+            for (; at < full; at += kFlight * kStep) {
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u) load_piece<E>(row + at + u * kStep, v + u * E);
-            take(v, Whole<kFlight>{}, at);
-        }
-        for (; at < count; at += kStep) {
-            float v[E];
+                for (int u = 0; u < kFlight; ++u) {
+                    const Vec<T, E> o = load_all<T, E>(row + at + u * kStep);
 #pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = -__builtin_huge_valf();
-            if (at + E <= count) {
-                load_piece<E>(row + at, v);
-            } else {
-#pragma unroll
-                for (int i = 0; i < E; ++i)
-                    if (at + i < count) v[i] = static_cast<float>(row[at + i]);
+                    for (int i = 0; i < E; ++i) v[u * E + i] = static_cast<float>(o[i]);
+                }
+                take(v, at);
             }
-            take(v, Whole<1>{}, at);
+        }
+        if (kShort || at - tid * E < count) {
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u)
+                load_part<T, E>(row, at + u * kStep, count, v + u * E);
+            take(v, at);
         }
         Stat st = merge_lanes({m, s - 1.f, w}, c);
         u64 best = 0;
         if constexpr (kTop) {
+            // Elements that reach the best of the waves' top-th largest maxima.
             const u64 own = last >= 0 ? key(m, last) : 0;
-            const u64 sorted = merge_waves<kWaves>(sort_wave(own, lane), s_list, wave, lane);
-            if (wave == 0 && lane == a.top - 1) s_bound = sorted;
+            const u64 least = kth_wave(own, a.top);
+            if (lane == 0) s_bound[wave] = least;
             __syncthreads();
-            const u64 bound = s_bound;
+            u64 bound = s_bound[0];
+#pragma unroll
+            for (int i = 1; i < kWaves; ++i) bound = s_bound[i] > bound ? s_bound[i] : bound;
             u64 *found = s_found[wave];
             int have = 0;
-            const int pieces = (count + kStep - 1) / kStep;
             const u64 below = (1ull << lane) - 1ull;
-            u64 again = __ballot(own != 0 && own >= bound);
-            while (again) {
-                const int src = __builtin_ctzll(again);
-                again &= again - 1;
-                for (int i0 = 0; i0 < pieces; i0 += kWave) {
-                    const int64_t from = static_cast<int64_t>(i0 + lane) * kStep +
-                                         (wave * kWave + src) * E;
-                    float v[E];
+            auto look = [&](const float *x, int32_t from) {  // E elements from column `from`
 #pragma unroll
-                    for (int i = 0; i < E; ++i) v[i] = -__builtin_huge_valf();
-                    if (from + E <= count) {
-                        load_piece<E>(row + from, v);
-                    } else {
+                for (int i = 0; i < E; ++i) {
+                    const u64 k = key(x[i], from + i);
+                    const bool in = k != 0 && k >= bound;
+                    const u64 who = __ballot(in);
+                    if (in) found[have + __popcll(who & below)] = k;
+                    have += __popcll(who);
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                while (have >= kWave) {
+                    have -= kWave;
+                    best = merge_wave(best, sort_wave(found[have + lane], lane), lane);
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            };
+            const u64 again = __ballot(own != 0 && own >= bound);
+            if constexpr (kShort) {
+                if (again) {
+#pragma unroll 1
+                    for (int u = 0; u < kFlight; ++u) {
+                        float x[E];
 #pragma unroll
-                        for (int i = 0; i < E; ++i)
-                            if (from + i < count) v[i] = static_cast<float>(row[from + i]);
-                    }
+                        for (int i = 0; i < E; ++i) {
+                            x[i] = v[i];
 #pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        const u64 k = key(v[i], static_cast<int32_t>(from) + i);
-                        const bool in = k != 0 && k >= bound;
-                        const u64 who = __ballot(in);
-                        if (in) found[have + __popcll(who & below)] = k;
-                        have += __popcll(who);
+                            for (int o = 1; o < kFlight; ++o) x[i] = u == o ? v[o * E + i] : x[i];
+                        }
+                        look(x, tid * E + u * kStep);
                     }
-                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                    __builtin_amdgcn_wave_barrier();
-                    while (have >= kWave) {
-                        have -= kWave;
-                        best = merge_wave(best, sort_wave(found[have + lane], lane), lane);
-                    }
-                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                    __builtin_amdgcn_wave_barrier();
+                }
+            } else {
+                // the pieces of the threads that have such elements, 64 at a time
+                int *list = s_again[wave];
+                if ((again >> lane) & 1) list[__popcll(again & below)] = lane;
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                const int pieces = (count + kStep - 1) / kStep;
+                const int all = __popcll(again) * pieces;
+                for (int i0 = 0; i0 < all; i0 += kWave) {
+                    const int i = i0 + lane;
+                    const int32_t from = i < all ? i % pieces * kStep +
+                                                       (wave * kWave + list[i / pieces]) * E
+                                                 : count;
+                    float x[E];
+                    load_part<T, E>(row, from, count, x);
+                    look(x, from);
                 }
             }
-            if (have > 0) best = merge_wave(best, sort_wave(lane < have ? found[lane] : 0, lane), lane);
+            if (have > 0)
+                best = merge_wave(best, sort_wave(lane < have ? found[lane] : 0, lane), lane);
             best = merge_waves<kWaves>(best, s_list, wave, lane);
             // keys count from the part's first column
             if (best != 0) best -= static_cast<u64>(static_cast<uint32_t>(first));
@@ -357,41 +429,40 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(Place p) {
     }
 }
 
-// The parts of a row joined in their order.
-constexpr int kJoinWaves = 16;
-template <typename T, typename I, bool kTop>
-__global__ __launch_bounds__(kJoinWaves *kWave) void k_join(Place p) {
+// The parts of a row joined in their order, by W waves.
+template <typename T, typename I, int W>
+__global__ __launch_bounds__(W *kWave) void k_join(Place p) {
     const LogprobsArgs &a = p.a;
-    __shared__ u64 s_list[kTop ? kJoinWaves : 1][kWave];
+    __shared__ u64 s_list[W][kWave];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const float c = a.scale * kLog2e;
     for (int64_t t = blockIdx.x; t < a.n; t += gridDim.x) {
         u64 best = 0;
-        if constexpr (kTop) {
-            const int32_t keys = p.parts * a.top;
-            const u64 *from = p.best + t * p.parts * a.top;
-            for (int32_t i = wave * kWave; i < keys; i += kJoinWaves * kWave)
-                best = merge_wave(best, sort_wave(i + lane < keys ? from[i + lane] : 0, lane), lane);
-            best = merge_waves<kJoinWaves>(best, s_list, wave, lane);
+        const int32_t keys = p.parts * a.top;
+        const u64 *from = p.best + t * keys;
+        for (int32_t i = wave * kWave; i < keys; i += W * kWave) {
+            const u64 more = sort_wave(i + lane < keys ? from[i + lane] : 0, lane);
+            best = i == wave * kWave ? more : merge_wave(best, more, lane);
         }
+        if constexpr (W > 1) best = merge_waves<W>(best, s_list, wave, lane);
         if (wave == 0) {
             Stat st{kFirst, -1.f, 0.f};
-            const float *from = p.stat + 3 * t * p.parts;
+            const float *stat = p.stat + 3 * t * p.parts;
             for (int32_t i = lane; i < p.parts; i += kWave)
-                st = merge(st, {from[3 * i], from[3 * i + 1], from[3 * i + 2]}, c);
+                st = merge(st, {stat[3 * i], stat[3 * i + 1], stat[3 * i + 2]}, c);
             finish<T, I>(a, t, merge_lanes(st, c), best, lane);
         }
-        if (kTop) __syncthreads();
+        if constexpr (W > 1) __syncthreads();
     }
 }
 
-// Parts of a row: few rows are cut, so that kGroups workgroups run, into parts
-// of no less than one step of a workgroup and a whole number of them.
+// Parts of a row: few rows are cut, so that about kGroups workgroups run, into
+// parts of no less than kUnit columns and a whole number of them.
 constexpr int64_t kGroups = 1024;
 constexpr int kMostParts = 64;
+constexpr int32_t kUnit = 4096;
 void cut(int32_t V, int64_t n, int32_t *parts, int32_t *part) {
-    constexpr int32_t kUnit = kThreads * 8;
     const int64_t units = std::max<int64_t>(1, (static_cast<int64_t>(V) + kUnit - 1) / kUnit);
     const int64_t want = std::min<int64_t>({units, kMostParts, (kGroups + n - 1) / n});
     const int64_t per = (units + want - 1) / want;
@@ -433,10 +504,9 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a, 
 #pragma unroll
             for (int i = 0; i < E; ++i) v[u][i] = 0.f;
             if (zero) continue;
-            if (at + E <= a.V)
-                load_piece<E>(src + at, v[u]);
-            else if (at < a.V)
-                load_piece_tail<E>(src + at, static_cast<int>(a.V - at), v[u]);
+            const Vec<T, E> o = load_some<T, E>(src + at, a.V - at);
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[u][i] = static_cast<float>(o[i]);
         }
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
@@ -467,10 +537,16 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a, 
                     for (int i = 0; i < E; ++i) v[u][i] = at + i == id ? d : v[u][i];
                 }
             }
-            if (at + E <= a.V)
-                store_piece<E>(dst + at, v[u]);
-            else
-                store_piece_tail<E>(dst + at, static_cast<int>(a.V - at), v[u]);
+            Vec<B, E> o;
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[i] = static_cast<B>(v[u][i]);
+            if (at + E <= a.V) {
+                *reinterpret_cast<Loose<B, E> *>(dst + at) = o;
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (at + i < a.V) dst[at + i] = o[i];
+            }
         }
     }
 }
@@ -502,15 +578,23 @@ spmv_status logprobs(const LogprobsArgs &a, hipStream_t s) {
         with_ids(a.id_dtype, [&](auto i) {
             using T = decltype(x);
             using I = decltype(i);
-            if (a.top > 0)
-                k_logprobs<T, I, true><<<grid, kThreads, 0, s>>>(p);
+            const bool brief = p.part <= kFlight * kThreads * kPer<T>;
+            if (a.top > 0 && brief)
+                k_logprobs<T, I, true, true><<<grid, kThreads, 0, s>>>(p);
+            else if (a.top > 0)
+                k_logprobs<T, I, true, false><<<grid, kThreads, 0, s>>>(p);
+            else if (brief)
+                k_logprobs<T, I, false, true><<<grid, kThreads, 0, s>>>(p);
             else
-                k_logprobs<T, I, false><<<grid, kThreads, 0, s>>>(p);
+                k_logprobs<T, I, false, false><<<grid, kThreads, 0, s>>>(p);
             if (p.parts == 1) return;
-            if (a.top > 0)
-                k_join<T, I, true><<<groups_for(a.n, 1), kJoinWaves * kWave, 0, s>>>(p);
+            const unsigned rows = groups_for(a.n, 1);
+            if (p.parts * a.top <= 2 * kWave)
+                k_join<T, I, 1><<<rows, kWave, 0, s>>>(p);
+            else if (p.parts * a.top <= 8 * kWave)
+                k_join<T, I, 4><<<rows, 4 * kWave, 0, s>>>(p);
             else
-                k_join<T, I, false><<<groups_for(a.n, 1), kWave, 0, s>>>(p);
+                k_join<T, I, 16><<<rows, 16 * kWave, 0, s>>>(p);
         });
     });
     SPMV_HIP(hipGetLastError());

@@ -8,6 +8,32 @@
 
 namespace spmv {
 
+// Vectors in registers, and in memory at the alignment of their elements: the
+// compiler takes such an access apart if it is one of a struct or an array.
+template <typename T, int E>
+struct VecOf {
+    typedef T type __attribute__((ext_vector_type(E)));
+    typedef T loose __attribute__((ext_vector_type(E), aligned(sizeof(T)), may_alias));
+};
+template <typename T, int E>
+using Vec = typename VecOf<T, E>::type;
+template <typename T, int E>
+using Loose = typename VecOf<T, E>::loose;
+template <typename T, int E>
+__device__ inline Vec<T, E> load_all(const T *p) {
+    return *reinterpret_cast<const Loose<T, E> *>(p);
+}
+// E neighbours, the first `there` of them; the others are 0.
+template <typename T, int E>
+__device__ inline Vec<T, E> load_some(const T *p, int64_t there) {
+    if (there >= E) return *reinterpret_cast<const Loose<T, E> *>(p);
+    Vec<T, E> o = {};
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+        if (i < there) o[i] = p[i];
+    return o;
+}
+
 // Alternatives per row, at most: one per lane of the wave that sorts them.
 constexpr int kMostTop = kWave;
 
