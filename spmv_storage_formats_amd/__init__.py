@@ -1150,17 +1150,16 @@ def _adapters(down, up, scales, like, index):
     import torch
     if not (isinstance(down, torch.Tensor) and isinstance(up, torch.Tensor)):
         raise TypeError("down and up must be cuda tensors")
-    if down.dim() != 3 or up.dim() != 3 or up.shape[0] != down.shape[0] \
-            or up.shape[2] != down.shape[1]:
+    ds, us = down.shape, up.shape
+    if len(ds) != 3 or len(us) != 3 or us[0] != ds[0] or us[2] != ds[1]:
         raise ValueError(f"down and up must be [L, rank, C] and [L, R, rank], got "
-                         f"{tuple(down.shape)} and {tuple(up.shape)}")
-    for t, name in ((down, "down"), (up, "up")):
-        if t.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    L, rank, C = down.shape
-    sp = None if scales is None else _like(scales, (L,), torch.float32, index, "scales")
-    return (L, rank, C, up.shape[1], _dev(down, like.dtype, "down"), _dev(up, like.dtype, "up"),
-            sp)
+                         f"{tuple(ds)} and {tuple(us)}")
+    if down.get_device() != index or up.get_device() != index:
+        raise ValueError(f"down and up are on {down.device} and {up.device}, expected "
+                         f"cuda:{index}")
+    return (ds[0], ds[1], ds[2], us[1], _dev(down, like.dtype, "down"),
+            _dev(up, like.dtype, "up"),
+            None if scales is None else _like(scales, ds[:1], torch.float32, index, "scales"))
 
 
 def _unless(t, flat, base, what):

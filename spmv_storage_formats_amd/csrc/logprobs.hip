@@ -14,7 +14,7 @@
 // held at kLowest there.  NaN and +inf reach s as NaN.
 //
 // Alternatives: every thread's own maximum, kept anyway, is one element of the
-// row, so the top-th largest of the threads' maxima is a bound that at least
+// row, so the top-th largest of some threads' maxima is a bound that at least
 // `top` elements reach.  Only threads whose maximum reaches it look at their
 // elements again.  Elements are compared as whole numbers (key()) that order by
 // value, then by the lower index: no two are equal, so nothing depends on the
@@ -30,7 +30,12 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kFlight = 4;            // pieces of a row in flight per thread
+// Pieces of a row in flight per thread: 4096 x 128000 bf16 takes 190 us with
+// four, 195 with two; with alternatives, which need registers of their own, 48 x
+// 50001 fp16 takes 17 and 14.
+template <bool kTop>
+constexpr int kPieces = kTop ? 2 : 4;
+constexpr int kGradFlight = 4;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLowest = -160.f;     // 2^kLowest is 0 in fp32
@@ -127,8 +132,8 @@ __device__ inline u64 merge_wave(u64 a, u64 b, int lane) {
     return exchange<32>(a > back ? a : back, lane, 64);
 }
 
-// The k-th largest of the wave's keys that are not 0; 0 if there are fewer.
-__device__ inline u64 kth_wave(u64 key, int k) {
+// How many of the wave's keys are larger than the lane's.
+__device__ inline int rank_wave(u64 key) {
     const uint32_t lo = static_cast<uint32_t>(key), hi = static_cast<uint32_t>(key >> 32);
     int before = 0;
 #pragma unroll
@@ -138,11 +143,14 @@ __device__ inline u64 kth_wave(u64 key, int k) {
             static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, l));
         before += other > key;
     }
+    return before;
+}
+
+// The k-th largest of the wave's keys that are not 0; 0 if there are fewer.
+__device__ inline u64 kth_wave(u64 key, int k) {
+    const int before = rank_wave(key);
     const u64 who = __ballot(key != 0 && before == k - 1);  // keys differ: one lane or none
-    if (!who) return 0;
-    const int at = __builtin_ctzll(who);
-    return (static_cast<u64>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, at))) << 32) |
-           static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, at));
+    return who ? __shfl(key, __builtin_ctzll(who)) : 0;
 }
 
 // The 64 largest of the waves' lists, in wave 0.  Begins and ends with a barrier.
@@ -231,15 +239,15 @@ __device__ inline void load_part(const T *row, int32_t at, int32_t count, float 
 // row's results, otherwise the part's, which k_join puts together.  kShort: the
 // part is no longer than kFlight pieces of each thread and stays in registers.
 template <typename T, typename I, bool kTop, bool kShort>
-__global__ __launch_bounds__(kThreads) void k_logprobs(Place p) {
-    constexpr int E = kPer<T>;
+__global__ __launch_bounds__(kThreads, kTop && !kShort ? 6 : 1) void k_logprobs(Place p) {
+    constexpr int E = kPer<T>, kFlight = kPieces<kTop>;
     constexpr int kStep = kThreads * E;
     const LogprobsArgs &a = p.a;
     __shared__ Stat s_stat[kWaves];
     __shared__ u64 s_list[kTop ? kWaves : 1][kWave];
     __shared__ u64 s_found[kTop ? kWaves : 1][kWave * (E + 1)];
     __shared__ int s_again[kTop && !kShort ? kWaves : 1][kWave];
-    __shared__ u64 s_bound[kWaves];
+    __shared__ u64 s_bound[kTop ? kWave : 1];
     const int lane = threadIdx.x % kWave, tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const float c = a.scale * kLog2e;
@@ -302,14 +310,15 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(Place p) {
         Stat st = merge_lanes({m, s - 1.f, w}, c);
         u64 best = 0;
         if constexpr (kTop) {
-            // Elements that reach the best of the waves' top-th largest maxima.
+            // The bound: the top-th largest of each wave's 16 largest maxima.
             const u64 own = last >= 0 ? key(m, last) : 0;
-            const u64 least = kth_wave(own, a.top);
-            if (lane == 0) s_bound[wave] = least;
+            const int place = rank_wave(own);
+            constexpr int kShare = kWave / kWaves;
+            if (own != 0 && place < kShare) s_bound[wave * kShare + place] = own;
+            const int seen = __popcll(__ballot(own != 0));
+            if (lane >= seen && lane < kShare) s_bound[wave * kShare + lane] = 0;
             __syncthreads();
-            u64 bound = s_bound[0];
-#pragma unroll
-            for (int i = 1; i < kWaves; ++i) bound = s_bound[i] > bound ? s_bound[i] : bound;
+            const u64 bound = kth_wave(s_bound[lane], a.top);
             u64 *found = s_found[wave];
             int have = 0;
             const u64 below = (1ull << lane) - 1ull;
@@ -474,7 +483,7 @@ size_t stat_bytes(int64_t items) { return (static_cast<size_t>(items) * 12 + 15)
 
 // ------------------------------------------------------------------ gradient
 
-// A workgroup's threads take kFlight pieces each of one row.  Reads and writes
+// A workgroup's threads take kGradFlight pieces each of one row.  Reads and writes
 // as a copy does; a row whose two weights are 0 is not read.
 template <typename T, typename B, typename I, bool kEntropy>
 __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a, int32_t blocks) {
@@ -484,7 +493,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a, 
     const int64_t items = a.n * blocks;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int64_t t = item / blocks;
-        const int32_t first = static_cast<int32_t>(item % blocks) * (kFlight * kStep);
+        const int32_t first = static_cast<int32_t>(item % blocks) * (kGradFlight * kStep);
         const int64_t token = static_cast<const I *>(a.ids)[t];
         const bool given = token >= 0 && token < a.V;
         const int32_t id = given ? static_cast<int32_t>(token) : -1;
@@ -497,9 +506,9 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a, 
         const float L2 = L * kLog2e;
         const T *src = static_cast<const T *>(a.logits) + t * a.ld;
         B *dst = static_cast<B *>(a.out) + t * a.out_ld;
-        float v[kFlight][E];
+        float v[kGradFlight][E];
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
+        for (int u = 0; u < kGradFlight; ++u) {
             const int32_t at = first + u * kStep + static_cast<int32_t>(threadIdx.x) * E;
 #pragma unroll
             for (int i = 0; i < E; ++i) v[u][i] = 0.f;
@@ -509,7 +518,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a, 
             for (int i = 0; i < E; ++i) v[u][i] = static_cast<float>(o[i]);
         }
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
+        for (int u = 0; u < kGradFlight; ++u) {
             const int32_t at = first + u * kStep + static_cast<int32_t>(threadIdx.x) * E;
             if (at >= a.V) continue;
             if (!zero) {
@@ -578,7 +587,8 @@ spmv_status logprobs(const LogprobsArgs &a, hipStream_t s) {
         with_ids(a.id_dtype, [&](auto i) {
             using T = decltype(x);
             using I = decltype(i);
-            const bool brief = p.part <= kFlight * kThreads * kPer<T>;
+            const int pieces = a.top > 0 ? kPieces<true> : kPieces<false>;
+            const bool brief = p.part <= pieces * kThreads * kPer<T>;
             if (a.top > 0 && brief)
                 k_logprobs<T, I, true, true><<<grid, kThreads, 0, s>>>(p);
             else if (a.top > 0)
@@ -608,7 +618,7 @@ spmv_status logprobs_grad(const LogprobsGradArgs &a, hipStream_t s) {
             using I = decltype(i);
             auto go = [&](auto to) {
                 using B = decltype(to);
-                constexpr int kRun = kFlight * kThreads * kPer<B>;
+                constexpr int kRun = kGradFlight * kThreads * kPer<B>;
                 const int32_t blocks =
                     static_cast<int32_t>((static_cast<int64_t>(a.V) + kRun - 1) / kRun);
                 const unsigned grid = groups_for(a.n * blocks, 1);

@@ -1,0 +1,69 @@
+"""gfx950 code generation of the kernels on a step's rows, from the assembly hipcc writes for this
+repository's sources (CPU only).
+
+- No kernel selects or branches on the scalar condition code where the compare before it set a
+  vector one (the pattern that the weight tables' test describes).
+- No sum is made by atomics in memory: the sort counts rows by whole-number ones in LDS alone.
+- No kernel spills vector registers to memory, but those for more than 64 ranks.
+- Rows of 16-bit results and bases move in accesses of 8 or 16 bytes."""
+import os
+import re
+import subprocess
+
+import pytest
+
+from spmv_storage_formats_amd import _build
+from test_tables_codegen import misread_conditions
+
+SOURCES = ["adapt.hip", "adapt_fp32.hip", "adapt_fp16.hip", "adapt_bf16.hip", "logprobs.hip"]
+
+
+@pytest.fixture(scope="module")
+def listings(tmp_path_factory):
+    if not os.path.exists(_build.HIPCC):
+        pytest.skip("hipcc not installed")
+    d = tmp_path_factory.mktemp("asm")
+    out = {}
+    running = []
+    for name in SOURCES:
+        s = d / (name + ".s")
+        running.append((name, s, subprocess.Popen(
+            [_build.HIPCC, *_build.CFLAGS, "--cuda-device-only", "-S",
+             os.path.join(_build.CSRC, name), "-o", str(s)],
+            stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    for name, s, p in running:
+        said, _ = p.communicate()
+        assert p.returncode == 0, said
+        out[name] = s.read_text()
+    return out
+
+
+@pytest.mark.parametrize("name", SOURCES)
+def test_conditions_are_read_where_they_were_set(listings, name):
+    assert misread_conditions(listings[name]) == []
+
+
+@pytest.mark.parametrize("name", SOURCES)
+def test_no_global_atomics(listings, name):
+    assert not re.search(r"\b(global|flat|buffer)_atomic_", listings[name])
+
+
+@pytest.mark.parametrize("name", SOURCES)
+def test_no_spills(listings, name):
+    kernels = re.findall(r"\.amdhsa_kernel (\S+)(.*?)\.end_amdhsa_kernel", listings[name], re.S)
+    assert kernels
+    for kernel, body in kernels:
+        private = int(re.search(r"private_segment_fixed_size (\d+)", body).group(1))
+        many = re.search(r"k_adapt_expand\S*Li[48]ELi4", kernel)
+        assert private == 0 or many, (kernel, private)
+
+
+@pytest.mark.parametrize("name", ["adapt_fp16.hip", "adapt_bf16.hip"])
+def test_rows_move_in_whole_vectors(listings, name):
+    """The results of 64 rows by 256 columns: a store of four neighbours for each of a lane's
+    rows, not one per element."""
+    text = listings[name]
+    for kernel in re.findall(r"^(_ZN\S*k_adapt_expand\S*Li0ELi4E\S*):", text, re.M):
+        body = text[text.index(kernel + ":"):]
+        body = body[:body.index(".end_amdhsa_kernel")]
+        assert len(re.findall(r"global_store_dwordx[24]", body)) >= 16
