@@ -105,8 +105,10 @@ struct Adapt {
     static void shrink(const ShrinkArgs &a, int64_t tiles, hipStream_t s);
     static void shrink_both(const ShrinkArgs &a, const ShrinkArgs &across, int64_t tiles,
                             hipStream_t s);
-    static void expand(const ExpandArgs &a, bool across, bool out_fp32, int64_t tiles,
-                       hipStream_t s);
+    static void expand(const ExpandArgs &a, bool out_fp32, int64_t tiles, hipStream_t s);
+    // expand by an across matrix (dx), and the numbers that `weights` reads
+    static void back(const ExpandArgs &a, bool dx, const FinishArgs &h, const FinishArgs &g,
+                     bool finish, int64_t tiles, hipStream_t s);
     // ddown from x and dup (across) from grad; either may have no blocks
     static void weights(const WeightArgs &down, const WeightArgs &up, int32_t adapters,
                         int64_t chunks, hipStream_t s);
@@ -517,8 +519,7 @@ struct Numbers<float, G, kAll> {
 // Column tile j holds columns i16 * NT + j, so that a lane's results of one row
 // are neighbours, and those of 16 lanes are 128 bytes (fp32: 256) or more.
 template <typename T, typename B, int G, int NT, bool kAcross>
-__global__ __launch_bounds__(kAdaptThreads, G == 2 && sizeof(T) == 2 ? 3 : 1) void
-k_adapt_expand(ExpandArgs a) {
+__device__ inline void expand_rows(const ExpandArgs &a) {
     using H = Numbers<T, G, sizeof(B) == 4>;
     using M = Vec<T, H::kPer>;
     constexpr int K = H::kPer, NG = H::kGroups;
@@ -740,6 +741,100 @@ k_adapt_expand(ExpandArgs a) {
                 store(u, e, __builtin_convertvector(v, Vec<B, NT>));
             }
         }
+    }
+}
+
+template <typename T, typename B, int G, int NT>
+__global__ __launch_bounds__(kAdaptThreads, G == 2 && sizeof(T) == 2 ? 3 : 1) void
+k_adapt_expand(ExpandArgs a) {
+    expand_rows<T, B, G, NT, false>(a);
+}
+
+// Sums of the splits, scaled, rank by rank: what the matrices' gradients read.
+// A workgroup takes a tile and 16 ranks, a thread four of a row.
+template <typename T>
+__device__ inline void finish_rows(const FinishArgs &f, int32_t number, int32_t ranks) {
+    const AdaptTile tile = f.tiles[number];
+    if (tile.adapter < 0 || tile.adapter >= f.adapters) return;
+    const int32_t row = static_cast<int32_t>(threadIdx.x) / 4;
+    const int32_t k = ranks * 16 + static_cast<int32_t>(threadIdx.x) % 4 * 4;
+    const float scale = f.scales ? f.scales[tile.adapter] : 1.f;
+    const bool there = row < tile.count;
+    const int32_t at = tile.first + (there ? row : 0);
+    const float *p = f.sums + static_cast<int64_t>(f.order[at]) * f.width + k;
+    float v[4];
+    load_piece<4>(p, v);
+#pragma unroll 4
+    for (int32_t j = 1; j < f.splits; ++j) {
+        float more[4];
+        load_piece<4>(p + static_cast<int64_t>(j) * f.n * f.width, more);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += more[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = there && k + i < f.rank ? v[i] * scale : 0.f;
+    Power power[4] = {{1.f, 1.f}, {1.f, 1.f}, {1.f, 1.f}, {1.f, 1.f}};
+    if constexpr (std::is_same<T, f16>::value) {
+        // the largest of the tile's rows, by rank
+        __shared__ float s_most[kAdaptWaves][16];
+        const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+        float most[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            most[i] = fabsf(v[i]);
+            // a NaN must not hide what is beside it: its row is no number anyway
+#pragma unroll
+            for (int j = 4; j < kWave; j *= 2) most[i] = fmaxf(most[i], __shfl_xor(most[i], j));
+            if (lane < 4) s_most[wave][lane * 4 + i] = most[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float m = 0.f;
+#pragma unroll
+            for (int w = 0; w < kAdaptWaves; ++w)
+                m = fmaxf(m, s_most[w][threadIdx.x % 4 * 4 + i]);
+            power[i] = spmv::power(m);
+        }
+        if (row == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f.factors[static_cast<int64_t>(number) * f.width + k + i] = power[i].back;
+        }
+    }
+    if (!there) return;
+    const int64_t part = static_cast<int64_t>(f.stride) * f.width;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t to = static_cast<int64_t>(k + i) * f.stride + at;
+        float s = v[i] * power[i].up;
+        if constexpr (std::is_same<T, f16>::value) {
+            f16 *out = static_cast<f16 *>(f.out) + to;
+            const f16 lead = static_cast<f16>(s);
+            out[0] = lead;
+            out[part] = rest_of(s, lead);
+        } else if constexpr (std::is_same<T, bf16>::value) {
+            bf16 *out = static_cast<bf16 *>(f.out) + to;
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                out[q * part] = upper(s);
+                s = below(s);
+            }
+        } else {
+            static_cast<float *>(f.out)[to] = s;
+        }
+    }
+}
+
+// dx, and by further workgroups what the matrices' gradients read.
+template <typename T, int G, int NT>
+__global__ __launch_bounds__(kAdaptThreads, G == 2 && sizeof(T) == 2 ? 3 : 1) void
+k_adapt_back(ExpandArgs a, int32_t groups, FinishArgs h, FinishArgs g) {
+    if (static_cast<int32_t>(blockIdx.x) < groups) {
+        expand_rows<T, T, G, NT, true>(a);
+    } else {
+        const int32_t at = static_cast<int32_t>(blockIdx.x) - groups, ranks = h.width / 16;
+        finish_rows<T>(at % 2 ? g : h, at / (2 * ranks), at / 2 % ranks);
     }
 }
 
@@ -1000,20 +1095,32 @@ void Adapt<T>::shrink_both(const ShrinkArgs &a, const ShrinkArgs &across, int64_
     });
 }
 
+constexpr int kExpandTiles = 4;  // column tiles of a wave
+inline int64_t expand_groups(int32_t D, int64_t tiles) {
+    return tiles * ((D - 1) / (kAdaptWaves * 16 * kExpandTiles) + 1);
+}
+
 template <typename T>
-void Adapt<T>::expand(const ExpandArgs &a, bool across, bool out_fp32, int64_t tiles,
-                      hipStream_t s) {
-    constexpr int NT = 4;
-    const unsigned grid =
-        static_cast<unsigned>(tiles * ((a.D - 1) / (kAdaptWaves * 16 * NT) + 1));
+void Adapt<T>::expand(const ExpandArgs &a, bool out_fp32, int64_t tiles, hipStream_t s) {
+    const unsigned grid = static_cast<unsigned>(expand_groups(a.D, tiles));
     with_groups(a.rank, [&](auto groups) {
-        constexpr int G = decltype(groups)::value;
-        if (across)  // dx, of the inputs' type
-            k_adapt_expand<T, T, G, NT, true><<<grid, kAdaptThreads, 0, s>>>(a);
-        else if (out_fp32)
-            k_adapt_expand<T, float, G, NT, false><<<grid, kAdaptThreads, 0, s>>>(a);
+        constexpr int G = decltype(groups)::value, NT = kExpandTiles;
+        if (out_fp32)
+            k_adapt_expand<T, float, G, NT><<<grid, kAdaptThreads, 0, s>>>(a);
         else
-            k_adapt_expand<T, T, G, NT, false><<<grid, kAdaptThreads, 0, s>>>(a);
+            k_adapt_expand<T, T, G, NT><<<grid, kAdaptThreads, 0, s>>>(a);
+    });
+}
+
+template <typename T>
+void Adapt<T>::back(const ExpandArgs &a, bool dx, const FinishArgs &h, const FinishArgs &g,
+                    bool finish, int64_t tiles, hipStream_t s) {
+    const int64_t groups = dx ? expand_groups(a.D, tiles) : 0;
+    const int64_t more = finish ? tiles * 2 * (h.width / 16) : 0;
+    with_groups(a.rank, [&](auto ranks) {
+        constexpr int G = decltype(ranks)::value;
+        k_adapt_back<T, G, kExpandTiles><<<static_cast<unsigned>(groups + more), kAdaptThreads, 0, s>>>(
+            a, static_cast<int32_t>(groups), h, g);
     });
 }
 

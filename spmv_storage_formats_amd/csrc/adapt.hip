@@ -214,84 +214,6 @@ __global__ __launch_bounds__(kGroupThreads) void k_adapt_group(GroupArgs a) {
         for (int k = tid; k < keys; k += kGroupThreads) a.chunk_start[k] = s_first[k];
 }
 
-// Sums of the splits, scaled, rank by rank: what the matrices' gradients read.
-// A workgroup takes a tile and 16 ranks, a thread four of a row.
-template <typename T>
-__global__ __launch_bounds__(kAdaptThreads) void k_adapt_finish(FinishArgs a, FinishArgs b) {
-    const FinishArgs &f = blockIdx.y == 0 ? a : b;
-    const AdaptTile tile = f.tiles[blockIdx.x];
-    if (tile.adapter < 0 || tile.adapter >= f.adapters) return;
-    const int32_t row = static_cast<int32_t>(threadIdx.x) / 4;
-    const int32_t k =
-        static_cast<int32_t>(blockIdx.z) * 16 + static_cast<int32_t>(threadIdx.x) % 4 * 4;
-    const float scale = f.scales ? f.scales[tile.adapter] : 1.f;
-    const bool there = row < tile.count;
-    const int32_t at = tile.first + (there ? row : 0);
-    const float *p = f.sums + static_cast<int64_t>(f.order[at]) * f.width + k;
-    float v[4];
-    load_piece<4>(p, v);
-#pragma unroll 4
-    for (int32_t j = 1; j < f.splits; ++j) {
-        float more[4];
-        load_piece<4>(p + static_cast<int64_t>(j) * f.n * f.width, more);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += more[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = there && k + i < f.rank ? v[i] * scale : 0.f;
-    Power power[4] = {{1.f, 1.f}, {1.f, 1.f}, {1.f, 1.f}, {1.f, 1.f}};
-    if constexpr (std::is_same<T, f16>::value) {
-        // the largest of the tile's rows, by rank
-        __shared__ float s_most[kAdaptWaves][16];
-        const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-        float most[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            most[i] = fabsf(v[i]);
-            // a NaN must not hide what is beside it: its row is no number anyway
-#pragma unroll
-            for (int j = 4; j < kWave; j *= 2) most[i] = fmaxf(most[i], __shfl_xor(most[i], j));
-            if (lane < 4) s_most[wave][lane * 4 + i] = most[i];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float m = 0.f;
-#pragma unroll
-            for (int w = 0; w < kAdaptWaves; ++w)
-                m = fmaxf(m, s_most[w][threadIdx.x % 4 * 4 + i]);
-            power[i] = spmv::power(m);
-        }
-        if (row == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f.factors[static_cast<int64_t>(blockIdx.x) * f.width + k + i] = power[i].back;
-        }
-    }
-    if (!there) return;
-    const int64_t part = static_cast<int64_t>(f.stride) * f.width;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t to = static_cast<int64_t>(k + i) * f.stride + at;
-        float s = v[i] * power[i].up;
-        if constexpr (std::is_same<T, f16>::value) {
-            f16 *out = static_cast<f16 *>(f.out) + to;
-            const f16 lead = static_cast<f16>(s);
-            out[0] = lead;
-            out[part] = rest_of(s, lead);
-        } else if constexpr (std::is_same<T, bf16>::value) {
-            bf16 *out = static_cast<bf16 *>(f.out) + to;
-#pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                out[q * part] = upper(s);
-                s = below(s);
-            }
-        } else {
-            static_cast<float *>(f.out)[to] = s;
-        }
-    }
-}
-
 // The chunks' sums of a matrix's gradient, joined in their order.
 struct JoinArgs {
     const float *down, *up;   // chunks x [rank, C], [R, rank]
@@ -449,7 +371,7 @@ spmv_status adapt(const AdaptArgs &a, hipStream_t s) {
                       tiles, s);
         A::expand({rows, sums, p.splits_c, p.width, a.scales, a.up, a.R, a.rank, a.base, a.base_ld,
                    a.out, a.out_ld},
-                  false, a.out_dtype == SPMV_FP32, tiles, s);
+                  a.out_dtype == SPMV_FP32, tiles, s);
     });
     SPMV_HIP(hipGetLastError());
     return SPMV_OK;
@@ -478,17 +400,16 @@ spmv_status adapt_grad(const AdaptGradArgs &a, hipStream_t s) {
         const ShrinkArgs g{rows, a.grad, a.grad_ld, a.up, a.R, a.rank, p.width, p.splits_r,
                            p.part_r, p.subs, floats(p.sums_r)};
         if (any) A::shrink_both(h, g, p.tiles, s);
-        if (a.dx && a.n > 0 && a.C > 0)
-            A::expand({rows, g.sums, g.splits, p.width, a.scales, a.down, a.C, a.rank, a.base,
-                       a.base_ld, a.dx, a.dx_ld},
-                      true, false, p.tiles, s);
-        if (!any || !weights) return;
         const FinishArgs fh{h.sums, h.splits, p.width, a.n, a.rank, a.adapters, a.scales, order,
                             tiles, ws + p.v_c, floats(p.factors_c), p.stride};
         const FinishArgs fg{g.sums, g.splits, p.width, a.n, a.rank, a.adapters, a.scales, order,
                             tiles, ws + p.v_r, floats(p.factors_r), p.stride};
-        const dim3 grid(static_cast<unsigned>(p.tiles), 2, static_cast<unsigned>(p.width / 16));
-        k_adapt_finish<decltype(x)><<<grid, kAdaptThreads, 0, s>>>(fh, fg);
+        const bool dx = a.dx && a.n > 0 && a.C > 0;
+        if (dx || (any && weights))
+            A::back({rows, g.sums, g.splits, p.width, a.scales, a.down, a.C, a.rank, a.base,
+                     a.base_ld, a.dx, a.dx_ld},
+                    dx, fh, fg, any && weights, p.tiles, s);
+        if (!any || !weights) return;
         auto sums = [&](const void *x, int64_t ld, const FinishArgs &f, int32_t D, size_t partial,
                         void *out) {
             return WeightArgs{x, ld, f.out, f.factors, p.stride, D, a.rank, p.width, order, chunks,

@@ -1,4 +1,5 @@
 // C ABI of the operators on a step's rows (include/spmv.h): argument checks.
+#include <algorithm>
 #include <cmath>
 
 #include "requests.h"
@@ -15,6 +16,9 @@ spmv_status adapt_sizes(int32_t adapters, int32_t rank, int32_t C, int32_t R, in
     if (adapters > kMostAdapters || rank > kMostRank || C > kMostColumns || R > kMostColumns ||
         n > kMostAdaptRows)
         return SPMV_ERR_TOO_LARGE;
+    // workgroups of one launch: tiles of 64 rows, one more of each adapter, by 256 columns
+    const int64_t tiles = (n + 63) / 64 + std::min<int64_t>(adapters + 1, n);
+    if (tiles * ((std::max(C, R) + 255) / 256) > kMostAdaptGroups) return SPMV_ERR_TOO_LARGE;
     return SPMV_OK;
 }
 

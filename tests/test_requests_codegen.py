@@ -4,7 +4,7 @@ repository's sources (CPU only).
 - No kernel selects or branches on the scalar condition code where the compare before it set a
   vector one (the pattern that the weight tables' test describes).
 - No sum is made by atomics in memory: the sort counts rows by whole-number ones in LDS alone.
-- No kernel spills vector registers to memory, but those for more than 64 ranks.
+- No kernel spills registers to memory.
 - Rows of 16-bit results and bases move in accesses of 8 or 16 bytes."""
 import os
 import re
@@ -54,8 +54,7 @@ def test_no_spills(listings, name):
     assert kernels
     for kernel, body in kernels:
         private = int(re.search(r"private_segment_fixed_size (\d+)", body).group(1))
-        many = re.search(r"k_adapt_expand\S*Li[48]ELi4", kernel)
-        assert private == 0 or many, (kernel, private)
+        assert private == 0, (kernel, private)
 
 
 @pytest.mark.parametrize("name", ["adapt_fp16.hip", "adapt_bf16.hip"])

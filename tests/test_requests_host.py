@@ -134,7 +134,8 @@ def adapt_grad(lib, **change):
 SIZES = [({"L": -1}, INVALID), ({"rank": 0}, INVALID), ({"rank": -1}, INVALID),
          ({"C": -1}, INVALID), ({"R": -1}, INVALID), ({"n": -1}, INVALID),
          ({"L": 2049}, TOO_LARGE), ({"rank": 257}, TOO_LARGE), ({"C": 2**21 + 1}, TOO_LARGE),
-         ({"R": 2**21 + 1}, TOO_LARGE), ({"n": 2**24 + 1}, TOO_LARGE)]
+         ({"R": 2**21 + 1}, TOO_LARGE), ({"n": 2**24 + 1}, TOO_LARGE),
+         ({"n": 2**24, "C": 2**14}, TOO_LARGE), ({"n": 2**24, "R": 2**14}, TOO_LARGE)]
 
 
 @pytest.mark.parametrize("change,status", SIZES + [
