@@ -279,13 +279,17 @@ __global__ __launch_bounds__(kThreads, kTop && !kShort ? 6 : 1) void k_logprobs(
                 for (int u = kFlight - 1; u >= 0; --u)
                     if (pm[u] == cm) last = at + u * kStep + E - 1;
             }
+            // these pieces' sums first: fewer roundings than one by one into s and w
+            float ps = 0.f, pw = 0.f;
 #pragma unroll
             for (int i = 0; i < kFlight * E; ++i) {
                 const float y = (v[i] - m) * c;
                 const float e = __builtin_amdgcn_exp2f(y);
-                s += e;
-                w += e * fmaxf(y, kLowest);
+                ps += e;
+                pw += e * fmaxf(y, kLowest);
             }
+            s += ps;
+            w += pw;
         };
         float v[kFlight * E];
         int32_t at = tid * E;
