@@ -395,18 +395,21 @@ spmv_status adapt_grad(const AdaptGradArgs &a, hipStream_t s) {
         using A = Adapt<decltype(x)>;
         const bool any = a.adapters > 0 && a.n > 0;
         const RowsArgs rows{a.ids, a.id_dtype, a.n, a.adapters, order, tiles};
-        const ShrinkArgs h{rows, a.x, a.x_ld, a.down, a.C, a.rank, p.width, p.splits_c, p.part_c,
-                           p.subs, floats(p.sums_c)};
-        const ShrinkArgs g{rows, a.grad, a.grad_ld, a.up, a.R, a.rank, p.width, p.splits_r,
-                           p.part_r, p.subs, floats(p.sums_r)};
-        if (any) A::shrink_both(h, g, p.tiles, s);
-        const FinishArgs fh{h.sums, h.splits, p.width, a.n, a.rank, a.adapters, a.scales, order,
-                            tiles, ws + p.v_c, floats(p.factors_c), p.stride};
-        const FinishArgs fg{g.sums, g.splits, p.width, a.n, a.rank, a.adapters, a.scales, order,
-                            tiles, ws + p.v_r, floats(p.factors_r), p.stride};
+        // what is not wanted has no splits: no workgroups of the launch
         const bool dx = a.dx && a.n > 0 && a.C > 0;
+        ShrinkArgs h{rows, a.x, a.x_ld, a.down, a.C, a.rank, p.width, p.splits_c, p.part_c, p.subs,
+                     floats(p.sums_c)};
+        ShrinkArgs g{rows, a.grad, a.grad_ld, a.up, a.R, a.rank, p.width, p.splits_r, p.part_r,
+                     p.subs, floats(p.sums_r)};
+        if (!a.dup) h.splits = 0;
+        if (!dx && !a.ddown) g.splits = 0;
+        if (any && h.splits + g.splits > 0) A::shrink_both(h, g, p.tiles, s);
+        const FinishArgs fh{h.sums, p.splits_c, p.width, a.n, a.rank, a.adapters, a.scales, order,
+                            tiles, ws + p.v_c, floats(p.factors_c), p.stride};
+        const FinishArgs fg{g.sums, p.splits_r, p.width, a.n, a.rank, a.adapters, a.scales, order,
+                            tiles, ws + p.v_r, floats(p.factors_r), p.stride};
         if (dx || (any && weights))
-            A::back({rows, g.sums, g.splits, p.width, a.scales, a.down, a.C, a.rank, a.base,
+            A::back({rows, g.sums, p.splits_r, p.width, a.scales, a.down, a.C, a.rank, a.base,
                      a.base_ld, a.dx, a.dx_ld},
                     dx, fh, fg, any && weights, p.tiles, s);
         if (!any || !weights) return;

@@ -353,6 +353,40 @@ def test_gradients_are_differences(dev):
             assert loss(*moved) - at == d.view(-1)[i].item()
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("n", [40, 900])
+def test_each_gradient_alone(dev, dtype, n):
+    """Any of the three gradients without the others is what it is beside them."""
+    c = Case(n, 3, 12, 200, 330, dtype, 9).to(dev)
+    args = (c.grad, c.x, c.down, c.up, c.ids)
+    every = spmv.adapt_grad(*args, scales=c.scales)
+    for keep in range(3):
+        want = [None if i == keep else False for i in range(3)]
+        got = spmv.adapt_grad(*args, None, *want, scales=c.scales)
+        assert torch.equal(got[keep], every[keep])
+        assert [g is None for g in got] == [i != keep for i in range(3)]
+
+
+def test_one_row_without_dimensions(dev):
+    c = Case(1, 2, 4, 30, 20, "bf16", 2, pad=0.0).to(dev)
+    y = spmv.adapt(c.x, c.down, c.up, c.ids, scales=c.scales)
+    one = spmv.adapt(c.x[0], c.down, c.up, c.ids[0], scales=c.scales)
+    assert one.shape == (20,) and torch.equal(one, y[0])
+    dx, dd, du = spmv.adapt_grad(c.grad[0], c.x[0], c.down, c.up, c.ids[0], scales=c.scales)
+    want = spmv.adapt_grad(c.grad, c.x, c.down, c.up, c.ids, scales=c.scales)
+    assert torch.equal(dx, want[0][0]) and torch.equal(dd, want[1]) and torch.equal(du, want[2])
+
+
+def test_rows_by_lists_and_without(dev):
+    """Batches that find their rows (up to 256) and batches sorted into lists give a row the same
+    result: whole numbers, whose sums are exact in any order."""
+    c = Case(400, 6, 16, 700, 500, "bf16", 4, exact=True).to(dev)
+    y = spmv.adapt(c.x, c.down, c.up, c.ids, scales=c.scales)
+    for a, b in ((0, 256), (256, 257), (100, 355), (0, 257), (17, 50)):
+        part = spmv.adapt(c.x[a:b], c.down, c.up, c.ids[a:b], scales=c.scales)
+        assert torch.equal(part, y[a:b])
+
+
 def test_refusals(dev):
     c = Case(6, 2, 4, 10, 12, "fp16", 1).to(dev)
     ok = (c.x, c.down, c.up, c.ids)

@@ -371,6 +371,32 @@ def test_gradient_in_place_and_strides(dev):
     assert e.logprobs.shape == (0,) and e.top_ids.shape == (0, 2)
 
 
+def test_one_row_without_dimensions(dev):
+    x, ids = make(1, 6000, "bf16", 3)
+    x, ids = x.to(dev), ids.to(dev)
+    want = spmv.token_logprobs(x, ids, top=4)
+    r = spmv.token_logprobs(x[0], ids[0], top=4)
+    assert r.logprobs.shape == () and r.stats.shape == (2,) and r.top_ids.shape == (4,)
+    assert all(torch.equal(a, b[0]) for a, b in zip(r, want))
+    g = torch.ones(1, device=dev)
+    d = spmv.token_logprobs_grad(g[0], x[0], ids[0], r.stats)
+    assert torch.equal(d, spmv.token_logprobs_grad(g, x, ids, want.stats)[0])
+
+
+def test_results_do_not_depend_on_the_batch(dev):
+    """Rows as part of a large batch (one workgroup each) and cut into parts: the same
+    alternatives, numbers within both bounds."""
+    x, ids = make(1100, 20000, "bf16", 6)
+    x, ids = x.to(dev), ids.to(dev)
+    r = spmv.token_logprobs(x, ids, top=10)
+    w = Want(x[:3], ids[:3], 1.0, 10)
+    for t in range(3):
+        one = spmv.token_logprobs(x[t:t + 1], ids[t:t + 1], top=10)
+        assert torch.equal(one.top_ids[0], r.top_ids[t])
+        assert (one.logprobs[0] - r.logprobs[t]).abs().item() <= 2 * w.lp_tol[t]
+        assert (one.entropy[0] - r.entropy[t]).abs().item() <= 2 * w.entropy_tol[t]
+
+
 def test_refusals(dev):
     x, ids = make(4, 50, "fp16", 1)
     x, ids = x.to(dev), ids.to(dev)
