@@ -123,6 +123,8 @@ inline int32_t adapt_width(int32_t rank) {
 // Ranks of a workgroup of shrink and weights; more are further workgroups.
 inline int32_t adapt_slabs(int32_t rank) { return (rank + 63) / 64; }
 constexpr int32_t kShrinkColumns = kAdaptWaves * 64;     // of a workgroup's step
+constexpr int kExpandTiles = 4;                          // column tiles of a wave
+constexpr int32_t kExpandColumns = kAdaptWaves * 16 * kExpandTiles;  // of a workgroup
 constexpr int32_t kWeightColumns = 128;                  // of a workgroup
 
 // bf16 parts of a number: its upper 16 bits, the next ones of the rest, the rest.
@@ -1095,9 +1097,8 @@ void Adapt<T>::shrink_both(const ShrinkArgs &a, const ShrinkArgs &across, int64_
     });
 }
 
-constexpr int kExpandTiles = 4;  // column tiles of a wave
 inline int64_t expand_groups(int32_t D, int64_t tiles) {
-    return tiles * ((D - 1) / (kAdaptWaves * 16 * kExpandTiles) + 1);
+    return tiles * ((D - 1) / kExpandColumns + 1);
 }
 
 template <typename T>

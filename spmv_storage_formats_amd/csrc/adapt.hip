@@ -273,14 +273,24 @@ struct Plan {
 };
 
 // Parts of D columns: workgroups for the whole card, no part of less than 256
-// columns, at most 8 (every workgroup of expand adds them up).
-void split(int32_t D, int32_t groups, int32_t *splits, int32_t *part) {
-    constexpr int32_t kGroups = 1024, kUnit = kShrinkColumns, kMost = 8;
+// columns, at most `most`.
+void split(int32_t D, int32_t groups, int32_t most, int32_t *splits, int32_t *part) {
+    constexpr int32_t kGroups = 1024, kUnit = kShrinkColumns;
     const int32_t units = std::max(1, (D + kUnit - 1) / kUnit);
-    const int32_t want = std::min(std::min(kMost, units), (kGroups - 1) / std::max(1, groups) + 1);
+    const int32_t want = std::min(std::min(most, units), (kGroups - 1) / std::max(1, groups) + 1);
     const int32_t per = (units + want - 1) / want;
     *splits = (units + per - 1) / per;
     *part = per * kUnit;
+}
+
+// Every workgroup of expand reads the sums of all parts: a fifth, at most, of
+// the bytes that a row's own numbers and results take.  16384 rows of 4096 to
+// 12288 columns, rank 64: 326 us with four parts, 289 with two, 263 with one;
+// dx of 8192 rows, 4096 to 4096, rank 16 (with the products before it): 73, 77, 81.
+int32_t most_splits(int32_t from, int32_t to, int32_t width) {
+    const int64_t row = (static_cast<int64_t>(from) + 2 * static_cast<int64_t>(to)) * 2;
+    const int64_t sums = static_cast<int64_t>(width) * 4 * (to / kExpandColumns + 1);
+    return static_cast<int32_t>(std::min<int64_t>(8, std::max<int64_t>(1, row / (5 * sums))));
 }
 
 constexpr int32_t kPast = 32;  // rows that the last step of a chunk loads past its end
@@ -300,9 +310,10 @@ Plan plan(int32_t n, int32_t adapters, int32_t rank, int32_t C, int32_t R, bool 
     // few rows of small ranks: 32 of a workgroup; many: 64
     const int32_t full = (n + kAdaptTile - 1) / kAdaptTile;
     p.subs = full >= 1024 || rank > 32 ? 1 : 2;
-    const int32_t groups = !grad && n <= kAdaptDirect ? n : full * p.subs;
-    split(C, groups, &p.splits_c, &p.part_c);
-    split(R, groups, &p.splits_r, &p.part_r);
+    const bool direct = !grad && n <= kAdaptDirect;
+    const int32_t groups = direct ? n : full * p.subs;
+    split(C, groups, grad || direct ? 8 : most_splits(C, R, p.width), &p.splits_c, &p.part_c);
+    split(R, groups, most_splits(R, C, p.width), &p.splits_r, &p.part_r);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
