@@ -14,10 +14,14 @@
 // or first (up in shrink, down in expand: "across").  All sums are in fp32 on
 // the matrix unit and made in an order that the sorted rows fix.
 //
-// The numbers between two products are fp32.  Beside bf16 matrices they are
-// split into bf16 parts by their bits, from the top: two parts (16 bits) where
-// the result is rounded to bf16, three (all 24) where it is fp32.  fp16 and
-// fp32 operands multiply them as fp32 numbers.
+// The numbers between two products are fp32.  A matrix product takes operands of
+// one type, so they meet 16-bit operands as parts that add up to them:
+//   bf16: by their bits, from the top.  Two parts (16 bits, an error of 2^-16)
+//         where the result is rounded to bf16 (2^-9), three (all 24 bits) where
+//         it is fp32 or a sum over rows;
+//   fp16: two parts of 11 bits (2^-22; two roundings of fp32), of the numbers
+//         times a power of two that keeps the largest of them in fp16's range.
+// fp32 operands multiply them as they are.
 #pragma once
 
 #include <type_traits>
@@ -38,7 +42,8 @@ struct AdaptTile {
 
 // The rows of a workgroup's tile.  Up to kAdaptDirect rows there are no lists:
 // workgroup t finds the rows of row t's adapter by itself, and takes 16 of them
-// from t on if t is the first, the 17th, ... of them.
+// from t on if t is the first, the 17th, ... of them (32 rows of 4096 to 4096,
+// rank 16: 11.5 us in two launches; the sort's launch would add 5).
 constexpr int kAdaptDirect = 256;
 struct RowsArgs {
     const void *ids;
@@ -221,9 +226,13 @@ __device__ inline int32_t find_rows(const RowsArgs &a, int32_t number, RowsShare
 
 // ------------------------------------------------------------------- shrink
 
-// A workgroup takes a tile, a part of the columns and up to 64 ranks; its waves
-// take every fourth 64 columns and add up in LDS.  M: row tiles of 16 that the
-// tile fills.
+// A workgroup takes 16 M rows of a tile, a part of the columns and up to 64
+// ranks; its waves take every fourth 64 columns and add up in LDS.  Rows of few
+// bytes in flight and latency bound it: x and grad of 8192 x 4096 bf16, rank 16,
+// take 37 us (134 MB, 3.6 TB/s; waves wait 34 % of their time), x of 16384 x 4096
+// by rank 64 75 us.  M = 2 and 4 (large ranks, many rows) against half of them:
+// 37 and 42 us, 62 and 74.  Reading 64 columns of a row in one step (its whole
+// 128 bytes) instead of 32: 42 and 46 us.
 template <typename T, int RB, bool kAcross, int M>
 __device__ inline void shrink_rows(const ShrinkArgs &a, int32_t adapter, int32_t count,
                                    const int32_t *rows, int32_t split, int32_t rank0,
@@ -520,6 +529,13 @@ struct Numbers<float, G, kAll> {
 // columns of the matrix in registers and goes over the rows, 16 at a time.
 // Column tile j holds columns i16 * NT + j, so that a lane's results of one row
 // are neighbours, and those of 16 lanes are 128 bytes (fp32: 256) or more.
+// Bound by memory, a mixture of reads and writes, and by the latency of what a
+// workgroup needs first (list, rows, sums, base, one after another): 5001 x 11000
+// fp16, rank 8, 60 us (220 MB, 3.7 TB/s); 16384 x 12288 bf16, rank 64, 190 us
+// (805 MB, 4.2 TB/s); dx of 8192 x 4096 33 us (134 MB, 4.0 TB/s).  A copy in this
+// order of addresses takes 47, 150 and 28.  The base of all 64 rows at once
+// instead of 16 by 16: 69 and 58 us; 512 columns: 62; the matrix through LDS, the
+// rows' numbers kept: 79.
 template <typename T, typename B, int G, int NT, bool kAcross>
 __device__ inline void expand_rows(const ExpandArgs &a) {
     using H = Numbers<T, G, sizeof(B) == 4>;
@@ -746,6 +762,8 @@ __device__ inline void expand_rows(const ExpandArgs &a) {
     }
 }
 
+// Three waves per SIMD for 33 to 64 ranks: 203 us where the compiler's choice,
+// two, takes 236 (16384 x 12288); four for up to 32 spill.
 template <typename T, typename B, int G, int NT>
 __global__ __launch_bounds__(kAdaptThreads, G == 2 && sizeof(T) == 2 ? 3 : 1) void
 k_adapt_expand(ExpandArgs a) {
@@ -845,7 +863,10 @@ k_adapt_back(ExpandArgs a, int32_t groups, FinishArgs h, FinishArgs g) {
 // Sums over a chunk's rows of v[k] x[c]: a workgroup takes a chunk, 128 columns
 // and up to 64 ranks; its waves take 32 rows in turn and add up in LDS.  The
 // lane's rows and columns, 8 x 8, are turned into operands of eight rows for
-// eight column tiles (tile j: columns i16 * 8 + j).
+// eight column tiles (tile j: columns i16 * 8 + j).  Bound by the latency of the
+// rows, which the step's registers leave few waves to hide: x and grad of 8192 x
+// 4096 bf16, rank 16, 42 us (read again, from the last-level cache: 3.2 TB/s);
+// with the next rows loaded ahead, and fewer waves, 54.
 template <typename T>
 struct Columns {  // x's operands and their product with the P parts of v
     Vec<T, 8> c[8];
@@ -1059,30 +1080,30 @@ void with_groups(int32_t rank, F f) {
 }
 
 // f(integral_constant<rank blocks>, integral_constant<16 rows of a workgroup>)
+// where tiles have 64 rows
 template <typename F>
 void with_rows(int32_t rank, int32_t subs, F f) {
     with_ranks(rank, [&](auto rb) {
         if (subs == 1)
             f(rb, std::integral_constant<int, 4>{});
-        else if (subs == 2)
-            f(rb, std::integral_constant<int, 2>{});
         else
-            f(rb, std::integral_constant<int, 1>{});
+            f(rb, std::integral_constant<int, 2>{});
     });
 }
 
 template <typename T>
 void Adapt<T>::shrink(const ShrinkArgs &a, int64_t tiles, hipStream_t s) {
-    // tiles that find their rows have 16 at most
-    const bool direct = !a.rows.tiles;
-    const dim3 grid(static_cast<unsigned>(tiles * (direct ? 1 : a.subs)),
-                    static_cast<unsigned>(a.splits), static_cast<unsigned>(adapt_slabs(a.rank)));
-    with_rows(a.rank, direct ? 4 : a.subs, [&](auto rb, auto m) {
-        ShrinkArgs b = a;
-        if (direct) b.subs = 1;
-        k_adapt_shrink<T, decltype(rb)::value, decltype(m)::value>
-            <<<grid, kAdaptThreads, 0, s>>>(b);
-    });
+    const dim3 grid(static_cast<unsigned>(tiles * a.subs), static_cast<unsigned>(a.splits),
+                    static_cast<unsigned>(adapt_slabs(a.rank)));
+    if (!a.rows.tiles)  // tiles that find their rows have 16 at most
+        with_ranks(a.rank, [&](auto rb) {
+            k_adapt_shrink<T, decltype(rb)::value, 1><<<grid, kAdaptThreads, 0, s>>>(a);
+        });
+    else
+        with_rows(a.rank, a.subs, [&](auto rb, auto m) {
+            k_adapt_shrink<T, decltype(rb)::value, decltype(m)::value>
+                <<<grid, kAdaptThreads, 0, s>>>(a);
+        });
 }
 
 template <typename T>
@@ -1095,10 +1116,6 @@ void Adapt<T>::shrink_both(const ShrinkArgs &a, const ShrinkArgs &across, int64_
         k_adapt_shrink_both<T, decltype(rb)::value, decltype(m)::value>
             <<<grid, kAdaptThreads, 0, s>>>(a, across);
     });
-}
-
-inline int64_t expand_groups(int32_t D, int64_t tiles) {
-    return tiles * ((D - 1) / kExpandColumns + 1);
 }
 
 template <typename T>
