@@ -194,3 +194,22 @@ def test_adapt_rejects_host_tensors():
                  lambda: spmv.adapt_grad(torch.zeros(3, 6), x, down, up, ids)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_committed_profile_matches_the_kernel_sources():
+    """The kernel times and counters of profiles/requests_kernel_trace.md were taken on the
+    committed code: the hash that it carries is that of the sources that these kernels are
+    compiled from, comments and whitespace removed."""
+    import hashlib
+    import os
+    import re
+    package = os.path.dirname(spmv.__file__)
+    h = hashlib.sha256()
+    for f in ("internal.h", "tables.h", "requests.h", "adapt.h", "adapt.hip", "adapt_bf16.hip",
+              "adapt_fp16.hip", "adapt_fp32.hip", "logprobs.hip"):
+        text = open(os.path.join(package, "csrc", f), encoding="utf-8").read()
+        text = re.sub(r"//[^\n]*", " ", re.sub(r"/\*.*?\*/", " ", text, flags=re.S))
+        h.update(" ".join(text.split()).encode())
+    profile = open(os.path.join(package, "..", "profiles", "requests_kernel_trace.md"),
+                   encoding="utf-8").read()
+    assert f"kernel_source_sha: {h.hexdigest()[:16]}" in profile
