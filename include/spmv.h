@@ -690,8 +690,9 @@ spmv_status spmv_token_logprobs_grad(int32_t num_cols, int64_t n, const void *lo
  * adapter ids[t]; rows whose id is outside [0, num_adapters) use none.  Rows of one
  * adapter need not lie together.
  *   1 <= rank <= 256; at most 2048 adapters, 2^24 rows, 2^21 columns, and
- *   n / 64 + min(num_adapters + 1, n) tiles of rows times columns / 256 (each rounded
- *   up) at most 2^23; else SPMV_ERR_TOO_LARGE.  Smaller ranks are stored with zeros.
+ *   n / 64 + min(num_adapters + 1, n) tiles of rows times columns / 256 + 32 (both
+ *   rounded up) below 2^24; else SPMV_ERR_TOO_LARGE.  Smaller ranks are stored with
+ *   zeros.
  *   Numbers between two products (down[a] x[t], up[a]^T grad[t]) are kept in fp32 and
  *   enter the next one with all their bits, but with 16 of them where x's type and the
  *   result's are bf16 (a result of 8 bits), and with 22 where x's type is fp16 (fewer

@@ -1118,6 +1118,10 @@ void Adapt<T>::shrink_both(const ShrinkArgs &a, const ShrinkArgs &across, int64_
     });
 }
 
+inline int64_t expand_groups(int32_t D, int64_t tiles) {
+    return tiles * ((D - 1) / kExpandColumns + 1);
+}
+
 template <typename T>
 void Adapt<T>::expand(const ExpandArgs &a, bool out_fp32, int64_t tiles, hipStream_t s) {
     const unsigned grid = static_cast<unsigned>(expand_groups(a.D, tiles));

@@ -85,7 +85,7 @@ constexpr int32_t kMostRank = 256;
 constexpr int32_t kMostAdapters = 2048;
 constexpr int32_t kMostColumns = 1 << 21;
 constexpr int32_t kMostAdaptRows = 1 << 24;
-constexpr int64_t kMostAdaptGroups = 1 << 23;
+constexpr int64_t kMostAdaptGroups = 1 << 24;
 
 struct AdaptArgs {
     int32_t n, adapters, rank, C, R;  // rows, adapters, their rank, columns of x and of out

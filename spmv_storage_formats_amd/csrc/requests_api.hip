@@ -16,9 +16,10 @@ spmv_status adapt_sizes(int32_t adapters, int32_t rank, int32_t C, int32_t R, in
     if (adapters > kMostAdapters || rank > kMostRank || C > kMostColumns || R > kMostColumns ||
         n > kMostAdaptRows)
         return SPMV_ERR_TOO_LARGE;
-    // workgroups of one launch: tiles of 64 rows, one more of each adapter, by 256 columns
+    // workgroups of one launch: tiles of 64 rows, one more of each adapter, by 256 columns,
+    // and up to 32 for what the matrices' gradients read
     const int64_t tiles = (n + 63) / 64 + std::min<int64_t>(adapters + 1, n);
-    if (tiles * ((std::max(C, R) + 255) / 256) > kMostAdaptGroups) return SPMV_ERR_TOO_LARGE;
+    if (tiles * ((std::max(C, R) + 255) / 256 + 32) >= kMostAdaptGroups) return SPMV_ERR_TOO_LARGE;
     return SPMV_OK;
 }
 
