@@ -531,8 +531,8 @@ struct Numbers<float, G, kAll> {
 // are neighbours, and those of 16 lanes are 128 bytes (fp32: 256) or more.
 // Bound by memory, a mixture of reads and writes, and by the latency of what a
 // workgroup needs first (list, rows, sums, base, one after another): 5001 x 11000
-// fp16, rank 8, 60 us (220 MB, 3.7 TB/s); 16384 x 12288 bf16, rank 64, 190 us
-// (805 MB, 4.2 TB/s); dx of 8192 x 4096 33 us (134 MB, 4.0 TB/s).  A copy in this
+// fp16, rank 8, 60 us (220 MB, 3.7 TB/s); 16384 x 12288 bf16, rank 64, 182 us
+// (805 MB, 4.4 TB/s); dx of 8192 x 4096 35 us (134 MB, 3.8 TB/s).  A copy in this
 // order of addresses takes 47, 150 and 28.  The base of all 64 rows at once
 // instead of 16 by 16: 69 and 58 us; 512 columns: 62; the matrix through LDS, the
 // rows' numbers kept: 79.
