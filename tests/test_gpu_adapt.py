@@ -333,6 +333,20 @@ def test_empty_and_none(dev):
         assert (dd[1] == 0).all() and (du[1] == 0).all() and (dx == 21).all()
 
 
+@pytest.mark.parametrize("n", [40, 900])
+def test_no_row_names_an_adapter(dev, n):
+    """A padded batch throughout: the base is handed on, gradients of the matrices are zeros."""
+    c = Case(n, 3, 8, 70, 90, "bf16", 5, pad=2.0).to(dev)
+    assert ((c.ids < 0) | (c.ids >= 3)).all()
+    base = c.base.to(torch.bfloat16)
+    assert torch.equal(spmv.adapt(c.x, c.down, c.up, c.ids, base), base)
+    assert (spmv.adapt(c.x, c.down, c.up, c.ids) == 0).all()
+    keep = base.clone()
+    assert torch.equal(spmv.adapt(c.x, c.down, c.up, c.ids, keep, keep), base)
+    dx, dd, du = spmv.adapt_grad(c.grad, c.x, c.down, c.up, c.ids, c.back)
+    assert torch.equal(dx, c.back) and (dd == 0).all() and (du == 0).all()
+
+
 def test_gradients_are_differences(dev):
     """L = sum(r * adapt(x, down, up)) is linear in each operand: with whole numbers a step of 1
     in one element changes L by exactly its gradient."""
